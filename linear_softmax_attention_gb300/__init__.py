@@ -20,6 +20,8 @@ __all__ = [
     "causal_state", "causal_output", "status_string", "ENTRY_POINTS", "fwd_bidir_static", "static_scratch_bytes",
     "new_decode_state", "decode_step", "decode_prefill", "decode_prefill_workspace_bytes", "FEATURE_MAPS",
     "bwd_bidir", "bwd_causal", "bwd_workspace_bytes", "selftest_wait_timeout",
+    "fwd_gated_scan", "bwd_gated_scan", "gated_scan_step", "new_gated_scan_state", "fwd_layer_norm",
+    "bwd_layer_norm", "bwd_layer_norm_workspace_bytes", "fwd_rotary", "bwd_rotary", "new_rotary_table",
 ]
 
 F32 = 0
@@ -95,6 +97,7 @@ def load():
                                          c_vp, c_size, c_vp, c_vp]
     lib.favor_decode_prefill_workspace_bytes.restype = c_size
     lib.favor_decode_prefill_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int]
+    sequence.declare(lib)
     _lib = lib
     return lib
 
@@ -354,3 +357,9 @@ def bwd_causal(Q, K, V, dO, omega, qk_scale, workspace=None, feature_map="prf", 
     """Gradients (dQ, dK, dV) of the causal pass."""
     return bwd_bidir(Q, K, V, dO, omega, qk_scale, workspace, feature_map, dQ, dK, dV, dev_status, stream,
                      causal=True)
+
+
+from . import sequence                                                   # noqa: E402  (uses load and FavorError)
+from .sequence import (bwd_gated_scan, bwd_layer_norm, bwd_layer_norm_workspace_bytes, bwd_rotary,  # noqa: E402
+                       fwd_gated_scan, fwd_layer_norm, fwd_rotary, gated_scan_step, new_gated_scan_state,
+                       new_rotary_table)

@@ -68,7 +68,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     _check_arch_stamp()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(INCLUDE, "favor.h"))
+    headers += [os.path.join(INCLUDE, f) for f in ("favor.h", "favor_ops.h")]
     flags = CFLAGS + list(extra_flags or [])
     jobs = []
     objs = []
