@@ -49,14 +49,16 @@ extern "C" {
  * leaves hT at its last token.
  * h0: fp32 [B, H, d] contiguous, NULL for zeros.  hT: the same, NULL if not
  * wanted; hT may be h0.  h may be x or g.  h is rounded to dt once, the
- * state is carried in fp32.
- * Supported: B H d < 2^31.
+ * state is carried in fp32.  dev_status: a bounded wait of a cluster's CTAs
+ * on one another that ran out is reported there (FAVOR_ERR_TIMEOUT).
+ * Supported: B H d < 2^31, L <= 2^30, token strides below 2^31.
  */
 favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides,
                                   const void* g, const int64_t* g_strides,
                                   void* h, const int64_t* h_strides,
                                   const float* h0, float* hT,
-                                  int B, int H, int L, int d, favor_dtype dt, void* stream);
+                                  int B, int H, int L, int d, favor_dtype dt,
+                                  int32_t* dev_status, void* stream);
 
 /*
  * favor_bwd_gated_scan — its gradients, for dh = dL/dh and dhT = dL/dhT
@@ -74,7 +76,8 @@ favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides,
                                   void* dx, const int64_t* dx_strides,
                                   void* dg, const int64_t* dg_strides,
                                   const float* h0, const float* dhT, float* dh0,
-                                  int B, int H, int L, int d, favor_dtype dt, void* stream);
+                                  int B, int H, int L, int d, favor_dtype dt,
+                                  int32_t* dev_status, void* stream);
 
 /*
  * favor_gated_scan_step — one token: x, g and h contiguous [B, H, d],

@@ -58,6 +58,34 @@ struct FastDiv {
   __device__ __forceinline__ uint32_t div(uint32_t n) const { return static_cast<uint32_t>((n * m) >> shift); }
 };
 
+// ---- rows -------------------------------------------------------------------
+// Offsets of the rows (b, h, t), t fastest, of up to three tensors.  Axes that
+// every tensor walks with one stride are merged, so that contiguous tensors
+// need no division.
+struct Rows {
+  FastDiv l, h;          // extents of the inner two axes; 1: merged away or single
+  Strides s[3];
+  // row -> (b, h, t)
+  __device__ __forceinline__ void split(uint32_t row, uint32_t* b, uint32_t* hh, uint32_t* t) const {
+    uint32_t r = row;
+    *t = 0;
+    *hh = 0;
+    if (l.d > 1) {
+      r = l.div(row);
+      *t = row - r * l.d;
+    }
+    *b = r;
+    if (h.d > 1) {
+      *b = h.div(r);
+      *hh = r - *b * h.d;
+    }
+  }
+  __device__ __forceinline__ int64_t offset(int i, uint32_t b, uint32_t hh, uint32_t t) const {
+    return b * s[i].b + hh * s[i].h + t * s[i].l;
+  }
+};
+Rows make_rows(int B, int H, int L, const Strides* s, int n);
+
 // ---- launchers ------------------------------------------------------------------
 struct ScanArgs {
   const void *x, *g, *h_in, *dh;      // forward: x, g; backward: g, h_in, dh
@@ -66,9 +94,11 @@ struct ScanArgs {
   const float* first;                 // h0 (forward), dhT (backward): the carry at the start, or NULL
   const float* h0;                    // backward: h_{-1}, or NULL
   float* last;                        // hT (forward), dh0 (backward), or NULL
+  int32_t* status;
   int B, H, L, d;
 };
-cudaError_t launch_scan(const ScanArgs& a, bool backward, bool bf16, bool pairs, cudaStream_t stream);
+// align: pieces of this many bytes (16, 4 or 2) make up every row of every tensor
+cudaError_t launch_scan(const ScanArgs& a, bool backward, bool bf16, int align, cudaStream_t stream);
 cudaError_t launch_scan_step(const void* x, const void* g, void* h, const float* state, float* new_state, int64_t n,
                              bool bf16, cudaStream_t stream);
 

@@ -1,6 +1,7 @@
 // C ABI entry points of the sequence operators: argument checks and dispatch.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "ops.cuh"
 
@@ -107,6 +108,42 @@ bool overlap(const View& a, const View& b) {
   return hits(x, y, order, k, bytes / a.esz);
 }
 
+Rows make_rows(int B, int H, int L, const Strides* s, int n) {
+  Rows r{};
+  for (int i = 0; i < n; ++i) r.s[i] = s[i];
+  // (b, h, t) -> rows of one axis: first t into h, then h into b
+  bool t_in_h = true, h_in_b = true;
+  for (int i = 0; i < n; ++i) t_in_h = t_in_h && (H == 1 || L == 1 || s[i].h == L * s[i].l);
+  int h_ext = H, l_ext = L;
+  if (t_in_h) {
+    // one axis of H L rows, kept as h
+    for (int i = 0; i < n; ++i)
+      if (L > 1) r.s[i].h = s[i].l;
+    const int64_t hl = (int64_t)H * L;
+    l_ext = 1;
+    for (int i = 0; i < n; ++i) h_in_b = h_in_b && (B == 1 || hl == 1 || s[i].b == hl * r.s[i].h);
+    h_ext = (int)hl;
+  } else {
+    for (int i = 0; i < n; ++i) h_in_b = h_in_b && B == 1;
+    if (B == 1) {
+      // (h, t) only: h is what remains of the division by L
+      for (int i = 0; i < n; ++i) r.s[i].b = s[i].h;
+      r.l = FastDiv((uint32_t)L);
+      r.h = FastDiv(1);
+      return r;
+    }
+    h_in_b = false;
+  }
+  if (h_in_b) {
+    for (int i = 0; i < n; ++i)
+      if (h_ext > 1) r.s[i].b = r.s[i].h;
+    h_ext = 1;
+  }
+  r.l = FastDiv((uint32_t)l_ext);
+  r.h = FastDiv((uint32_t)h_ext);
+  return r;
+}
+
 }  // namespace favor
 
 namespace {
@@ -137,6 +174,20 @@ bool clash(const float* out, int64_t n, const float* p, int64_t np, bool in_plac
   return favor::overlap(favor::flat_view(out, n, 4), favor::flat_view(p, np, 4));
 }
 
+// 32-bit token strides and positions of the scan kernels
+bool scan_fits(std::initializer_list<const View*> views) {
+  for (const View* v : views)
+    if (v->n[2] > (1 << 30) || v->s[2] >= (int64_t(1) << 31)) return false;
+  return true;
+}
+
+// the largest of 16, 4 and 2 bytes that all the views' rows are made of
+int common_piece(std::initializer_list<const View*> views) {
+  int piece = 16;
+  for (const View* v : views) piece = v->pieces(piece) ? piece : piece >= 4 && v->pieces(4) ? 4 : 2;
+  return piece;
+}
+
 favor_status done(cudaError_t e) { return e == cudaSuccess ? FAVOR_OK : FAVOR_ERR_CUDA; }
 
 bool positive(float x) { return std::isfinite(x) && x > 0.f; }
@@ -164,7 +215,7 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   if (pairs < 1 || 2 * pairs > d) return FAVOR_ERR_INVALID_ARG;
   const int64_t lim = int64_t(1) << 31;
   if (d > favor::kNormMaxD || (int64_t)B * Hq >= lim || (int64_t)B * Hq * L >= lim) return FAVOR_ERR_UNSUPPORTED;
-  if (keys && ((int64_t)B * Hk >= lim || (int64_t)B * Hk * L >= lim)) return FAVOR_ERR_UNSUPPORTED;
+  if (keys && ((int64_t)Hq + Hk >= lim || (int64_t)B * Hk >= lim || (int64_t)B * Hk * L >= lim)) return FAVOR_ERR_UNSUPPORTED;
   const int e = elem(dt);
   View vq, vqo, vk{}, vko{};
   if (!favor::make_view(&vq, q, qs, B, Hq, L, d, e) || !favor::make_view(&vqo, qo, qos, B, Hq, L, d, e))
@@ -212,7 +263,7 @@ extern "C" {
 
 favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides, const void* g, const int64_t* g_strides,
                                   void* h, const int64_t* h_strides, const float* h0, float* hT, int B, int H, int L,
-                                  int d, favor_dtype dt, void* stream) {
+                                  int d, favor_dtype dt, int32_t* dev_status, void* stream) {
   const favor_status st = sizes_ok(B, H, L, d, dt);
   if (st != FAVOR_OK) return st;
   if (!flat_ok(h0) || !flat_ok(hT)) return FAVOR_ERR_INVALID_ARG;
@@ -223,6 +274,7 @@ favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides, const
       !favor::make_view(&vh, h, h_strides, B, H, L, d, e))
     return FAVOR_ERR_INVALID_ARG;
   const int64_t n = (int64_t)B * H * d;
+  if (!scan_fits({&vx, &vg, &vh})) return FAVOR_ERR_UNSUPPORTED;
   if (favor::self_overlap(vh) || clash(vh, vx, true) || clash(vh, vg, true) || clash(vh, h0, n) || clash(vh, hT, n) ||
       clash(vx, hT, n) || clash(vg, hT, n) || clash(hT, n, h0, n, true))
     return FAVOR_ERR_INVALID_ARG;
@@ -233,20 +285,21 @@ favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides, const
   a.xs = vx.strides();
   a.gs = vg.strides();
   a.hs = vh.strides();
+  a.status = dev_status;
   a.first = h0;
   a.last = hT;
   a.B = B;
   a.H = H;
   a.L = L;
   a.d = d;
-  const bool pairs = vx.pieces(2 * e) && vg.pieces(2 * e) && vh.pieces(2 * e);
-  return done(favor::launch_scan(a, false, dt == FAVOR_BF16, pairs, static_cast<cudaStream_t>(stream)));
+  return done(favor::launch_scan(a, false, dt == FAVOR_BF16, common_piece({&vx, &vg, &vh}),
+                                 static_cast<cudaStream_t>(stream)));
 }
 
 favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides, const void* h, const int64_t* h_strides,
                                   const void* dh, const int64_t* dh_strides, void* dx, const int64_t* dx_strides,
                                   void* dg, const int64_t* dg_strides, const float* h0, const float* dhT, float* dh0,
-                                  int B, int H, int L, int d, favor_dtype dt, void* stream) {
+                                  int B, int H, int L, int d, favor_dtype dt, int32_t* dev_status, void* stream) {
   const favor_status st = sizes_ok(B, H, L, d, dt);
   if (st != FAVOR_OK) return st;
   if (!flat_ok(h0) || !flat_ok(dhT) || !flat_ok(dh0)) return FAVOR_ERR_INVALID_ARG;
@@ -258,6 +311,7 @@ favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides, const
       !favor::make_view(&vdx, dx, dx_strides, B, H, L, d, e) || !favor::make_view(&vdg, dg, dg_strides, B, H, L, d, e))
     return FAVOR_ERR_INVALID_ARG;
   const int64_t n = (int64_t)B * H * d;
+  if (!scan_fits({&vg, &vh, &vdh, &vdx, &vdg})) return FAVOR_ERR_UNSUPPORTED;
   if (favor::self_overlap(vdx) || favor::self_overlap(vdg) || clash(vdx, vdg, false) || clash(vdx, vg, false) ||
       clash(vdx, vh, false) || clash(vdx, vdh, true) || clash(vdg, vg, true) || clash(vdg, vh, false) ||
       clash(vdg, vdh, false))
@@ -278,6 +332,7 @@ favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides, const
   a.dhs = vdh.strides();
   a.dxs = vdx.strides();
   a.dgs = vdg.strides();
+  a.status = dev_status;
   a.first = dhT;
   a.h0 = h0;
   a.last = dh0;
@@ -285,9 +340,8 @@ favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides, const
   a.H = H;
   a.L = L;
   a.d = d;
-  bool pairs = true;
-  for (const View* v : {&vg, &vh, &vdh, &vdx, &vdg}) pairs = pairs && v->pieces(2 * e);
-  return done(favor::launch_scan(a, true, dt == FAVOR_BF16, pairs, static_cast<cudaStream_t>(stream)));
+  return done(favor::launch_scan(a, true, dt == FAVOR_BF16, common_piece({&vg, &vh, &vdh, &vdx, &vdg}),
+                                 static_cast<cudaStream_t>(stream)));
 }
 
 favor_status favor_gated_scan_step(const void* x, const void* g, void* h, const float* state, float* new_state, int B,

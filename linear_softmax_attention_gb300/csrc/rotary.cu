@@ -1,10 +1,19 @@
 // Rotation of queries and keys by positions on one to four axes.
+//
+// Bound by memory: every channel is read and written once.  A thread takes one
+// 16-byte piece of a token's channels (two where the pairs are halves apart)
+// in every head of its share: the sines and cosines of the token are formed
+// once and used for all of them, and the heads' loads are in flight together.
+// The heads are shared out over more threads only where the tokens are few.
+#include <algorithm>
+
 #include "ops.cuh"
 
 namespace favor {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;             // heads of a thread whose loads are in flight together
 
 // The angle of a pair, in half turns: the position times the pair's fraction
 // of a turn per unit, in 64-bit fixed point, wraps to the exact fraction of a
@@ -15,60 +24,235 @@ __device__ __forceinline__ float half_turns(int32_t pos, uint64_t per_unit) {
 }
 
 struct Axes {
-  int end[FAVOR_ROTARY_MAX_AXES];   // pairs of the axes up to and with each
+  int end[FAVOR_ROTARY_MAX_AXES];     // pairs of the axes up to and with each
 };
 
-// one thread per pair (or channel behind the last pair) of a row
-template <typename T>
-__global__ void rotary_kernel(const T* in, T* out, Strides is, Strides os, const int32_t* pos, int pos_B,
-                              const uint64_t* table, Axes ax, int H, int L, int d, int P, int halves, float sign,
-                              int64_t total) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= total) return;
-  const int items = d - P;          // P pairs and d - 2 P channels
-  const int64_t row = i / items;
-  const int p = (int)(i - row * items);
-  const int64_t bh = row / L, t = row - bh * L, b = bh / H, h = bh - b * H;
-  in += b * is.b + h * is.h + t * is.l;
-  out += b * os.b + h * os.h + t * os.l;
-  if (p >= P) {
-    out[p + P] = in[p + P];
-    return;
+struct Shared {                       // what q's and k's heads have in common
+  Strides is, os;
+  const void* in;
+  void* out;
+};
+
+template <typename T> struct Piece;
+template <> struct Piece<float> {
+  using Raw = float4;
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = r.x;
+    f[1] = r.y;
+    f[2] = r.z;
+    f[3] = r.w;
   }
-  int a = 0;
-  while (p >= ax.end[a]) ++a;
-  const int32_t at = pos[((int64_t)a * pos_B + (pos_B > 1 ? b : 0)) * L + t];
-  float s, c;
-  sincospif(half_turns(at, table[p]), &s, &c);
-  s *= sign;
-  const int iu = halves ? p : 2 * p, iv = halves ? p + P : 2 * p + 1;
-  const float u = to_f32(in[iu]), v = to_f32(in[iv]);
-  out[iu] = from_f32<T>(u * c - v * s);
-  out[iv] = from_f32<T>(u * s + v * c);
+  static __device__ __forceinline__ Raw pack(const float* f) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <> struct Piece<__nv_bfloat16> {
+  using Raw = uint4;
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) {
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const unsigned*>(&v);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+struct Work {
+  Shared q, k;
+  const int32_t* pos;
+  const uint64_t* table;
+  Axes ax;
+  FastDiv l, items;                   // tokens of a row; pieces (pairs of pieces) of a token
+  int tokens, per_cta, pos_B, n_axes, L, P, d, Hq, heads, share;
+  float sign;
+};
+
+// positions of a token on each axis
+__device__ __forceinline__ void token_positions(const Work& w, int b, int t, int32_t (&at)[FAVOR_ROTARY_MAX_AXES]) {
+#pragma unroll
+  for (int a = 0; a < FAVOR_ROTARY_MAX_AXES; ++a)
+    at[a] = a < w.n_axes ? w.pos[((int64_t)a * w.pos_B + (w.pos_B > 1 ? b : 0)) * w.L + t] : 0;
+}
+__device__ __forceinline__ int32_t on_axis(const Axes& ax, const int32_t (&at)[FAVOR_ROTARY_MAX_AXES], int p) {
+  int32_t r = at[0];
+#pragma unroll
+  for (int a = 1; a < FAVOR_ROTARY_MAX_AXES; ++a) r = p >= ax.end[a - 1] ? at[a] : r;
+  return r;
 }
 
+template <typename T, bool HALVES>
+__global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
+  using P = Piece<T>;
+  using Raw = typename P::Raw;
+  constexpr int E = P::E, N = HALVES ? E : E / 2;      // pairs of a thread
+  const int items = w.items.d;
+  const int within = items <= kThreads ? w.items.div(threadIdx.x) : 0;
+  const int64_t token = (int64_t)blockIdx.x * w.per_cta + within;
+  if (within >= w.per_cta || token >= w.tokens) return;
+  const int b = (int)w.l.div((uint32_t)token), t = (int)token - b * w.L;
+  const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
+  int32_t at[FAVOR_ROTARY_MAX_AXES];
+  token_positions(w, b, t, at);
+  for (int item = threadIdx.x - within * items; item < items; item += kThreads) {
+    const int turning = HALVES ? w.P / E : 2 * w.P / E;
+    const bool turns = item < turning;
+    // first channel of the piece, and of the second half's
+    const int c0 = HALVES && !turns ? 2 * w.P + (item - turning) * E : item * E, c1 = c0 + w.P;
+    float cs[N], sn[N];
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int p = HALVES ? c0 + i : c0 / 2 + i;
+        sincospif(half_turns(on_axis(w.ax, at, p), w.table[p]), &sn[i], &cs[i]);
+        sn[i] *= w.sign;
+      }
+    }
+    for (int hb = h0; hb < h1; hb += kHeads) {
+      Raw r0[kHeads], r1[kHeads];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int hh = hb + i;
+        if (hh < h1) {
+          const Shared& s = hh < w.Hq ? w.q : w.k;
+          const T* in = static_cast<const T*>(s.in) + b * s.is.b + (hh < w.Hq ? hh : hh - w.Hq) * s.is.h + t * s.is.l;
+          r0[i] = *reinterpret_cast<const Raw*>(in + c0);
+          if (HALVES && turns) r1[i] = *reinterpret_cast<const Raw*>(in + c1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int hh = hb + i;
+        if (hh < h1) {
+          const Shared& s = hh < w.Hq ? w.q : w.k;
+          T* out = static_cast<T*>(s.out) + b * s.os.b + (hh < w.Hq ? hh : hh - w.Hq) * s.os.h + t * s.os.l;
+          if (turns) {
+            float u[E], v[E], a[E], c[E];
+            P::unpack(r0[i], u);
+            if constexpr (HALVES) {
+              P::unpack(r1[i], v);
+#pragma unroll
+              for (int j = 0; j < E; ++j) {
+                a[j] = u[j] * cs[j] - v[j] * sn[j];
+                c[j] = u[j] * sn[j] + v[j] * cs[j];
+              }
+              *reinterpret_cast<Raw*>(out + c1) = P::pack(c);
+            } else {
+#pragma unroll
+              for (int j = 0; j < N; ++j) {
+                a[2 * j] = u[2 * j] * cs[j] - u[2 * j + 1] * sn[j];
+                a[2 * j + 1] = u[2 * j] * sn[j] + u[2 * j + 1] * cs[j];
+              }
+            }
+            *reinterpret_cast<Raw*>(out + c0) = P::pack(a);
+          } else {
+            *reinterpret_cast<Raw*>(out + c0) = r0[i];
+          }
+        }
+      }
+    }
+  }
+}
+
+// Any strides and sizes: a thread per pair, or channel behind the pairs
 template <typename T>
-void go(const RotaryArgs& a, const Axes& ax, const void* in, void* out, const Strides& is, const Strides& os, int H,
-        cudaStream_t stream) {
-  const int64_t total = (int64_t)a.B * H * a.L * (a.d - a.pairs);
-  rotary_kernel<T><<<(unsigned)((total + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
-      static_cast<const T*>(in), static_cast<T*>(out), is, os, a.pos, a.pos_B, a.table, ax, H, a.L, a.d, a.pairs,
-      a.halves ? 1 : 0, a.inverse ? -1.f : 1.f, total);
+__global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool halves) {
+  const int items = w.items.d;
+  const int within = items <= kThreads ? w.items.div(threadIdx.x) : 0;
+  const int64_t token = (int64_t)blockIdx.x * w.per_cta + within;
+  if (within >= w.per_cta || token >= w.tokens) return;
+  const int b = (int)w.l.div((uint32_t)token), t = (int)token - b * w.L;
+  const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
+  int32_t at[FAVOR_ROTARY_MAX_AXES];
+  token_positions(w, b, t, at);
+  for (int p = threadIdx.x - within * items; p < items; p += kThreads) {
+    const bool turns = p < w.P;
+    const int iu = !turns ? p + w.P : halves ? p : 2 * p, iv = !turns ? iu : halves ? p + w.P : 2 * p + 1;
+    float cs = 1.f, sn = 0.f;
+    if (turns) {
+      sincospif(half_turns(on_axis(w.ax, at, p), w.table[p]), &sn, &cs);
+      sn *= w.sign;
+    }
+    for (int hb = h0; hb < h1; hb += kHeads) {
+      T u[kHeads], v[kHeads];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int hh = hb + i;
+        if (hh < h1) {
+          const Shared& s = hh < w.Hq ? w.q : w.k;
+          const T* in = static_cast<const T*>(s.in) + b * s.is.b + (hh < w.Hq ? hh : hh - w.Hq) * s.is.h + t * s.is.l;
+          u[i] = in[iu];
+          v[i] = in[iv];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int hh = hb + i;
+        if (hh < h1) {
+          const Shared& s = hh < w.Hq ? w.q : w.k;
+          T* out = static_cast<T*>(s.out) + b * s.os.b + (hh < w.Hq ? hh : hh - w.Hq) * s.os.h + t * s.os.l;
+          if (turns) {
+            const float x = to_f32(u[i]), y = to_f32(v[i]);
+            out[iu] = from_f32<T>(x * cs - y * sn);
+            out[iv] = from_f32<T>(x * sn + y * cs);
+          } else {
+            out[iu] = u[i];
+          }
+        }
+      }
+    }
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, bool vec, cudaStream_t stream) {
-  (void)vec;
-  Axes ax;
+  Work w{};
+  w.q = Shared{a.qs, a.qos, a.q, a.qo};
+  w.k = Shared{a.ks, a.kos, a.k, a.ko};
+  w.pos = a.pos;
+  w.table = a.table;
   int end = 0;
-  for (int i = 0; i < FAVOR_ROTARY_MAX_AXES; ++i) ax.end[i] = end += i < a.n_axes ? a.sections[i] : 0;
-  if (bf16) {
-    go<__nv_bfloat16>(a, ax, a.q, a.qo, a.qs, a.qos, a.Hq, stream);
-    if (a.Hk > 0) go<__nv_bfloat16>(a, ax, a.k, a.ko, a.ks, a.kos, a.Hk, stream);
+  for (int i = 0; i < FAVOR_ROTARY_MAX_AXES; ++i) w.ax.end[i] = end += i < a.n_axes ? a.sections[i] : 0;
+  w.l = FastDiv((uint32_t)a.L);
+  w.tokens = a.B * a.L;
+  w.pos_B = a.pos_B;
+  w.n_axes = a.n_axes;
+  w.L = a.L;
+  w.P = a.pairs;
+  w.d = a.d;
+  w.Hq = a.Hq;
+  w.heads = a.Hq + a.Hk;
+  w.sign = a.inverse ? -1.f : 1.f;
+  // whole pieces: each half of the pairs (all of them, side by side) is made of 16 bytes
+  const int E = bf16 ? 8 : 4;
+  const bool pieces = vec && (a.halves ? a.pairs % E == 0 : 2 * a.pairs % E == 0);
+  const int items = !pieces ? a.d - a.pairs : a.halves ? a.pairs / E + (a.d - 2 * a.pairs) / E : a.d / E;
+  w.items = FastDiv((uint32_t)items);
+  w.per_cta = std::max(1, kThreads / items);
+  // enough threads for every SM's 2048: fewer heads each where tokens are few
+  const int64_t threads = (int64_t)w.tokens * items, want = (int64_t)sm_count() * 2048;
+  const int64_t parts = std::min<int64_t>(std::min(w.heads, 65535), std::max<int64_t>(1, want / std::max<int64_t>(1, threads)));
+  w.share = (int)((w.heads + parts - 1) / parts);
+  const dim3 grid((unsigned)(((int64_t)w.tokens + w.per_cta - 1) / w.per_cta),
+                  (unsigned)((w.heads + w.share - 1) / w.share));
+  if (pieces) {
+    if (bf16 && a.halves) rotary_pieces_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(w);
+    else if (bf16) rotary_pieces_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(w);
+    else if (a.halves) rotary_pieces_kernel<float, true><<<grid, kThreads, 0, stream>>>(w);
+    else rotary_pieces_kernel<float, false><<<grid, kThreads, 0, stream>>>(w);
   } else {
-    go<float>(a, ax, a.q, a.qo, a.qs, a.qos, a.Hq, stream);
-    if (a.Hk > 0) go<float>(a, ax, a.k, a.ko, a.ks, a.kos, a.Hk, stream);
+    if (bf16) rotary_pairs_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(w, a.halves);
+    else rotary_pairs_kernel<float><<<grid, kThreads, 0, stream>>>(w, a.halves);
   }
   return cudaGetLastError();
 }

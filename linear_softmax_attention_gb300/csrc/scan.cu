@@ -1,91 +1,674 @@
 // Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per channel, forward,
 // backward and one token.
+//
+// A run of tokens acts on the state before it as one affine map, h -> A h + s
+// with A the product of its gates and s its own sum; two runs in sequence
+// compose to (A1 A2, A2 s1 + s2).  The backward pass is the same recurrence
+// against time: c_t = a_t c_{t+1} + a_t dh_t, dx_t = dh_t + c_{t+1},
+// dg_t = c_t h_{t-1}.
+//
+// Bound by memory: every element is read and written once.  Channels are
+// independent, but a whole GPU of them is rare, so a cluster of CTAs walks
+// 32 lanes of channels together, R tokens per warp, W worker warps and K CTAs
+// per step.  The workers copy their tokens ahead into a ring in shared memory
+// and form their runs' maps; one more warp per CTA joins the maps in a fixed
+// order, within the CTA through shared memory and across the cluster through
+// distributed shared memory, while the workers form the next step's maps; then
+// they walk their runs once more from the state before them and write.
+// Nothing is read twice and nothing is passed through global memory, so the
+// call needs no workspace and its bits do not depend on timing.
+#include <mutex>
+
 #include "ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace favor {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMaxWarps = 8;          // warps of a CTA
+constexpr int kMaxCluster = 16;       // CTAs of a cluster
+constexpr int kFold = 4;              // maps read together while they are joined
+constexpr int kRun = 8;               // tokens of a run
+constexpr int kStages = 3;            // runs of a warp in its ring
+constexpr int kStepThreads = 128;
 
-// exp(g) = 0 drops the state, whatever it is
-__device__ __forceinline__ float apply(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
-
-// one thread per channel walks the tokens
-template <typename T>
-__global__ void scan_fwd_kernel(ScanArgs p) {
-  const int64_t n = (int64_t)p.B * p.H * p.d;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n) return;
-  const int64_t bh = i / p.d, c = i - bh * p.d, b = bh / p.H, hd = bh - b * p.H;
-  const T* x = static_cast<const T*>(p.x) + b * p.xs.b + hd * p.xs.h + c;
-  const T* g = static_cast<const T*>(p.g) + b * p.gs.b + hd * p.gs.h + c;
-  T* out = static_cast<T*>(p.h) + b * p.hs.b + hd * p.hs.h + c;
-  float h = p.first != nullptr ? p.first[i] : 0.f;
-  for (int t = 0; t < p.L; ++t) {
-    h = apply(expf(to_f32(g[t * p.gs.l])), h, to_f32(x[t * p.xs.l]));
-    out[t * p.hs.l] = from_f32<T>(h);
-  }
-  if (p.last != nullptr) p.last[i] = h;
+// ---- V = 1 or 2 channels of a lane, fp32 ------------------------------------------
+// Two channels go through the packed fp32 instructions.
+template <int V> struct Vec { float f[V]; };
+using u64 = unsigned long long;
+__device__ __forceinline__ u64 bits(const Vec<2>& a) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.f[0]), "f"(a.f[1]));
+  return r;
+}
+__device__ __forceinline__ Vec<2> vec(u64 r) {
+  Vec<2> a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.f[0]), "=f"(a.f[1]) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ Vec<1> fma_(Vec<1> a, Vec<1> b, Vec<1> c) { return {fmaf(a.f[0], b.f[0], c.f[0])}; }
+__device__ __forceinline__ Vec<1> mul_(Vec<1> a, Vec<1> b) { return {a.f[0] * b.f[0]}; }
+__device__ __forceinline__ Vec<1> add_(Vec<1> a, Vec<1> b) { return {a.f[0] + b.f[0]}; }
+__device__ __forceinline__ Vec<2> fma_(Vec<2> a, Vec<2> b, Vec<2> c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return vec(r);
+}
+__device__ __forceinline__ Vec<2> mul_(Vec<2> a, Vec<2> b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return vec(r);
+}
+__device__ __forceinline__ Vec<2> add_(Vec<2> a, Vec<2> b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return vec(r);
 }
 
-template <typename T>
-__global__ void scan_bwd_kernel(ScanArgs p) {
-  const int64_t n = (int64_t)p.B * p.H * p.d;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n) return;
-  const int64_t bh = i / p.d, c = i - bh * p.d, b = bh / p.H, hd = bh - b * p.H;
-  const T* g = static_cast<const T*>(p.g) + b * p.gs.b + hd * p.gs.h + c;
-  const T* h = static_cast<const T*>(p.h_in) + b * p.his.b + hd * p.his.h + c;
-  const T* dh = static_cast<const T*>(p.dh) + b * p.dhs.b + hd * p.dhs.h + c;
-  T* dx = static_cast<T*>(p.dx) + b * p.dxs.b + hd * p.dxs.h + c;
-  T* dg = static_cast<T*>(p.dg) + b * p.dgs.b + hd * p.dgs.h + c;
-  float carry = p.first != nullptr ? p.first[i] : 0.f;
-  for (int t = p.L - 1; t >= 0; --t) {
-    const float a = expf(to_f32(g[t * p.gs.l]));
-    const float u = to_f32(dh[t * p.dhs.l]) + carry;
-    const float prev = t > 0 ? to_f32(h[(t - 1) * p.his.l]) : (p.h0 != nullptr ? p.h0[i] : 0.f);
-    carry = a == 0.f ? 0.f : a * u;
-    dx[t * p.dxs.l] = from_f32<T>(u);
-    dg[t * p.dgs.l] = from_f32<T>(a == 0.f ? 0.f : carry * prev);
+// A h + s, where A = 0 drops h, whatever it is
+template <int V>
+__device__ __forceinline__ Vec<V> apply(const Vec<V>& A, const Vec<V>& s, const Vec<V>& h) {
+  Vec<V> r = fma_(A, h, s);
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.f[v] = A.f[v] == 0.f ? s.f[v] : r.f[v];
+  return r;
+}
+
+// 0 for finite values, NaN otherwise: 0 times an infinity or NaN is NaN
+template <int V>
+__device__ __forceinline__ Vec<V> residue(const Vec<V>& a, const Vec<V>& r) {
+  Vec<V> zero;
+#pragma unroll
+  for (int v = 0; v < V; ++v) zero.f[v] = 0.f;
+  return fma_(a, zero, r);
+}
+__device__ __forceinline__ bool none(const Vec<1>& r) { return r.f[0] == 0.f; }
+__device__ __forceinline__ bool none(const Vec<2>& r) { return r.f[0] + r.f[1] == 0.f; }
+template <int V>
+__device__ __forceinline__ bool finite(const Vec<V>& a) {
+  Vec<V> zero;
+#pragma unroll
+  for (int v = 0; v < V; ++v) zero.f[v] = 0.f;
+  return none(residue(a, zero));
+}
+
+// V channels side by side as they lie in memory
+template <typename T, int V> struct Piece;
+template <> struct Piece<float, 1> {
+  using Raw = float;
+  static __device__ __forceinline__ Vec<1> unpack(Raw r) { return {r}; }
+  static __device__ __forceinline__ Raw pack(const Vec<1>& a) { return a.f[0]; }
+};
+template <> struct Piece<__nv_bfloat16, 1> {
+  using Raw = unsigned short;
+  static __device__ __forceinline__ Vec<1> unpack(Raw r) { return {__uint_as_float((unsigned)r << 16)}; }
+  static __device__ __forceinline__ Raw pack(const Vec<1>& a) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(a.f[0]));
   }
-  if (p.last != nullptr) p.last[i] = carry;
+};
+template <> struct Piece<__nv_bfloat16, 2> {
+  using Raw = unsigned;
+  static __device__ __forceinline__ Vec<2> unpack(Raw r) {
+    return {__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u)};
+  }
+  static __device__ __forceinline__ Raw pack(const Vec<2>& a) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a.f[0], a.f[1]);
+    return *reinterpret_cast<const unsigned*>(&v);
+  }
+};
+
+template <int V>
+__device__ __forceinline__ Vec<V> exp_(Vec<V> g) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) g.f[v] = expf(g.f[v]);
+  return g;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> all(float x) {
+  Vec<V> r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.f[v] = x;
+  return r;
+}
+
+// ---- the ring of tokens ---------------------------------------------------------------
+// N arrays, R tokens of each per thread and stage; every thread copies and
+// reads only its own places (word order [stage][array][token][thread]), so
+// that waiting for its own copies is enough.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool in) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  const int n = in ? BYTES : 0;               // 0: the place is filled with zeros
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- joining the runs ----------------------------------------------------------------------
+// The map (A, s) of one channel
+struct alignas(8) Map {
+  float A, s;
+};
+// after `m`, the map `x`
+__device__ __forceinline__ Map then(const Map& m, const Map& x) { return {m.A * x.A, fmaf(x.A, m.s, x.s)}; }
+// the same where infinities or NaN are about: a closed gate drops what was before it
+__device__ __forceinline__ float through(const Map& x, float h) { return x.A == 0.f ? x.s : fmaf(x.A, h, x.s); }
+__device__ __forceinline__ Map then_checked(const Map& m, const Map& x) {
+  return {x.A == 0.f ? 0.f : m.A * x.A, through(x, m.s)};
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
+// A map into another CTA of the cluster, counted there by the barrier `bar`.
+// (A cluster barrier with release semantics instead would wait, every step,
+// until the global stores of the step before have been acknowledged.)
+__device__ __forceinline__ void send(uint32_t at, const Map& m, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+               "f"(m.A), "f"(m.s), "r"(bar)
+               : "memory");
+}
+
+template <int V>
+struct Joint {
+  Map warp[2][V][kMaxWarps][32];      // the runs' maps, from the workers
+  float in[2][V][kMaxWarps][32];      // the state before each run, to the workers
+  uint64_t bar[2][V];
+  int abort_flag;
+};
+
+// Hardware barriers between the workers and the joiners: "maps" of a step are
+// there (the joiners wait), "states" of a step are there (the workers wait);
+// two of each, by the step's parity.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+constexpr int kBarMaps = 1, kBarStates = 3;
+
+// A joiner's walk over the steps, for channel v of each lane.  A buffer of
+// parity n & 1 is free again at step n + 2: the workers hand over a step's
+// maps only after they have read the states of the step two before, and a CTA
+// sends its map of step n + 2 only when it has every CTA's of step n + 1,
+// which they send after their reads of step n.  cta: the CTAs' maps,
+// [2][V][K][32].  Returns the state behind the last step.
+template <int V>
+__device__ float join(Joint<V>& sm, Map (*cta)[32], int v, int steps, int K, int W, int rank, int lane, float carry,
+                      const tc::WaitCtx& ctx) {
+  const uint32_t me = tc::smem_addr(&sm);
+  const uint32_t peer = K > 1 && lane < K ? tc::map_to_rank(me, lane) : 0;
+  const int threads = (W + V) * 32;
+  for (int n = 0; n < steps; ++n) {
+    const int buf = n & 1;
+    Map(*const there)[32] = cta + (buf * V + v) * K;
+    uint64_t* const bar = &sm.bar[buf][v];
+    if (K > 1 && lane == 0) tc::mbar_arrive_expect_tx(bar, K * 32 * (int)sizeof(Map));
+    bar_sync(kBarMaps + buf, threads);
+    Map m[kMaxWarps];
+#pragma unroll
+    for (int w = 0; w < kMaxWarps; ++w)
+      if (w < W) m[w] = sm.warp[buf][v][w][lane];
+    float h = carry;
+    if (K > 1) {
+      Map total = m[0];
+#pragma unroll
+      for (int w = 1; w < kMaxWarps; ++w)
+        if (w < W) total = then(total, m[w]);
+      // 0 times an infinity or NaN is NaN and stays so: only then are closed gates looked for
+      if (!(finite(total.s) && finite(total.A))) {
+        total = m[0];
+#pragma unroll
+        for (int w = 1; w < kMaxWarps; ++w)
+          if (w < W) total = then_checked(total, m[w]);
+      }
+      const uint32_t at = tc::smem_addr(&there[rank][lane]) - me, bar_at = tc::smem_addr(bar) - me;
+#pragma unroll 1
+      for (int r0 = 0; r0 < K; r0 += kFold) {
+        uint32_t to[kFold];
+#pragma unroll
+        for (int r = 0; r < kFold; ++r) to[r] = __shfl_sync(0xffffffffu, peer, r0 + r);
+#pragma unroll
+        for (int r = 0; r < kFold; ++r)
+          if (r0 + r < K) send(to[r] + at, total, to[r] + bar_at);
+      }
+      tc::mbar_wait(bar, (n >> 1) & 1, ctx);
+      float r = carry;
+#pragma unroll 1
+      for (int c0 = 0; c0 < K; c0 += kFold) {
+        Map c[kFold];
+#pragma unroll
+        for (int i = 0; i < kFold; ++i)
+          if (c0 + i < K) c[i] = there[c0 + i][lane];
+#pragma unroll
+        for (int i = 0; i < kFold; ++i)
+          if (c0 + i < K) {
+            if (c0 + i == rank) h = r;
+            r = fmaf(c[i].A, r, c[i].s);
+          }
+      }
+      if (!finite(r)) {
+        r = carry;
+        for (int c = 0; c < K; ++c) {
+          if (c == rank) h = r;
+          r = through(there[c][lane], r);
+        }
+      }
+      carry = r;
+    }
+    const float first = h;
+#pragma unroll
+    for (int w = 0; w < kMaxWarps; ++w)
+      if (w < W) {
+        sm.in[buf][v][w][lane] = h;
+        h = fmaf(m[w].A, h, m[w].s);
+      }
+    if (!finite(h)) {
+      h = first;
+#pragma unroll
+      for (int w = 0; w < kMaxWarps; ++w)
+        if (w < W) {
+          sm.in[buf][v][w][lane] = h;
+          h = through(m[w], h);
+        }
+    }
+    if (K == 1) carry = h;
+    bar_arrive(kBarStates + buf, threads);
+  }
+  return carry;
+}
+
+// The lane's channels: slots of V channels over all of (B, H, d / V)
+struct Lane {
+  int b, h, c;
+  bool valid;
+};
+__device__ __forceinline__ Lane find_lane(const ScanArgs& p, int V, uint32_t slots, uint32_t slot, int unit) {
+  Lane ln;
+  ln.valid = slot < slots;
+  // idle lanes read the last slot (where `unit` slots go at once, the last
+  // unit's first) and write nothing
+  const uint32_t q = ln.valid ? slot : slots - unit;
+  const uint32_t per_head = p.d / V, bh = q / per_head;
+  ln.c = (int)(q - bh * per_head) * V;
+  ln.b = (int)(bh / p.H);
+  ln.h = (int)(bh - (uint32_t)ln.b * p.H);
+  return ln;
+}
+
+// One walk over the tokens in the order of u (forward t = u, backward
+// t = L - 1 - u).  S: stages of the ring; C: bytes of a copy into it, 16 (four
+// lanes' channels at once), 4 (a lane's own) or 2 (which no asynchronous copy
+// takes: loads that wait in registers until the next fetch).
+template <typename T, int V, int R, int S, int C, bool BACK>
+__global__ void __launch_bounds__((kMaxWarps + V) * 32, 2) scan_kernel(ScanArgs p, uint32_t slots, int K, int W) {
+  using P = Piece<T, V>;
+  using Raw = typename P::Raw;
+  constexpr int N = BACK ? 3 : 2;
+  constexpr int M = C / (int)sizeof(Raw);             // lanes of a copy
+  __shared__ Joint<V> sm;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = K > 1 ? (int)tc::cluster_ctarank() : 0;
+  const uint32_t tile = blockIdx.x / K;
+  const Lane ln = find_lane(p, V, slots, tile * 32 + lane, 1);
+  const int64_t ch = ((int64_t)ln.b * p.H + ln.h) * p.d + ln.c;
+  const int step = K * W * R, steps = (p.L + step - 1) / step;
+  if (K > 1) {
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) tc::mbar_init(&sm.bar[i / V][i % V], 1);
+      tc::fence_barrier_init();
+      sm.abort_flag = 0;
+    }
+    tc::cluster_sync();
+  }
+  if (warp >= W) {                                    // there are no such warps where W = 1
+    const int v = warp - W;
+    float carry = p.first != nullptr ? p.first[ch + v] : 0.f;
+    carry = join<V>(sm, reinterpret_cast<Map(*)[32]>(ring_bytes), v, steps, K, W, rank, lane, carry,
+                    tc::WaitCtx{&sm.abort_flag, p.status});
+    // tokens behind the last one are identities: carry is the state after it
+    if (p.last != nullptr && rank == 0 && ln.valid) p.last[ch + v] = carry;
+    return;
+  }
+
+  // the lane whose channels this thread copies: its own, or where a copy
+  // holds several lanes' the first of them
+  const Lane cl = M > 1 ? find_lane(p, V, slots, tile * 32 + (lane % (32 / M)) * M, M) : ln;
+  auto base = [&](const void* q, const Strides& st, const Lane& at) {
+    return static_cast<const T*>(q) + at.b * st.b + at.h * st.h + at.c;
+  };
+  // arrays in: gates first, then x or dh, then (backward) h of the token before
+  const T* src[N];
+  int ld[N];
+  src[0] = base(p.g, p.gs, cl);
+  ld[0] = (int)p.gs.l;
+  src[1] = BACK ? base(p.dh, p.dhs, cl) : base(p.x, p.xs, cl);
+  ld[1] = (int)(BACK ? p.dhs.l : p.xs.l);
+  if constexpr (BACK) {
+    src[2] = base(p.h_in, p.his, cl);
+    ld[2] = (int)p.his.l;
+  }
+  T* out = const_cast<T*>(BACK ? base(p.dx, p.dxs, ln) : base(p.h, p.hs, ln));
+  T* out2 = BACK ? const_cast<T*>(base(p.dg, p.dgs, ln)) : nullptr;
+  const int lo = (int)(BACK ? p.dxs.l : p.hs.l), lo2 = (int)p.dgs.l;
+
+  Raw* ring = reinterpret_cast<Raw*>(ring_bytes + (K > 1 ? 2 * V * K * 32 * sizeof(Map) : 0)) + threadIdx.x;
+  constexpr int kRow = kMaxWarps * 32;                // a constant, so that a run's words have constant offsets
+  auto place = [&](int stage, int n, int i) -> Raw* { return ring + stage * (N * R * kRow) + (n * R + i) * kRow; };
+  Raw waiting[C == 2 ? N : 1][R];
+  int waiting_stage = -1;
+  // starts the copies of the run that begins at u
+  auto fetch = [&](int stage, int u) {
+    if constexpr (C == 2) {
+      if (waiting_stage >= 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int i = 0; i < R; ++i) *place(waiting_stage, n, i) = waiting[n][i];
+      waiting_stage = stage;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      // h of the token before: none before the first
+      const int t0 = (BACK ? p.L - 1 - u : u) - (n == 2 ? 1 : 0), have = p.L - u - (n == 2 ? 1 : 0);
+      const int sign = BACK ? -1 : 1;
+      if constexpr (C == 2) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          waiting[n][i] =
+              i < have ? *reinterpret_cast<const Raw*>(src[n] + (int64_t)(t0 + sign * i) * ld[n]) : Raw{};
+      } else {
+        const int i0 = lane / (32 / M);               // M tokens of the warp at once
+        Raw* to = place(stage, n, i0) + ((lane % (32 / M)) * M - lane);
+        if (have >= R) {
+          const T* q = src[n] + (int64_t)(t0 + sign * i0) * ld[n];
+#pragma unroll
+          for (int i = 0; i < R; i += M) copy_async<C>(to + i * kRow, q + (int64_t)(sign * i) * ld[n], true);
+        } else {
+          for (int i = 0; i < R; i += M) {
+            const bool in = i0 + i < have;
+            copy_async<C>(to + i * kRow, in ? src[n] + (int64_t)(t0 + sign * (i0 + i)) * ld[n] : src[n], in);
+          }
+        }
+      }
+    }
+  };
+  auto get = [&](int stage, int n, int i) -> Vec<V> { return P::unpack(*place(stage, n, i)); };
+
+  // a run's gates and its map; true if all of it is finite
+  auto form = [&](int stage, int buf, Vec<V> (&a)[R], Vec<V>& A, Vec<V>& s) -> bool {
+    A = all<V>(1.f);
+    s = all<V>(0.f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      a[i] = exp_(get(stage, 0, i));
+      const Vec<V> x = get(stage, 1, i);
+      s = BACK ? mul_(a[i], add_(x, s)) : fma_(a[i], s, x);
+      A = mul_(A, a[i]);
+    }
+    // An infinity or NaN lives on in s and A to the end of the run (0 times it
+    // is NaN): only then is each token looked at for a closed gate.
+    const bool plain = none(residue(s, residue(A, all<V>(0.f))));
+    if (!plain) {
+      A = all<V>(1.f);
+      s = all<V>(0.f);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const Vec<V> x = get(stage, 1, i);
+        if constexpr (BACK) s = apply(a[i], all<V>(0.f), add_(x, s));
+        else s = apply(a[i], x, s);
+        A = apply(a[i], all<V>(0.f), A);
+      }
+    }
+    if (W > 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) sm.warp[buf][v][warp][lane] = Map{A.f[v], s.f[v]};
+      bar_arrive(kBarMaps + buf, (W + V) * 32);
+    }
+    return plain;
+  };
+  // the run's outputs from the state before it
+  auto finish = [&](int stage, int u, const Vec<V> (&a)[R], const Vec<V>& in, bool plain) {
+    const int have = p.L - u;
+    const int t = BACK ? p.L - 1 - u : u;
+    T* po = out + (int64_t)t * lo;
+    T* po2 = BACK ? out2 + (int64_t)t * lo2 : nullptr;
+    // whole runs of finite values (backward: without token 0)
+    if (__all_sync(0xffffffffu, plain && finite(in) && ln.valid) && have >= R + (BACK ? 1 : 0)) {
+      Vec<V> c = in, odd = all<V>(0.f);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const Vec<V> x = get(stage, 1, i);
+        if constexpr (BACK) {
+          const Vec<V> dx = add_(x, c);
+          c = mul_(a[i], dx);
+          const Vec<V> dg = mul_(c, get(stage, 2, i));
+          odd = residue(dg, odd);
+          *reinterpret_cast<Raw*>(po - (int64_t)i * lo) = P::pack(dx);
+          *reinterpret_cast<Raw*>(po2 - (int64_t)i * lo2) = P::pack(dg);
+        } else {
+          c = fma_(a[i], c, x);
+          *reinterpret_cast<Raw*>(po + (int64_t)i * lo) = P::pack(c);
+        }
+      }
+      if (!BACK || none(odd)) return;
+    }
+    // the others, and those whose dg an h that is not finite has touched
+    if (!ln.valid) return;
+    Vec<V> c = in;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (i < have) {
+        const Vec<V> x = get(stage, 1, i);
+        if constexpr (BACK) {
+          const Vec<V> dx = add_(x, c);
+          Vec<V> h = get(stage, 2, i);
+          if (t == i) {                               // before token 0: the initial state
+#pragma unroll
+            for (int v = 0; v < V; ++v) h.f[v] = p.h0 != nullptr ? p.h0[ch + v] : 0.f;
+          }
+          c = apply(a[i], all<V>(0.f), dx);
+          Vec<V> dg;
+#pragma unroll
+          for (int v = 0; v < V; ++v)                 // a closed gate passes nothing on
+            dg.f[v] = a[i].f[v] == 0.f ? 0.f : c.f[v] * h.f[v];
+          *reinterpret_cast<Raw*>(po - (int64_t)i * lo) = P::pack(dx);
+          *reinterpret_cast<Raw*>(po2 - (int64_t)i * lo2) = P::pack(dg);
+        } else {
+          c = apply(a[i], x, c);
+          *reinterpret_cast<Raw*>(po + (int64_t)i * lo) = P::pack(c);
+        }
+      }
+    }
+  };
+
+  int u = (rank * W + warp) * R;
+#pragma unroll
+  for (int st = 0; st < S; ++st) {
+    fetch(st, u + st * step);
+    commit();
+  }
+  auto landed = [&]() {
+    wait_but<S - 2>();
+    __syncwarp();
+  };
+  Vec<V> a[R], A, s;
+  landed();
+  bool plain = form(0, 0, a, A, s);
+  if (W == 1) {                                       // one run, one step
+    Vec<V> in = all<V>(0.f);
+    if (p.first != nullptr)
+#pragma unroll
+      for (int v = 0; v < V; ++v) in.f[v] = p.first[ch + v];
+    finish(0, u, a, in, plain);
+    const Vec<V> end = apply(A, s, in);
+    wait_but<0>();
+    if (p.last != nullptr && ln.valid)
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.last[ch + v] = end.f[v];
+    return;
+  }
+  int stage = 0, n = 0;
+  // one step: forms the next run's gates b while this one's maps are joined
+  auto advance = [&](const Vec<V> (&a)[R], bool plain, Vec<V> (&b)[R]) -> bool {
+    const int next = stage + 1 == S ? 0 : stage + 1;
+    bool plain_next = true;
+    if (n + 1 < steps) {
+      landed();
+      plain_next = form(next, (n + 1) & 1, b, A, s);
+    }
+    bar_sync(kBarStates + (n & 1), (W + V) * 32);
+    Vec<V> in;
+#pragma unroll
+    for (int v = 0; v < V; ++v) in.f[v] = sm.in[n & 1][v][warp][lane];
+    finish(stage, u, a, in, plain);
+    __syncwarp();
+    fetch(stage, u + S * step);
+    commit();
+    stage = next;
+    u += step;
+    ++n;
+    return plain_next;
+  };
+  Vec<V> b[R];
+  while (n < steps) {
+    plain = advance(a, plain, b);
+    if (n < steps) plain = advance(b, plain, a);
+  }
+  wait_but<0>();
 }
 
 template <typename T>
 __global__ void scan_step_kernel(const T* x, const T* g, T* h, const float* state, float* new_state, int n) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
+  const int i = blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= n) return;
-  const float v = apply(expf(to_f32(g[i])), state[i], to_f32(x[i]));
-  new_state[i] = v;
-  h[i] = from_f32<T>(v);
+  const Vec<1> v = apply(Vec<1>{expf(to_f32(g[i]))}, Vec<1>{to_f32(x[i])}, Vec<1>{state[i]});
+  new_state[i] = v.f[0];
+  h[i] = from_f32<T>(v.f[0]);
+}
+
+// How many clusters of each size a device holds at once (of 1: CTAs).
+struct Fits {
+  bool known;
+  int clusters[kMaxCluster + 1];
+};
+template <typename F>
+cudaError_t ask_fits(Fits* fits, const void* kernel, int threads, F&& bytes) {
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, bytes(1));
+  if (e != cudaSuccess) return e;
+  fits->clusters[1] = per_sm * sm_count();
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  for (int k = 2; k <= kMaxCluster; ++k) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)k, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)k);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes(k);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&fits->clusters[k], kernel, &cfg);
+    if (e != cudaSuccess) return e;
+  }
+  fits->known = true;
+  return cudaSuccess;
+}
+
+template <typename T, int V, int C, bool BACK>
+cudaError_t go(const ScanArgs& a, cudaStream_t stream) {
+  constexpr int R = kRun, S = kStages;
+  const auto kernel = scan_kernel<T, V, R, S, C, BACK>;
+  const void* id = reinterpret_cast<const void*>(kernel);
+  const int64_t slots = (int64_t)a.B * a.H * (a.d / V), tiles = (slots + 31) / 32;
+  const int64_t runs = ((int64_t)a.L + R - 1) / R;
+  int W = 1, K = 1;
+  while (W < kMaxWarps && W < runs) W *= 2;
+  constexpr size_t ring = (size_t)S * (BACK ? 3 : 2) * R * kMaxWarps * 32 * sizeof(typename Piece<T, V>::Raw);
+  auto bytes = [](int k) { return ring + (k > 1 ? 2 * V * k * 32 * sizeof(Map) : 0); };
+  cudaError_t e = ensure_dynamic_smem(id, bytes(kMaxCluster));
+  if (e != cudaSuccess) return e;
+  if (runs > kMaxWarps) {
+    // CTAs of a cluster: a wave of clusters of K takes time as 1 / K.  The
+    // smallest K whose waves take at most a tenth longer than the best's: at
+    // 32 tiles of 8192 tokens (bf16 forward) K = 8 takes 25.8 us, K = 4 29.4
+    // and K = 9 (a second wave) 40; at 16 tiles of 12288 (bf16 backward)
+    // K = 12 takes 34.5 us, K = 8 46.4, K = 16 (a second wave) 49.
+    static std::mutex mu;
+    static Fits known[64];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    Fits fits;
+    {
+      std::lock_guard<std::mutex> lock(mu);
+      if (!known[dev].known) {
+        e = ask_fits(&known[dev], id, (W + V) * 32, bytes);
+        if (e != cudaSuccess) return e;
+      }
+      fits = known[dev];
+    }
+    double best = 0;
+    for (const bool pick : {false, true})
+      for (const int k : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (fits.clusters[k] < 1 || (k > 1 && (int64_t)(k - 1) * W >= runs)) continue;
+        const int64_t waves = (tiles + fits.clusters[k] - 1) / fits.clusters[k];
+        const double rate = (double)k / (double)waves;
+        if (!pick) {
+          best = rate > best ? rate : best;
+        } else if (rate >= 0.9 * best) {
+          K = k;
+          break;
+        }
+      }
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)K, 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * K));
+  cfg.blockDim = dim3(W > 1 ? (W + V) * 32 : 32);
+  cfg.dynamicSmemBytes = bytes(K);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = K > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, (uint32_t)slots, K, W);
+}
+
+template <bool BACK>
+cudaError_t go(const ScanArgs& a, bool bf16, int align, cudaStream_t stream) {
+  using B16 = __nv_bfloat16;
+  // 16-byte copies where every row is made of whole ones (a quarter of the
+  // copy instructions); bf16 channels in pairs where rows are made of whole
+  // pairs, else one by one
+  if (!bf16) return align >= 16 ? go<float, 1, 16, BACK>(a, stream) : go<float, 1, 4, BACK>(a, stream);
+  if (align >= 4) return align >= 16 ? go<B16, 2, 16, BACK>(a, stream) : go<B16, 2, 4, BACK>(a, stream);
+  return go<B16, 1, 2, BACK>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_scan(const ScanArgs& a, bool backward, bool bf16, bool pairs, cudaStream_t stream) {
-  (void)pairs;
-  const int64_t n = (int64_t)a.B * a.H * a.d;
-  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
-  if (backward) {
-    if (bf16) scan_bwd_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-    else scan_bwd_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    if (bf16) scan_fwd_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-    else scan_fwd_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+cudaError_t launch_scan(const ScanArgs& a, bool backward, bool bf16, int align, cudaStream_t stream) {
+  return backward ? go<true>(a, bf16, align, stream) : go<false>(a, bf16, align, stream);
 }
 
 cudaError_t launch_scan_step(const void* x, const void* g, void* h, const float* state, float* new_state, int64_t n,
                              bool bf16, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
+  const unsigned grid = (unsigned)((n + kStepThreads - 1) / kStepThreads);
   if (bf16)
-    scan_step_kernel<<<grid, kThreads, 0, stream>>>(static_cast<const __nv_bfloat16*>(x),
-                                                    static_cast<const __nv_bfloat16*>(g),
-                                                    static_cast<__nv_bfloat16*>(h), state, new_state, (int)n);
+    scan_step_kernel<<<grid, kStepThreads, 0, stream>>>(static_cast<const __nv_bfloat16*>(x),
+                                                        static_cast<const __nv_bfloat16*>(g),
+                                                        static_cast<__nv_bfloat16*>(h), state, new_state, (int)n);
   else
-    scan_step_kernel<<<grid, kThreads, 0, stream>>>(static_cast<const float*>(x), static_cast<const float*>(g),
-                                                    static_cast<float*>(h), state, new_state, (int)n);
+    scan_step_kernel<<<grid, kStepThreads, 0, stream>>>(static_cast<const float*>(x), static_cast<const float*>(g),
+                                                        static_cast<float*>(h), state, new_state, (int)n);
   return cudaGetLastError();
 }
 

@@ -31,8 +31,8 @@ def declare(lib):
     """Argument and result types of the entry points."""
     i, size, vp, f = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
     sizes = [i, i, i, i, i, vp]                       # B, H, L, d, dtype, stream
-    lib.favor_fwd_gated_scan.argtypes = [vp] * 6 + [vp, vp] + sizes
-    lib.favor_bwd_gated_scan.argtypes = [vp] * 10 + [vp, vp, vp] + sizes
+    lib.favor_fwd_gated_scan.argtypes = [vp] * 6 + [vp, vp] + sizes + [vp]
+    lib.favor_bwd_gated_scan.argtypes = [vp] * 10 + [vp, vp, vp] + sizes + [vp]
     lib.favor_gated_scan_step.argtypes = [vp] * 5 + [i, i, i, i, vp]
     lib.favor_fwd_layer_norm.argtypes = [vp] * 4 + [vp, vp, f] + sizes
     lib.favor_bwd_layer_norm.argtypes = [vp] * 6 + [vp, vp, vp, f] + [i, i, i, i, i, vp, size, vp]
@@ -64,6 +64,15 @@ def _flat(what, name, t, shape, device):
         return None
     if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
         raise FavorError(f"{what}: {name} must be a contiguous fp32 tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _status(what, t, device):
+    """Pointer of the optional device status, int32."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or t.numel() < 1:
+        raise FavorError(f"{what}: dev_status must be an int32 tensor on {device}")
     return t.data_ptr()
 
 
@@ -107,7 +116,7 @@ def _state_shape(shape):
     return (shape[0], shape[1], shape[3]) if len(shape) == 4 else (shape[0], shape[2])
 
 
-def fwd_gated_scan(X, G, h0=None, O=None, hT=None, stream=None):
+def fwd_gated_scan(X, G, h0=None, O=None, hT=None, dev_status=None, stream=None):
     """h_t = exp(G_t) h_{t-1} + X_t over the tokens of X, G [B, H, L, d] (or
     [B, L, d]), from the state h0 (fp32 [B, H, d] or [B, d], None: zeros).
     Returns (O, hT): every h_t in X's dtype and layout, and the last one in
@@ -128,11 +137,12 @@ def fwd_gated_scan(X, G, h0=None, O=None, hT=None, stream=None):
     op, os_ = _tensor(what, "O", O, shape, dt, dev)
     state = _state_shape(shape)
     _run(what, dev, stream, (xp, xs, gp, gs, op, os_, _flat(what, "h0", h0, state, dev),
-                             _flat(what, "hT", hT, state, dev), B, H, L, d, _DT[dt]), made)
+                             _flat(what, "hT", hT, state, dev), B, H, L, d, _DT[dt],
+                             _status(what, dev_status, dev)), made)
     return O, hT
 
 
-def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, stream=None):
+def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, dev_status=None, stream=None):
     """Gradients (dX, dG, dh0) of fwd_gated_scan for those of its outputs, dO
     and dhT (None: zeros); O is its output and h0 its initial state.  dX may
     be dO, dG may be G, dh0 may be dhT.  For a gate broadcast over an axis sum
@@ -155,7 +165,7 @@ def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, stre
     for name, t in (("G", G), ("O", O), ("dO", dO), ("dX", dX), ("dG", dG)):
         args += _tensor(what, name, t, shape, dt, dev)
     args += [_flat(what, "h0", h0, state, dev), _flat(what, "dhT", dhT, state, dev),
-             _flat(what, "dh0", dh0, state, dev), B, H, L, d, _DT[dt]]
+             _flat(what, "dh0", dh0, state, dev), B, H, L, d, _DT[dt], _status(what, dev_status, dev)]
     _run(what, dev, stream, args, made)
     return dX, dG, dh0
 

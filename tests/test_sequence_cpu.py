@@ -25,7 +25,7 @@ def scan(lib, **kw):
     a = dict(x=0x1000, xs=None, g=0x2000, gs=None, h=0x3000, hs=None, h0=0x4000, hT=0x5000, B=1, H=2, L=8, d=8, dt=0)
     a.update(kw)
     return lib.favor_fwd_gated_scan(a["x"], a["xs"], a["g"], a["gs"], a["h"], a["hs"], a["h0"], a["hT"], a["B"],
-                                    a["H"], a["L"], a["d"], a["dt"], None)
+                                    a["H"], a["L"], a["d"], a["dt"], None, None)
 
 
 def scan_bwd(lib, **kw):
@@ -33,7 +33,7 @@ def scan_bwd(lib, **kw):
              d=8, dt=0, s=None)
     a.update(kw)
     return lib.favor_bwd_gated_scan(a["g"], None, a["h"], None, a["dh"], None, a["dx"], a["s"], a["dg"], None,
-                                    a["h0"], a["dhT"], a["dh0"], a["B"], a["H"], a["L"], a["d"], a["dt"], None)
+                                    a["h0"], a["dhT"], a["dh0"], a["B"], a["H"], a["L"], a["d"], a["dt"], None, None)
 
 
 def step(lib, **kw):
