@@ -5,9 +5,11 @@
 // thread), its mean and then its centred second moment summed from there, and
 // written once; the backward pass recomputes both from x instead of reading
 // them.  Rows of up to 512 values belong to a group of 4 to 32 lanes of a
-// warp, longer ones to a CTA.  The CTAs walk the rows with a stride, the next
-// row's loads in flight while one is worked on; gamma and beta, and in the
-// backward pass the columns' sums, stay in registers meanwhile.
+// warp, longer ones to a CTA.  The CTAs walk the rows with a stride; each
+// thread copies its pieces of the next rows ahead into its own places in
+// shared memory (48 to 64 KB in flight per SM, which registers alone could not
+// hold), while gamma and beta, and in the backward pass the columns' sums,
+// stay in registers.
 #include <algorithm>
 
 #include "ops.cuh"
@@ -18,7 +20,7 @@ namespace {
 
 constexpr int kWarps = 8;             // of a CTA that shares its rows out by groups of lanes
 constexpr int kMaxValues = 16;        // of a row in one thread
-constexpr int kSumRows = 8, kSumThreads = 32 * kSumRows;
+constexpr int kSumRows = 16, kSumThreads = 32 * kSumRows;
 
 // VW values side by side: 16 bytes, or one element
 template <typename T, int VW> struct Piece;
@@ -92,46 +94,114 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float* scratch
   }
 }
 
-// One row's values in this thread: piece j holds the columns from
-// (j lanes + lane) VW on
+// A row's pieces in this thread: piece j holds the columns from
+// (j lanes + lane) VW on.  Those of the next S rows of N tensors are on their
+// way, in the thread's own places in shared memory (bf16 elements one by one,
+// which no asynchronous copy takes, in registers: one row ahead).
 template <typename T, int VW, int NV, int CTA>
-struct Row {
-  using P = Piece<T, VW>;
-  using Raw = typename P::Raw;
-  Raw raw[NV];
-  __device__ __forceinline__ void load(const T* row, int lane, int lanes, int d, bool in) {
+struct Kind {};
+template <typename T, int VW, int NV, int N>
+struct Ahead {
+  using Raw = typename Piece<T, VW>::Raw;
+  static constexpr bool kAsync = sizeof(Raw) >= 4;
+  static constexpr int S = !kAsync ? 1 : N == 2 ? (NV * VW * sizeof(T) <= 16 ? 3 : NV * VW * sizeof(T) <= 32 ? 2 : 1)
+                                                : (NV * VW * sizeof(T) <= 16 ? 4 : NV * VW * sizeof(T) <= 32 ? 2 : 1);
+  static constexpr size_t kBytes = kAsync ? (size_t)S * N * NV * sizeof(Raw) : 0;   // per thread
+  Raw regs[kAsync ? 1 : N][kAsync ? 1 : NV];
+  Raw* mine;
+  int stage;
+  __device__ __forceinline__ Ahead(void* ring) : mine(static_cast<Raw*>(ring) + threadIdx.x), stage(0) {}
+  __device__ __forceinline__ Raw* place(int n, int j) const {
+    return mine + ((stage * N + n) * NV + j) * (int)blockDim.x;
+  }
+  // starts tensor n's copies of a row (none of them where !in)
+  __device__ __forceinline__ void fetch(int n, const T* any, const T* row, int lane, int lanes, int d, bool in) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * lanes + lane) * VW;
-      if (in && c < d) raw[j] = *reinterpret_cast<const Raw*>(row + c);
-      else raw[j] = Raw{};
+      const bool here = in && c < d;
+      if constexpr (kAsync) {
+        const uint32_t to = tc::smem_addr(place(n, j));
+        const T* from = here ? row + c : any;         // a source for the copy of no bytes: zeros
+        if constexpr (sizeof(Raw) == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(here ? 16 : 0)
+                       : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(here ? 4 : 0)
+                       : "memory");
+      } else {
+        regs[n][j] = here ? *reinterpret_cast<const Raw*>(row + c) : Raw{};
+      }
     }
   }
+  __device__ __forceinline__ void commit() {
+    if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() {
+    if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+  }
+  // nothing is on its way any more
+  __device__ __forceinline__ void drain() {
+    if constexpr (kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __device__ __forceinline__ void take(int n, float (&x)[NV][VW]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (kAsync) Piece<T, VW>::unpack(*place(n, j), x[j]);
+      else Piece<T, VW>::unpack(regs[n][j], x[j]);
+    }
+  }
+  __device__ __forceinline__ void advance() { stage = stage + 1 == S ? 0 : stage + 1; }
 };
 
-// mean and 1 / sqrt(var + eps); x becomes x - mean (0 behind the row)
-template <int VW, int NV, int CTA>
-__device__ __forceinline__ float centre(float (&x)[NV][VW], int lane, int lanes, int d, float inv_d, float eps,
-                                        float* scratch) {
-  float s[1] = {0.f};
+// Values two by two through the packed fp32 instructions, one by one where a
+// piece is one element
+template <int VW> struct Each {
+  template <typename F>
+  static __device__ __forceinline__ void go(F&& f) {
+    if constexpr (VW > 1) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < VW; ++i) s[0] += x[j][i];
-  row_sum<1, CTA>(s, lanes, scratch);
-  const float mean = s[0] * inv_d;
-  float v[1] = {0.f};
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const bool in = (j * lanes + lane) * VW < d;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) {
-      x[j][i] = in ? x[j][i] - mean : 0.f;
-      v[0] = fmaf(x[j][i], x[j][i], v[0]);
+      for (int i = 0; i < VW; i += 2) f(i);
+    } else {
+      f(0);
     }
   }
-  row_sum<1, CTA>(v, lanes, scratch + 32);
-  return 1.f / sqrtf(fmaf(v[0], inv_d, eps));
+  // (a pair of) x at i, and back; the second of a single value is 0
+  static __device__ __forceinline__ float2 get(const float (&x)[VW], int i) {
+    return VW > 1 ? make_float2(x[i], x[VW > 1 ? i + 1 : 0]) : make_float2(x[0], 0.f);
+  }
+  static __device__ __forceinline__ void put(float (&x)[VW], int i, float2 v) {
+    x[i] = v.x;
+    if (VW > 1) x[VW > 1 ? i + 1 : 0] = v.y;
+  }
+};
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+// x becomes x - mean (0 behind the row); returns this thread's part of the sum
+// of its squares
+template <int VW, int NV, int CTA>
+__device__ __forceinline__ float centre(float (&x)[NV][VW], int lane, int lanes, int d, float inv_d, float* scratch) {
+  using E = Each<VW>;
+  float2 s2 = twice(0.f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) E::go([&](int i) { s2 = add2(s2, E::get(x[j], i)); });
+  float s[1] = {s2.x + s2.y};
+  row_sum<1, CTA>(s, lanes, scratch);
+  const float2 mean = twice(-s[0] * inv_d);
+  const bool whole = NV * VW * lanes == d;            // no thread has places behind the row
+  float2 v2 = twice(0.f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const bool in = whole || (j * lanes + lane) * VW < d;
+    E::go([&](int i) {
+      float2 c = add2(E::get(x[j], i), mean);
+      if (VW == 1) c.y = 0.f;
+      if (!in) c = twice(0.f);
+      E::put(x[j], i, c);
+      v2 = fma2(c, c, v2);
+    });
+  }
+  return v2.x + v2.y;
 }
 
 template <int VW, int NV>
@@ -146,106 +216,134 @@ __device__ __forceinline__ void load_weights(float (&w)[NV][VW], const float* p,
 }
 
 template <typename T, int VW, int NV, int CTA>
-__global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps) norm_fwd_kernel(NormArgs p, Rows rows, uint32_t n,
-                                                                            Plan plan) {
+__global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : NV * VW > 8 ? 3 : 4)
+    norm_fwd_kernel(NormArgs p, Rows rows, uint32_t n, Plan plan) {
   using P = Piece<T, VW>;
+  using A = Ahead<T, VW, NV, 1>;
+  using E = Each<VW>;
   __shared__ float scratch[64];
+  extern __shared__ __align__(16) float ring[];
   const int lanes = plan.lanes, lane = CTA > 0 ? threadIdx.x : threadIdx.x & (lanes - 1);
   const uint32_t group = CTA > 0 ? blockIdx.x : blockIdx.x * plan.groups + threadIdx.x / lanes;
   const uint32_t stride = (uint32_t)plan.ctas * plan.groups;
   const float inv_d = 1.f / p.d;
+  const T* x0 = static_cast<const T*>(p.x);
+  A ahead(ring);
+  auto fetch = [&](uint32_t r) {
+    ahead.fetch(0, x0, x0 + rows.offset(0, r), lane, lanes, p.d, r < n);
+    ahead.commit();
+  };
+#pragma unroll
+  for (int s = 0; s < A::S; ++s) {
+    fetch(group + s * stride);
+    ahead.advance();
+  }
   float w[NV][VW], z[NV][VW];
   load_weights<VW, NV>(w, p.gamma, lane, lanes, p.d, 1.f);
   load_weights<VW, NV>(z, p.beta, lane, lanes, p.d, 0.f);
-  uint32_t b, h, t;
-  Row<T, VW, NV, CTA> next;
-  rows.split(group, &b, &h, &t);
-  next.load(static_cast<const T*>(p.x) + rows.offset(0, b, h, t), lane, lanes, p.d, group < n);
+  const bool affine = p.gamma != nullptr || p.beta != nullptr;
   // every thread of a warp (of a CTA) walks as long as its first one
   const uint32_t first = CTA > 0 ? group : group - (threadIdx.x & 31) / lanes;
   for (uint32_t r = group, r0 = first; r0 < n; r += stride, r0 += stride) {
     float x[NV][VW];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) P::unpack(next.raw[j], x[j]);
-    T* y = static_cast<T*>(p.y) + rows.offset(1, b, h, t);
-    if (r0 + stride < n) {
-      rows.split(r + stride, &b, &h, &t);
-      next.load(static_cast<const T*>(p.x) + rows.offset(0, b, h, t), lane, lanes, p.d, r + stride < n);
-    }
-    const float rstd = centre<VW, NV, CTA>(x, lane, lanes, p.d, inv_d, p.eps, scratch);
+    ahead.wait();
+    ahead.take(0, x);
+    fetch(r + A::S * stride);
+    ahead.advance();
+    float v[1] = {centre<VW, NV, CTA>(x, lane, lanes, p.d, inv_d, scratch)};
+    row_sum<1, CTA>(v, lanes, scratch + 32);
+    const float rstd = rsqrtf(fmaf(v[0], inv_d, p.eps));
+    T* y = static_cast<T*>(p.y) + rows.offset(1, r);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * lanes + lane) * VW;
-#pragma unroll
-      for (int i = 0; i < VW; ++i) x[j][i] = fmaf(x[j][i] * rstd, w[j][i], z[j][i]);
+      E::go([&](int i) {
+        float2 v = mul2(E::get(x[j], i), twice(rstd));
+        if (affine) v = fma2(v, E::get(w[j], i), E::get(z[j], i));
+        E::put(x[j], i, v);
+      });
       if (r < n && c < p.d) *reinterpret_cast<typename P::Raw*>(y + c) = P::pack(x[j]);
     }
   }
+  ahead.drain();
 }
 
 // dx, and the sums of dy xh and dy over the CTA's rows, [CTA][2][d] in `part`
 // (NULL: not wanted).
 template <typename T, int VW, int NV, int CTA>
-__global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : 2) norm_bwd_kernel(NormArgs p, Rows rows,
-                                                                                     uint32_t n, Plan plan,
-                                                                                     float* part) {
+__global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : NV * VW <= 4 ? 4 : 2)
+    norm_bwd_kernel(NormArgs p, Rows rows, uint32_t n, Plan plan, float* part) {
   using P = Piece<T, VW>;
-  __shared__ float scratch[128];
-  extern __shared__ float sums[];                     // [groups / 2][2][d], rows shared out by lanes
+  using A = Ahead<T, VW, NV, 2>;
+  using E = Each<VW>;
+  __shared__ float scratch[32 + 3 * 32];
+  extern __shared__ __align__(16) float ring[];
   const int lanes = plan.lanes, lane = CTA > 0 ? threadIdx.x : threadIdx.x & (lanes - 1);
   const uint32_t group = CTA > 0 ? blockIdx.x : blockIdx.x * plan.groups + threadIdx.x / lanes;
   const uint32_t stride = (uint32_t)plan.ctas * plan.groups;
   const float inv_d = 1.f / p.d;
+  const T *x0 = static_cast<const T*>(p.x), *dy0 = static_cast<const T*>(p.dy);
+  A ahead(ring);
+  auto fetch = [&](uint32_t r) {
+    ahead.fetch(0, x0, x0 + rows.offset(0, r), lane, lanes, p.d, r < n);
+    ahead.fetch(1, dy0, dy0 + rows.offset(1, r), lane, lanes, p.d, r < n);
+    ahead.commit();
+  };
+#pragma unroll
+  for (int s = 0; s < A::S; ++s) {
+    fetch(group + s * stride);
+    ahead.advance();
+  }
   float w[NV][VW], dw[NV][VW], dz[NV][VW];
   load_weights<VW, NV>(w, p.gamma, lane, lanes, p.d, 1.f);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < VW; ++i) dw[j][i] = dz[j][i] = 0.f;
-  uint32_t b, h, t;
-  Row<T, VW, NV, CTA> nx, ny;
-  auto load = [&](uint32_t r) {
-    rows.split(r, &b, &h, &t);
-    nx.load(static_cast<const T*>(p.x) + rows.offset(0, b, h, t), lane, lanes, p.d, r < n);
-    ny.load(static_cast<const T*>(p.dy) + rows.offset(1, b, h, t), lane, lanes, p.d, r < n);
-  };
-  load(group);
   const uint32_t first = CTA > 0 ? group : group - (threadIdx.x & 31) / lanes;
   for (uint32_t r = group, r0 = first; r0 < n; r += stride, r0 += stride) {
     float x[NV][VW], dy[NV][VW];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      P::unpack(nx.raw[j], x[j]);
-      P::unpack(ny.raw[j], dy[j]);
-    }
-    T* dx = static_cast<T*>(p.dx) + rows.offset(2, b, h, t);
-    if (r0 + stride < n) load(r + stride);
-    const float rstd = centre<VW, NV, CTA>(x, lane, lanes, p.d, inv_d, p.eps, scratch);
-    float s[2] = {0.f, 0.f};
+    ahead.wait();
+    ahead.take(0, x);
+    ahead.take(1, dy);
+    fetch(r + A::S * stride);
+    ahead.advance();
+    // one more sum of three values: (x - mean)^2, n = dy gamma, n (x - mean)
+    float s[3] = {centre<VW, NV, CTA>(x, lane, lanes, p.d, inv_d, scratch), 0.f, 0.f};
+    float2 s1 = twice(0.f), s2 = twice(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        x[j][i] *= rstd;                              // xh; dy is 0 behind the row
-        dw[j][i] = fmaf(dy[j][i], x[j][i], dw[j][i]);
-        dz[j][i] += dy[j][i];
-        dy[j][i] *= w[j][i];
-        s[0] += dy[j][i];
-        s[1] = fmaf(dy[j][i], x[j][i], s[1]);
-      }
-    row_sum<2, CTA>(s, lanes, scratch + 64);
-    const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+      E::go([&](int i) {                              // dy is 0 behind the row
+        const float2 g = E::get(dy[j], i), m = mul2(g, E::get(w[j], i));
+        E::put(dz[j], i, add2(E::get(dz[j], i), g));
+        s1 = add2(s1, m);
+        s2 = fma2(m, E::get(x[j], i), s2);
+      });
+    s[1] = s1.x + s1.y;
+    s[2] = s2.x + s2.y;
+    row_sum<3, CTA>(s, lanes, scratch + 32);
+    const float rstd = rsqrtf(fmaf(s[0], inv_d, p.eps));
+    const float2 m1 = twice(-s[1] * inv_d), m2 = twice(-s[2] * rstd * inv_d);
+    T* dx = static_cast<T*>(p.dx) + rows.offset(2, r);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * lanes + lane) * VW;
-#pragma unroll
-      for (int i = 0; i < VW; ++i) x[j][i] = rstd * (dy[j][i] - m1 - x[j][i] * m2);
+      E::go([&](int i) {
+        const float2 xh = mul2(E::get(x[j], i), twice(rstd)), g = E::get(dy[j], i);
+        E::put(dw[j], i, fma2(g, xh, E::get(dw[j], i)));
+        E::put(x[j], i, mul2(fma2(xh, m2, fma2(g, E::get(w[j], i), m1)), twice(rstd)));
+      });
       if (r < n && c < p.d) *reinterpret_cast<typename P::Raw*>(dx + c) = P::pack(x[j]);
     }
   }
+  ahead.drain();
   if (part == nullptr) return;
+  // the kernel that adds the CTAs' sums may take its place and wait
+  asm volatile("griddepcontrol.launch_dependents;");
   if constexpr (CTA == 0) {
-    // the groups' sums, halved until the first group has them all
+    // the groups' sums, halved until the first group has them all: [groups / 2][2][d]
+    // in the ring's place
+    float* sums = ring;
     const int me = threadIdx.x / lanes;
     for (int half = plan.groups >> 1; half > 0; half >>= 1) {
       __syncthreads();
@@ -310,38 +408,52 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float* part
   }
 }
 
-// CTAs: as many as are resident (the backward pass's hold half the SM's
-// registers each), so that every one walks about the same number of rows
+// CTAs: as many as the registers let be resident, so that every one walks
+// about the same number of rows
 Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
   const int vw = vec ? (bf16 ? 8 : 4) : 1;
   const int pieces = (d + vw - 1) / vw, per = kMaxValues / vw;     // pieces of a row, of a thread at most
   Plan p;
-  int64_t per_sm;
+  int nv;
   if (pieces <= 32 * per) {
+    // as many values a thread as there may be: what a row costs beside them (its
+    // address, sums over lanes, root) is then shared by the most of them.  16
+    // values against 8 (65536 x 16 rows of 128 bf16): FWD16 against FWD8 us.
     p.lanes = 4;
-    while (p.lanes < 32 && p.lanes < pieces) p.lanes *= 2;
+    while (p.lanes < 32 && p.lanes * per < pieces) p.lanes *= 2;
     p.threads = 32 * kWarps;
     p.groups = p.threads / p.lanes;
-    per_sm = backward ? 2 : 6;
+    nv = (pieces + p.lanes - 1) / p.lanes;
   } else {
-    p.threads = p.lanes = ((pieces + per - 1) / per + 31) / 32 * 32;
+    // element by element a thread gets through fewer of them: 4 while 256 threads
+    // hold the row (3333 rows of 771 fp32, backward: ODD4 us, with 16 ODD16)
+    const int most = vw == 1 && pieces <= 256 * 4 ? 4 : per;
+    p.threads = p.lanes = ((pieces + most - 1) / most + 31) / 32 * 32;
     p.groups = 1;
-    per_sm = std::max(1, (backward ? 640 : 1024) / p.threads);
+    nv = (pieces + p.lanes - 1) / p.lanes;
   }
-  p.ctas = (int)std::min<int64_t>((rows + p.groups - 1) / p.groups, per_sm * sm_count());
+  const bool many = p.threads <= 256 && nv * vw <= 8;
+  // threads of an SM
+  const int resident = backward ? (p.threads <= 256 && nv * vw <= 4 ? 1024 : 512) : many ? 1024 : 768;
+  const int64_t per_sm = std::max(1, resident / p.threads);
+  int64_t ctas = std::min<int64_t>((rows + p.groups - 1) / p.groups, per_sm * sm_count());
+  // every CTA's sums are added up after: rows enough for each to make that little
+  if (backward) ctas = std::min(ctas, std::max<int64_t>(2 * sm_count(), rows / (8 * p.groups)));
+  p.ctas = (int)ctas;
   return p;
 }
 
 // (T, VW, NV, CTA) of a plan; CTA: the most threads of a row's CTA, 0 for groups of
-// lanes (up to 256 threads may use twice the registers)
+// lanes (fewer threads may use more registers)
 template <typename F>
 cudaError_t dispatch(const Plan& plan, int d, bool bf16, bool vec, F&& f) {
   const int vw = vec ? (bf16 ? 8 : 4) : 1;
   const int nv = ((d + vw - 1) / vw + plan.lanes - 1) / plan.lanes;
-#define FAVOR_NORM(T, VW, NV)                          \
-  return plan.lanes <= 32    ? f(Row<T, VW, NV, 0>{})   \
-         : plan.lanes <= 256 ? f(Row<T, VW, NV, 256>{}) \
-                             : f(Row<T, VW, NV, 1024>{})
+#define FAVOR_NORM(T, VW, NV)                           \
+  return plan.lanes <= 32    ? f(Kind<T, VW, NV, 0>{})   \
+         : plan.lanes <= 256 ? f(Kind<T, VW, NV, 256>{}) \
+         : plan.lanes <= 512 ? f(Kind<T, VW, NV, 512>{}) \
+                             : f(Kind<T, VW, NV, 1024>{})
   if (bf16 && vec) {
     if (nv <= 1) { FAVOR_NORM(__nv_bfloat16, 8, 1); }
     FAVOR_NORM(__nv_bfloat16, 8, 2);
@@ -361,21 +473,24 @@ cudaError_t dispatch(const Plan& plan, int d, bool bf16, bool vec, F&& f) {
 }
 
 template <typename T, int VW, int NV, int CTA>
-cudaError_t fwd(Row<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint32_t n, const Plan& plan,
+cudaError_t fwd(Kind<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint32_t n, const Plan& plan,
                 cudaStream_t stream) {
-  norm_fwd_kernel<T, VW, NV, CTA><<<plan.ctas, plan.threads, 0, stream>>>(a, rows, n, plan);
+  const size_t smem = Ahead<T, VW, NV, 1>::kBytes * plan.threads;
+  const auto kernel = norm_fwd_kernel<T, VW, NV, CTA>;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<plan.ctas, plan.threads, smem, stream>>>(a, rows, n, plan);
   return cudaGetLastError();
 }
 
 template <typename T, int VW, int NV, int CTA>
-cudaError_t bwd(Row<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint32_t n, const Plan& plan, float* part,
+cudaError_t bwd(Kind<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint32_t n, const Plan& plan, float* part,
                 cudaStream_t stream) {
-  const size_t smem = part != nullptr && CTA == 0 ? (size_t)(plan.groups / 2) * 2 * a.d * sizeof(float) : 0;
+  const size_t sums = CTA == 0 ? (size_t)(plan.groups / 2) * 2 * a.d * sizeof(float) : 0;
+  const size_t smem = std::max(Ahead<T, VW, NV, 2>::kBytes * plan.threads, sums);
   const auto kernel = norm_bwd_kernel<T, VW, NV, CTA>;
-  if (smem > 0) {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
   kernel<<<plan.ctas, plan.threads, smem, stream>>>(a, rows, n, plan, part);
   return cudaGetLastError();
 }

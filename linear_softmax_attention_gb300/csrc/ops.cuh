@@ -80,11 +80,41 @@ struct Rows {
       *hh = r - *b * h.d;
     }
   }
-  __device__ __forceinline__ int64_t offset(int i, uint32_t b, uint32_t hh, uint32_t t) const {
+  __device__ __forceinline__ int64_t offset(int i, uint32_t row) const {
+    if (l.d == 1 && h.d == 1) return row * s[i].b;
+    uint32_t b, hh, t;
+    split(row, &b, &hh, &t);
     return b * s[i].b + hh * s[i].h + t * s[i].l;
   }
 };
 Rows make_rows(int B, int H, int L, const Strides* s, int n);
+
+// ---- two fp32 operations in one instruction --------------------------------------
+__device__ __forceinline__ unsigned long long f32x2_bits(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_of(unsigned long long r) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f32x2_bits(a)), "l"(f32x2_bits(b)), "l"(f32x2_bits(c)));
+  return f32x2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f32x2_bits(a)), "l"(f32x2_bits(b)));
+  return f32x2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f32x2_bits(a)), "l"(f32x2_bits(b)));
+  return f32x2_of(r);
+}
 
 // ---- launchers ------------------------------------------------------------------
 struct ScanArgs {

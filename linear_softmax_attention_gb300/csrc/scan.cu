@@ -35,34 +35,21 @@ constexpr int kStepThreads = 128;
 // ---- V = 1 or 2 channels of a lane, fp32 ------------------------------------------
 // Two channels go through the packed fp32 instructions.
 template <int V> struct Vec { float f[V]; };
-using u64 = unsigned long long;
-__device__ __forceinline__ u64 bits(const Vec<2>& a) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.f[0]), "f"(a.f[1]));
-  return r;
-}
-__device__ __forceinline__ Vec<2> vec(u64 r) {
-  Vec<2> a;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.f[0]), "=f"(a.f[1]) : "l"(r));
-  return a;
-}
 __device__ __forceinline__ Vec<1> fma_(Vec<1> a, Vec<1> b, Vec<1> c) { return {fmaf(a.f[0], b.f[0], c.f[0])}; }
 __device__ __forceinline__ Vec<1> mul_(Vec<1> a, Vec<1> b) { return {a.f[0] * b.f[0]}; }
 __device__ __forceinline__ Vec<1> add_(Vec<1> a, Vec<1> b) { return {a.f[0] + b.f[0]}; }
+__device__ __forceinline__ float2 both(const Vec<2>& a) { return make_float2(a.f[0], a.f[1]); }
 __device__ __forceinline__ Vec<2> fma_(Vec<2> a, Vec<2> b, Vec<2> c) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return vec(r);
+  const float2 r = fma2(both(a), both(b), both(c));
+  return {r.x, r.y};
 }
 __device__ __forceinline__ Vec<2> mul_(Vec<2> a, Vec<2> b) {
-  u64 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return vec(r);
+  const float2 r = mul2(both(a), both(b));
+  return {r.x, r.y};
 }
 __device__ __forceinline__ Vec<2> add_(Vec<2> a, Vec<2> b) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return vec(r);
+  const float2 r = add2(both(a), both(b));
+  return {r.x, r.y};
 }
 
 // A h + s, where A = 0 drops h, whatever it is

@@ -24,7 +24,9 @@ __all__ = ["fwd_gated_scan", "bwd_gated_scan", "gated_scan_step", "new_gated_sca
 PAIRINGS = {"adjacent": 0, "halves": 1}              # favor_pairing
 MAX_AXES = 4
 _S3 = ctypes.c_int64 * 3
-_NORM_MAX_D = 16384
+_INT = (1 << 31) - 1
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # None: a torch without CUDA
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def declare(lib):
@@ -45,75 +47,78 @@ def declare(lib):
     lib.favor_bwd_layer_norm_workspace_bytes.restype = size
 
 
-def _tensor(what, name, t, shape, dtype, device):
-    """Pointer and strides (None: contiguous) of a view [B, H, L, d]."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
-        raise FavorError(f"{what}: {name} must be a {dtype} tensor {list(shape)} on {device}, "
+# Small calls are bound by the host's time, so the helpers below ask torch for
+# little: device indexes instead of devices, the raw handle of the current
+# stream instead of a Stream object.
+
+def _view(what, name, t, shape, dtype, index):
+    """Pointer and strides (None: contiguous) of a view [B, H, L, d] or [B, L, d]."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise FavorError(f"{what}: {name} must be a {dtype} tensor {list(shape)} on cuda:{index}, "
                          f"not {t.dtype} {list(t.shape)} on {t.device}")
     if t.is_contiguous():
         return t.data_ptr(), None
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise FavorError(f"{what}: {name} must have a unit stride along its last axis")
-    return t.data_ptr(), (_S3(*st[:3]) if len(st) == 4 else _S3(st[0], 0, st[1]))
+    return t.data_ptr(), (_S3(st[0], st[1], st[2]) if len(st) == 4 else _S3(st[0], 0, st[1]))
 
 
-def _flat(what, name, t, shape, device):
-    """Pointer of a contiguous fp32 tensor, None for None."""
+def _flat(what, name, t, shape, index, dtype=torch.float32):
+    """Pointer of a contiguous tensor, None for None."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise FavorError(f"{what}: {name} must be a contiguous fp32 tensor {list(shape)} on {device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise FavorError(f"{what}: {name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
     return t.data_ptr()
 
 
-def _status(what, t, device):
+def _status(what, t, index):
     """Pointer of the optional device status, int32."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or t.numel() < 1:
-        raise FavorError(f"{what}: dev_status must be an int32 tensor on {device}")
+    if t.dtype is not torch.int32 or t.get_device() != index or t.numel() < 1:
+        raise FavorError(f"{what}: dev_status must be an int32 tensor on cuda:{index}")
     return t.data_ptr()
 
 
-def _sizes(what, name, t, dims=(3, 4)):
-    """(B, H, L, d, shape) of a CUDA tensor [B, H, L, d] or [B, L, d]."""
-    if not t.is_cuda or t.dtype not in _DT or t.dim() not in dims:
+def _sizes(what, name, t, four_only=False):
+    """B, H, L, d, dtype, device index of a CUDA tensor [B, H, L, d] or [B, L, d]."""
+    dims = t.dim()
+    if not t.is_cuda or t.dtype not in _DT or (dims != 4 and (four_only or dims != 3)):
         raise FavorError(f"{what}: {name} must be an fp32 or bf16 CUDA tensor [B, H, L, d]"
-                         + (" or [B, L, d]" if 3 in dims else ""))
-    shape = tuple(t.shape)
-    B, H, L, d = shape if len(shape) == 4 else (shape[0], 1, shape[1], shape[2])
-    if min(B, H, L, d) < 1 or max(B, H, L, d) >= 1 << 31:
-        raise FavorError(f"{what}: {name} has an empty or oversized axis: {list(shape)}")
-    return B, H, L, d, shape
-
-
-def _run(what, device, stream, args, made=()):
-    """The call `what` on the tensors' device.  `made`: tensors allocated here
-    on the current stream, used on `stream`."""
-    fn = getattr(load(), what)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _run(what, device, stream, args, made)
-    current = torch.cuda.current_stream(device)
-    if stream is None:
-        stream = current
+                         + ("" if four_only else " or [B, L, d]"))
+    if dims == 4:
+        B, H, L, d = t.shape
     else:
-        if stream.device != device:
-            raise FavorError(f"{what}: the stream belongs to {stream.device}, the tensors to {device}")
-        if stream != current:
-            for t in made:
-                t.record_stream(stream)
-    _check(fn(*args, stream.cuda_stream), what)
+        B, L, d = t.shape
+        H = 1
+    if B < 1 or H < 1 or L < 1 or d < 1 or B > _INT or H > _INT or L > _INT or d > _INT:
+        raise FavorError(f"{what}: {name} has an empty or oversized axis: {list(t.shape)}")
+    return B, H, L, d, t.dtype, t.get_device()
+
+
+def _call(what, index, stream, made, args):
+    """The entry point `what` on device `index`.  made: tensors allocated here
+    on the current stream, for use on `stream`."""
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return _call(what, index, stream, made, args)
+    handle = _raw_stream(index)
+    if stream is not None and stream.cuda_stream != handle:
+        if stream.device.index != index:
+            raise FavorError(f"{what}: the stream belongs to {stream.device}, the tensors to cuda:{index}")
+        handle = stream.cuda_stream
+        for t in made:
+            t.record_stream(stream)
+    code = getattr(load(), what)(*args, handle)
+    if code != 0:
+        _check(code, what)
 
 
 def new_gated_scan_state(B: int, H: int, d: int, device="cuda") -> torch.Tensor:
     """Zero state of the gated recurrence: fp32 [B, H, d]."""
     return torch.zeros((B, H, d), dtype=torch.float32, device=device)
-
-
-def _state_shape(shape):
-    return (shape[0], shape[1], shape[3]) if len(shape) == 4 else (shape[0], shape[2])
 
 
 def fwd_gated_scan(X, G, h0=None, O=None, hT=None, dev_status=None, stream=None):
@@ -123,22 +128,20 @@ def fwd_gated_scan(X, G, h0=None, O=None, hT=None, dev_status=None, stream=None)
     fp32.  A gate of minus infinity starts a new sequence; G = 0 with X = 0
     carries the state over padding.  O may be X or G, hT may be h0."""
     what = "favor_fwd_gated_scan"
-    B, H, L, d, shape = _sizes(what, "X", X)
-    dev, dt = X.device, X.dtype
+    B, H, L, d, dt, dev = _sizes(what, "X", X)
+    shape = X.shape
+    state = (B, H, d) if len(shape) == 4 else (B, d)
     made = []
     if O is None:
         O = torch.empty_like(X)
         made.append(O)
     if hT is None:
-        hT = torch.empty(_state_shape(shape), dtype=torch.float32, device=dev)
+        hT = X.new_empty(state, dtype=torch.float32)
         made.append(hT)
-    xp, xs = _tensor(what, "X", X, shape, dt, dev)
-    gp, gs = _tensor(what, "G", G, shape, dt, dev)
-    op, os_ = _tensor(what, "O", O, shape, dt, dev)
-    state = _state_shape(shape)
-    _run(what, dev, stream, (xp, xs, gp, gs, op, os_, _flat(what, "h0", h0, state, dev),
-                             _flat(what, "hT", hT, state, dev), B, H, L, d, _DT[dt],
-                             _status(what, dev_status, dev)), made)
+    _call(what, dev, stream, made,
+          (*_view(what, "X", X, shape, dt, dev), *_view(what, "G", G, shape, dt, dev),
+           *_view(what, "O", O, shape, dt, dev), _flat(what, "h0", h0, state, dev), _flat(what, "hT", hT, state, dev),
+           B, H, L, d, _DT[dt], _status(what, dev_status, dev)))
     return O, hT
 
 
@@ -148,9 +151,9 @@ def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, dev_
     be dO, dG may be G, dh0 may be dhT.  For a gate broadcast over an axis sum
     dG over it."""
     what = "favor_bwd_gated_scan"
-    B, H, L, d, shape = _sizes(what, "G", G)
-    dev, dt = G.device, G.dtype
-    state = _state_shape(shape)
+    B, H, L, d, dt, dev = _sizes(what, "G", G)
+    shape = G.shape
+    state = (B, H, d) if len(shape) == 4 else (B, d)
     made = []
     if dX is None:
         dX = torch.empty_like(dO)
@@ -159,14 +162,14 @@ def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, dev_
         dG = torch.empty_like(G)
         made.append(dG)
     if dh0 is None:
-        dh0 = torch.empty(state, dtype=torch.float32, device=dev)
+        dh0 = G.new_empty(state, dtype=torch.float32)
         made.append(dh0)
-    args = []
-    for name, t in (("G", G), ("O", O), ("dO", dO), ("dX", dX), ("dG", dG)):
-        args += _tensor(what, name, t, shape, dt, dev)
-    args += [_flat(what, "h0", h0, state, dev), _flat(what, "dhT", dhT, state, dev),
-             _flat(what, "dh0", dh0, state, dev), B, H, L, d, _DT[dt], _status(what, dev_status, dev)]
-    _run(what, dev, stream, args, made)
+    _call(what, dev, stream, made,
+          (*_view(what, "G", G, shape, dt, dev), *_view(what, "O", O, shape, dt, dev),
+           *_view(what, "dO", dO, shape, dt, dev), *_view(what, "dX", dX, shape, dt, dev),
+           *_view(what, "dG", dG, shape, dt, dev), _flat(what, "h0", h0, state, dev),
+           _flat(what, "dhT", dhT, state, dev), _flat(what, "dh0", dh0, state, dev), B, H, L, d, _DT[dt],
+           _status(what, dev_status, dev)))
     return dX, dG, dh0
 
 
@@ -175,24 +178,21 @@ def gated_scan_step(x, g, state, o=None, new_state=None, stream=None):
     exp(g) state + x to new_state (None: in place) and returns (o, new_state),
     o the new state in x's dtype."""
     what = "favor_gated_scan_step"
-    if not x.is_cuda or x.dtype not in _DT or x.dim() != 3:
+    dt, shape, dev = x.dtype, x.shape, x.get_device()
+    if dev < 0 or dt not in _DT or len(shape) != 3:
         raise FavorError(f"{what}: x must be an fp32 or bf16 CUDA tensor [B, H, d]")
-    shape = tuple(x.shape)
-    dev, dt = x.device, x.dtype
-    if min(shape) < 1:
-        raise FavorError(f"{what}: x has an empty axis: {list(shape)}")
+    B, H, d = shape
+    if B < 1 or H < 1 or d < 1 or B > _INT or H > _INT or d > _INT:
+        raise FavorError(f"{what}: x has an empty or oversized axis: {list(shape)}")
     made = ()
     if o is None:
-        o = torch.empty_like(x, memory_format=torch.contiguous_format)
+        o = x.new_empty(shape)
         made = (o,)
-    new_state = state if new_state is None else new_state
-    ptrs = []
-    for name, t in (("x", x), ("g", g), ("o", o)):
-        if t.dtype != dt or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise FavorError(f"{what}: {name} must be a contiguous {dt} tensor {list(shape)} on {dev}")
-        ptrs.append(t.data_ptr())
-    _run(what, dev, stream, (*ptrs, _flat(what, "state", state, shape, dev),
-                             _flat(what, "new_state", new_state, shape, dev), *shape, _DT[dt]), made)
+    if new_state is None:
+        new_state = state
+    _call(what, dev, stream, made,
+          (_flat(what, "x", x, shape, dev, dt), _flat(what, "g", g, shape, dev, dt), _flat(what, "o", o, shape, dev, dt),
+           _flat(what, "state", state, shape, dev), _flat(what, "new_state", new_state, shape, dev), B, H, d, _DT[dt]))
     return o, new_state
 
 
@@ -201,23 +201,25 @@ def fwd_layer_norm(X, gamma=None, beta=None, eps=1e-5, Y=None, stream=None):
     (fp32 [d], None: 1 and 0).  Returns Y, contiguous where none is given (as
     the attention takes it); Y may be X."""
     what = "favor_fwd_layer_norm"
-    B, H, L, d, shape = _sizes(what, "X", X)
-    dev, dt = X.device, X.dtype
+    B, H, L, d, dt, dev = _sizes(what, "X", X)
+    shape = X.shape
     made = ()
     if Y is None:
-        Y = torch.empty(shape, dtype=dt, device=dev)
+        Y = X.new_empty(shape)
         made = (Y,)
-    xp, xs = _tensor(what, "X", X, shape, dt, dev)
-    yp, ys = _tensor(what, "Y", Y, shape, dt, dev)
-    _run(what, dev, stream, (xp, xs, yp, ys, _flat(what, "gamma", gamma, (d,), dev),
-                             _flat(what, "beta", beta, (d,), dev), float(eps), B, H, L, d, _DT[dt]), made)
+    _call(what, dev, stream, made,
+          (*_view(what, "X", X, shape, dt, dev), *_view(what, "Y", Y, shape, dt, dev),
+           _flat(what, "gamma", gamma, (d,), dev), _flat(what, "beta", beta, (d,), dev), eps, B, H, L, d, _DT[dt]))
     return Y
 
 
 def bwd_layer_norm_workspace_bytes(B: int, H: int, L: int, d: int, dtype) -> int:
-    if min(B, H, L, d) < 1 or d > _NORM_MAX_D or B * H * L >= 1 << 31:
+    n = 0
+    if min(B, H, L, d) > 0 and max(B, H, L, d) <= _INT:
+        n = load().favor_bwd_layer_norm_workspace_bytes(B, H, L, d, _DT[dtype])
+    if n == 0:
         raise FavorError("unsupported shape")
-    return load().favor_bwd_layer_norm_workspace_bytes(B, H, L, d, _DT[dtype])
+    return n
 
 
 def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None, workspace=None, stream=None,
@@ -226,36 +228,34 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
     dgamma and dbeta are fp32 [d], summed over all rows; weight_grads=False
     leaves them out (None, None).  dX may be dY or X."""
     what = "favor_bwd_layer_norm"
-    B, H, L, d, shape = _sizes(what, "X", X)
-    dev, dt = X.device, X.dtype
+    B, H, L, d, dt, dev = _sizes(what, "X", X)
+    shape = X.shape
     made = []
     if dX is None:
-        dX = torch.empty(shape, dtype=dt, device=dev)
+        dX = X.new_empty(shape)
         made.append(dX)
-    need = 0
     if weight_grads:
-        need = bwd_layer_norm_workspace_bytes(B, H, L, d, dt)
         if dgamma is None:
-            dgamma = torch.empty(d, dtype=torch.float32, device=dev)
+            dgamma = X.new_empty(d, dtype=torch.float32)
             made.append(dgamma)
         if dbeta is None:
-            dbeta = torch.empty(d, dtype=torch.float32, device=dev)
+            dbeta = X.new_empty(d, dtype=torch.float32)
             made.append(dbeta)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if workspace is None:
+            workspace = X.new_empty(bwd_layer_norm_workspace_bytes(B, H, L, d, dt), dtype=torch.uint8)
             made.append(workspace)
     elif dgamma is not None or dbeta is not None:
         raise FavorError(f"{what}: dgamma or dbeta given with weight_grads=False")
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise FavorError(f"{what}: the workspace must be contiguous on {dev}")
-    args = []
-    for name, t in (("X", X), ("dY", dY), ("dX", dX)):
-        args += _tensor(what, name, t, shape, dt, dev)
-    args += [_flat(what, "gamma", gamma, (d,), dev), _flat(what, "dgamma", dgamma, (d,), dev),
-             _flat(what, "dbeta", dbeta, (d,), dev), float(eps), B, H, L, d, _DT[dt],
-             workspace.data_ptr() if workspace is not None else None,
-             workspace.numel() * workspace.element_size() if workspace is not None else 0]
-    _run(what, dev, stream, args, made)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise FavorError(f"{what}: the workspace must be contiguous on cuda:{dev}")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(what, dev, stream, made,
+          (*_view(what, "X", X, shape, dt, dev), *_view(what, "dY", dY, shape, dt, dev),
+           *_view(what, "dX", dX, shape, dt, dev), _flat(what, "gamma", gamma, (d,), dev),
+           _flat(what, "dgamma", dgamma, (d,), dev), _flat(what, "dbeta", dbeta, (d,), dev), eps, B, H, L, d, _DT[dt],
+           ws, nbytes))
     return dX, dgamma, dbeta
 
 
@@ -289,41 +289,37 @@ def _sections(sections):
 
 
 def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
-    B, Hq, L, d, shape = _sizes(what, "Q", Q, (4,))
-    dev, dt = Q.device, Q.dtype
-    sections, c_sections, pairs = _sections(tuple(sections))
-    if pairing not in PAIRINGS:
+    B, Hq, L, d, dt, dev = _sizes(what, "Q", Q, True)
+    sections, c_sections, pairs = _sections(sections if type(sections) is tuple else tuple(sections))
+    pairing = PAIRINGS.get(pairing)
+    if pairing is None:
         raise FavorError(f"{what}: pairing must be one of {sorted(PAIRINGS)}")
-    if 2 * pairs > d:
-        raise FavorError(f"{what}: {pairs} pairs do not fit {d} channels")
     n = len(sections)
-    ps = tuple(pos.shape)
-    if (pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous()
-            or ps not in ((n, B, L), (n, 1, L))):
-        raise FavorError(f"{what}: positions must be contiguous int32 [{n}, {B} or 1, {L}] on {dev}")
-    if table.dtype != torch.int64 or table.device != dev or tuple(table.shape) != (pairs,) \
-            or not table.is_contiguous():
-        raise FavorError(f"{what}: the table must be contiguous int64 [{pairs}] on {dev} (new_rotary_table)")
+    if (pos.dtype is not torch.int32 or pos.get_device() != dev or not pos.is_contiguous()
+            or (pos.shape != (n, B, L) and pos.shape != (n, 1, L))):
+        raise FavorError(f"{what}: positions must be contiguous int32 [{n}, {B} or 1, {L}] on cuda:{dev}")
     made = []
     if Qo is None:
-        Qo = torch.empty(shape, dtype=dt, device=dev)
+        Qo = Q.new_empty(Q.shape)
         made.append(Qo)
-    args = [*_tensor(what, "Q", Q, shape, dt, dev), *_tensor(what, "its output", Qo, shape, dt, dev)]
+    views = (*_view(what, "Q", Q, Q.shape, dt, dev), *_view(what, "Q's output", Qo, Q.shape, dt, dev))
     Hk = 0
     if K is not None:
-        Hk, kshape = K.shape[1] if K.dim() == 4 else 0, (B, K.shape[1] if K.dim() == 4 else 0, L, d)
-        if Hk < 1:
+        Hk = K.shape[1] if K.dim() == 4 else 0
+        if Hk < 1 or Hk > _INT:
             raise FavorError(f"{what}: K must be [B, Hk, L, d]")
+        shape = (B, Hk, L, d)
         if Ko is None:
-            Ko = torch.empty(kshape, dtype=dt, device=dev)
+            Ko = K.new_empty(shape)
             made.append(Ko)
-        args += [*_tensor(what, "K", K, kshape, dt, dev), *_tensor(what, "its output", Ko, kshape, dt, dev)]
+        views += (*_view(what, "K", K, shape, dt, dev), *_view(what, "K's output", Ko, shape, dt, dev))
+    elif Ko is None:
+        views += (None, None, None, None)
     else:
-        if Ko is not None:
-            raise FavorError(f"{what}: an output for keys without keys")
-        args += [None] * 4
-    args += [B, Hq, Hk, L, d, pos.data_ptr(), ps[1], n, c_sections, table.data_ptr(), PAIRINGS[pairing], _DT[dt]]
-    _run(what, dev, stream, args, made)
+        raise FavorError(f"{what}: an output for keys without keys")
+    _call(what, dev, stream, made,
+          (*views, B, Hq, Hk, L, d, pos.data_ptr(), pos.shape[1], n, c_sections,
+           _flat(what, "the table (new_rotary_table)", table, (pairs,), dev, torch.int64), pairing, _DT[dt]))
     return Qo, Ko
 
 
