@@ -25,6 +25,7 @@ PAIRINGS = {"adjacent": 0, "halves": 1}              # favor_pairing
 MAX_AXES = 4
 _S3 = ctypes.c_int64 * 3
 _INT = (1 << 31) - 1
+_PLAIN = torch.contiguous_format
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # None: a torch without CUDA
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
@@ -136,7 +137,7 @@ def fwd_gated_scan(X, G, h0=None, O=None, hT=None, dev_status=None, stream=None)
         O = torch.empty_like(X)
         made.append(O)
     if hT is None:
-        hT = X.new_empty(state, dtype=torch.float32)
+        hT = torch.empty(state, dtype=torch.float32, device=X.device)
         made.append(hT)
     _call(what, dev, stream, made,
           (*_view(what, "X", X, shape, dt, dev), *_view(what, "G", G, shape, dt, dev),
@@ -162,7 +163,7 @@ def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, dev_
         dG = torch.empty_like(G)
         made.append(dG)
     if dh0 is None:
-        dh0 = G.new_empty(state, dtype=torch.float32)
+        dh0 = torch.empty(state, dtype=torch.float32, device=G.device)
         made.append(dh0)
     _call(what, dev, stream, made,
           (*_view(what, "G", G, shape, dt, dev), *_view(what, "O", O, shape, dt, dev),
@@ -186,7 +187,7 @@ def gated_scan_step(x, g, state, o=None, new_state=None, stream=None):
         raise FavorError(f"{what}: x has an empty or oversized axis: {list(shape)}")
     made = ()
     if o is None:
-        o = x.new_empty(shape)
+        o = torch.empty_like(x, memory_format=_PLAIN)
         made = (o,)
     if new_state is None:
         new_state = state
@@ -205,7 +206,7 @@ def fwd_layer_norm(X, gamma=None, beta=None, eps=1e-5, Y=None, stream=None):
     shape = X.shape
     made = ()
     if Y is None:
-        Y = X.new_empty(shape)
+        Y = torch.empty_like(X, memory_format=_PLAIN)
         made = (Y,)
     _call(what, dev, stream, made,
           (*_view(what, "X", X, shape, dt, dev), *_view(what, "Y", Y, shape, dt, dev),
@@ -232,17 +233,17 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
     shape = X.shape
     made = []
     if dX is None:
-        dX = X.new_empty(shape)
+        dX = torch.empty_like(X, memory_format=_PLAIN)
         made.append(dX)
     if weight_grads:
         if dgamma is None:
-            dgamma = X.new_empty(d, dtype=torch.float32)
+            dgamma = torch.empty(d, dtype=torch.float32, device=X.device)
             made.append(dgamma)
         if dbeta is None:
-            dbeta = X.new_empty(d, dtype=torch.float32)
+            dbeta = torch.empty(d, dtype=torch.float32, device=X.device)
             made.append(dbeta)
         if workspace is None:
-            workspace = X.new_empty(bwd_layer_norm_workspace_bytes(B, H, L, d, dt), dtype=torch.uint8)
+            workspace = torch.empty(bwd_layer_norm_workspace_bytes(B, H, L, d, dt), dtype=torch.uint8, device=X.device)
             made.append(workspace)
     elif dgamma is not None or dbeta is not None:
         raise FavorError(f"{what}: dgamma or dbeta given with weight_grads=False")
@@ -300,7 +301,7 @@ def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
         raise FavorError(f"{what}: positions must be contiguous int32 [{n}, {B} or 1, {L}] on cuda:{dev}")
     made = []
     if Qo is None:
-        Qo = Q.new_empty(Q.shape)
+        Qo = torch.empty_like(Q, memory_format=_PLAIN)
         made.append(Qo)
     views = (*_view(what, "Q", Q, Q.shape, dt, dev), *_view(what, "Q's output", Qo, Q.shape, dt, dev))
     Hk = 0
@@ -310,7 +311,7 @@ def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
             raise FavorError(f"{what}: K must be [B, Hk, L, d]")
         shape = (B, Hk, L, d)
         if Ko is None:
-            Ko = K.new_empty(shape)
+            Ko = torch.empty_like(K, memory_format=_PLAIN)
             made.append(Ko)
         views += (*_view(what, "K", K, shape, dt, dev), *_view(what, "K's output", Ko, shape, dt, dev))
     elif Ko is None:
