@@ -10,6 +10,13 @@
 // shared memory (48 to 64 KB in flight per SM, which registers alone could not
 // hold), while gamma and beta, and in the backward pass the columns' sums,
 // stay in registers.
+//
+// Measured (one GB300; copy rate 6770 GB/s): 65536 x 16 rows of 128 bf16 94 us
+// forward, 5.7 TB/s (97 us out of a [B, L, 3, H, d] buffer), 127 us backward,
+// 6.3 TB/s; 32768 rows of 512 fp32 23.8 and 36.8 us, 5.6 and 5.5 TB/s.  Rows
+// whose pointers or strides are no multiples of 16 bytes go element by
+// element: 16384 x 16 rows of 128 bf16 59.6 against 29.8 us.  Small calls are
+// bound by their launches (8 rows of 512: 3.2 us; backward of 64: 6.0).
 #include <algorithm>
 
 #include "ops.cuh"
@@ -418,7 +425,7 @@ Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
   if (pieces <= 32 * per) {
     // as many values a thread as there may be: what a row costs beside them (its
     // address, sums over lanes, root) is then shared by the most of them.  16
-    // values against 8 (65536 x 16 rows of 128 bf16): FWD16 against FWD8 us.
+    // values against 8 (65536 x 16 rows of 128 bf16): 94 against 126 us.
     p.lanes = 4;
     while (p.lanes < 32 && p.lanes * per < pieces) p.lanes *= 2;
     p.threads = 32 * kWarps;
@@ -426,7 +433,7 @@ Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
     nv = (pieces + p.lanes - 1) / p.lanes;
   } else {
     // element by element a thread gets through fewer of them: 4 while 256 threads
-    // hold the row (3333 rows of 771 fp32, backward: ODD4 us, with 16 ODD16)
+    // hold the row (3333 rows of 771 fp32, backward: 19.4 us, with 16 values 23.2)
     const int most = vw == 1 && pieces <= 256 * 4 ? 4 : per;
     p.threads = p.lanes = ((pieces + most - 1) / most + 31) / 32 * 32;
     p.groups = 1;
@@ -437,7 +444,8 @@ Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
   const int resident = backward ? (p.threads <= 256 && nv * vw <= 4 ? 1024 : 512) : many ? 1024 : 768;
   const int64_t per_sm = std::max(1, resident / p.threads);
   int64_t ctas = std::min<int64_t>((rows + p.groups - 1) / p.groups, per_sm * sm_count());
-  // every CTA's sums are added up after: rows enough for each to make that little
+  // every CTA's sums are added up after: rows enough for each to make that
+  // little (3333 rows in 1216 CTAs of 64 threads: 23 us, 10 of them that)
   if (backward) ctas = std::min(ctas, std::max<int64_t>(2 * sm_count(), rows / (8 * p.groups)));
   p.ctas = (int)ctas;
   return p;

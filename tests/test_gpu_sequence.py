@@ -6,13 +6,18 @@ evaluation (``*_bound``), plus half a step of the storage type (2^-24 of the
 value for fp32, 2^-8 for bf16), plus the smallest normal number of the type.
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import oracle as orc
-import workloads as wl
 from helpers import to_np
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 pytestmark = pytest.mark.gpu
 
@@ -544,6 +549,35 @@ def test_two_graphs_share_a_workspace(cuda_lib):
     graphs[0].replay()
     for x, y in zip(want[1], outs[0]):
         assert torch.equal(x, y)
+
+
+def test_first_calls_under_capture(cuda_lib):
+    # a process whose first call of each operator is made while a graph is captured
+    code = """
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import linear_softmax_attention_gb300 as f
+x = torch.randn((2, 4, 1500, 64), device="cuda").to(torch.bfloat16)
+g = -x.abs()
+w = torch.ones(64, device="cuda")
+pos = torch.arange(1500, device="cuda", dtype=torch.int32).view(1, 1, -1)
+table = f.new_rotary_table((32,))
+def calls():
+    h, hT = f.fwd_gated_scan(x, g)
+    return [h, hT, *f.bwd_gated_scan(g, x, x), f.fwd_layer_norm(x, w), *f.bwd_layer_norm(x, x, w),
+            *f.fwd_rotary(x, x, pos, table, (32,))]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, calls()))
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_refusals_of_the_binding(cuda_lib):
