@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 8;             // of a CTA that shares its rows out by groups of lanes
 constexpr int kMaxValues = 16;        // of a row in one thread
-constexpr int kSumRows = 16, kSumThreads = 32 * kSumRows;
+constexpr int kSumRows = 32, kSumThreads = 32 * kSumRows;
 
 // VW values side by side: 16 bytes, or one element
 template <typename T, int VW> struct Piece;
@@ -211,14 +211,48 @@ __device__ __forceinline__ float centre(float (&x)[NV][VW], int lane, int lanes,
   return v2.x + v2.y;
 }
 
+// VW fp32 values at p, by 16 bytes where they lie so
+template <int VW>
+__device__ __forceinline__ void load_values(float (&w)[VW], const float* p, bool by16) {
+  if constexpr (VW >= 4) {
+    if (by16) {
+#pragma unroll
+      for (int i = 0; i < VW; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + i);
+        w[i] = v.x;
+        w[i + 1] = v.y;
+        w[i + 2] = v.z;
+        w[i + 3] = v.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VW; ++i) w[i] = p[i];
+}
+template <int VW>
+__device__ __forceinline__ void store_values(float* p, const float (&w)[VW]) {   // 16-byte aligned where VW >= 4
+  if constexpr (VW >= 4) {
+#pragma unroll
+    for (int i = 0; i < VW; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VW; ++i) p[i] = w[i];
+  }
+}
 template <int VW, int NV>
 __device__ __forceinline__ void load_weights(float (&w)[NV][VW], const float* p, int lane, int lanes, int d,
                                              float none) {
+  const bool by16 = reinterpret_cast<uintptr_t>(p) % 16 == 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (j * lanes + lane) * VW;
+    if (p != nullptr && c < d) {
+      load_values<VW>(w[j], p + c, by16);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VW; ++i) w[j][i] = p != nullptr && c < d ? p[c + i] : none;
+      for (int i = 0; i < VW; ++i) w[j][i] = none;
+    }
   }
 }
 
@@ -347,50 +381,37 @@ __global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : N
   if (part == nullptr) return;
   // the kernel that adds the CTAs' sums may take its place and wait
   asm volatile("griddepcontrol.launch_dependents;");
-  if constexpr (CTA == 0) {
-    // the groups' sums, halved until the first group has them all: [groups / 2][2][d]
-    // in the ring's place
-    float* sums = ring;
-    const int me = threadIdx.x / lanes;
-    for (int half = plan.groups >> 1; half > 0; half >>= 1) {
-      __syncthreads();
-      if (me >= half && me < 2 * half)
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < VW; ++i) {
-            const int c = (j * lanes + lane) * VW + i;
-            if (c < p.d) {
-              sums[(me - half) * 2 * p.d + c] = dw[j][i];
-              sums[(me - half) * 2 * p.d + p.d + c] = dz[j][i];
-            }
-          }
-      __syncthreads();
-      if (me < half)
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < VW; ++i) {
-            const int c = (j * lanes + lane) * VW + i;
-            if (c < p.d) {
-              dw[j][i] += sums[me * 2 * p.d + c];
-              dz[j][i] += sums[me * 2 * p.d + p.d + c];
-            }
-          }
-    }
-    if (me > 0) return;
-  }
   float* out = part + (size_t)blockIdx.x * 2 * p.d;
+  if constexpr (CTA == 0) {
+    // the groups' sums side by side in the ring's place, [groups][2][d], then
+    // added up column by column
+    __syncthreads();
+    float* sums = ring + (threadIdx.x / lanes) * 2 * p.d;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < VW; ++i) {
-      const int c = (j * lanes + lane) * VW + i;
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * lanes + lane) * VW;
       if (c < p.d) {
-        out[c] = dw[j][i];
-        out[p.d + c] = dz[j][i];
+        store_values<VW>(sums + c, dw[j]);
+        store_values<VW>(sums + p.d + c, dz[j]);
       }
     }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.d; c += blockDim.x) {
+      float v = ring[c];
+#pragma unroll 8
+      for (int g = 1; g < plan.groups; ++g) v += ring[g * 2 * p.d + c];
+      out[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * lanes + lane) * VW;
+      if (c < p.d) {
+        store_values<VW>(out + c, dw[j]);
+        store_values<VW>(out + p.d + c, dz[j]);
+      }
+    }
+  }
 }
 
 // The CTAs' sums in their order: a block per 32 columns of [2 d]
@@ -494,7 +515,7 @@ cudaError_t fwd(Kind<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint3
 template <typename T, int VW, int NV, int CTA>
 cudaError_t bwd(Kind<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint32_t n, const Plan& plan, float* part,
                 cudaStream_t stream) {
-  const size_t sums = CTA == 0 ? (size_t)(plan.groups / 2) * 2 * a.d * sizeof(float) : 0;
+  const size_t sums = CTA == 0 ? (size_t)plan.groups * 2 * a.d * sizeof(float) : 0;
   const size_t smem = std::max(Ahead<T, VW, NV, 2>::kBytes * plan.threads, sums);
   const auto kernel = norm_bwd_kernel<T, VW, NV, CTA>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
