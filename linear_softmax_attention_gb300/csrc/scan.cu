@@ -36,10 +36,8 @@
 namespace favor {
 namespace {
 
-constexpr int kMaxWarps = 8;          // warps of a CTA
 constexpr int kMaxCluster = 16;       // CTAs of a cluster
 constexpr int kFold = 4;              // maps read together while they are joined
-constexpr int kRun = 8;               // tokens of a run
 constexpr int kStages = 3;            // runs of a warp in its ring
 constexpr int kStepThreads = 128;
 
@@ -168,10 +166,10 @@ __device__ __forceinline__ void send(uint32_t at, const Map& m, uint32_t bar) {
                : "memory");
 }
 
-template <int V>
+template <int V, int MW>
 struct Joint {
-  Map warp[2][V][kMaxWarps][32];      // the runs' maps, from the workers
-  float in[2][V][kMaxWarps][32];      // the state before each run, to the workers
+  Map warp[2][V][MW][32];      // the runs' maps, from the workers
+  float in[2][V][MW][32];      // the state before each run, to the workers
   uint64_t bar[2][V];
   int abort_flag;
 };
@@ -193,8 +191,8 @@ constexpr int kBarMaps = 1, kBarStates = 3;
 // sends its map of step n + 2 only when it has every CTA's of step n + 1,
 // which they send after their reads of step n.  cta: the CTAs' maps,
 // [2][V][K][32].  Returns the state behind the last step.
-template <int V>
-__device__ float join(Joint<V>& sm, Map (*cta)[32], int v, int steps, int K, int W, int rank, int lane, float carry,
+template <int V, int MW>
+__device__ float join(Joint<V, MW>& sm, Map (*cta)[32], int v, int steps, int K, int W, int rank, int lane, float carry,
                       const tc::WaitCtx& ctx) {
   const uint32_t me = tc::smem_addr(&sm);
   const uint32_t peer = K > 1 && lane < K ? tc::map_to_rank(me, lane) : 0;
@@ -205,21 +203,21 @@ __device__ float join(Joint<V>& sm, Map (*cta)[32], int v, int steps, int K, int
     uint64_t* const bar = &sm.bar[buf][v];
     if (K > 1 && lane == 0) tc::mbar_arrive_expect_tx(bar, K * 32 * (int)sizeof(Map));
     bar_sync(kBarMaps + buf, threads);
-    Map m[kMaxWarps];
+    Map m[MW];
 #pragma unroll
-    for (int w = 0; w < kMaxWarps; ++w)
+    for (int w = 0; w < MW; ++w)
       if (w < W) m[w] = sm.warp[buf][v][w][lane];
     float h = carry;
     if (K > 1) {
       Map total = m[0];
 #pragma unroll
-      for (int w = 1; w < kMaxWarps; ++w)
+      for (int w = 1; w < MW; ++w)
         if (w < W) total = then(total, m[w]);
       // 0 times an infinity or NaN is NaN and stays so: only then are closed gates looked for
       if (!(finite(total.s) && finite(total.A))) {
         total = m[0];
 #pragma unroll
-        for (int w = 1; w < kMaxWarps; ++w)
+        for (int w = 1; w < MW; ++w)
           if (w < W) total = then_checked(total, m[w]);
       }
       const uint32_t at = tc::smem_addr(&there[rank][lane]) - me, bar_at = tc::smem_addr(bar) - me;
@@ -258,7 +256,7 @@ __device__ float join(Joint<V>& sm, Map (*cta)[32], int v, int steps, int K, int
     }
     const float first = h;
 #pragma unroll
-    for (int w = 0; w < kMaxWarps; ++w)
+    for (int w = 0; w < MW; ++w)
       if (w < W) {
         sm.in[buf][v][w][lane] = h;
         h = fmaf(m[w].A, h, m[w].s);
@@ -266,7 +264,7 @@ __device__ float join(Joint<V>& sm, Map (*cta)[32], int v, int steps, int K, int
     if (!finite(h)) {
       h = first;
 #pragma unroll
-      for (int w = 0; w < kMaxWarps; ++w)
+      for (int w = 0; w < MW; ++w)
         if (w < W) {
           sm.in[buf][v][w][lane] = h;
           h = through(m[w], h);
@@ -300,13 +298,13 @@ __device__ __forceinline__ Lane find_lane(const ScanArgs& p, int V, uint32_t slo
 // t = L - 1 - u).  S: stages of the ring; C: bytes of a copy into it, 16 (four
 // lanes' channels at once), 4 (a lane's own) or 2 (which no asynchronous copy
 // takes: loads that wait in registers until the next fetch).
-template <typename T, int V, int R, int S, int C, bool BACK>
-__global__ void __launch_bounds__((kMaxWarps + V) * 32, 2) scan_kernel(ScanArgs p, uint32_t slots, int K, int W) {
+template <typename T, int V, int MW, int R, int S, int C, bool BACK>
+__global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint32_t slots, int K, int W) {
   using P = Piece<T, V>;
   using Raw = typename P::Raw;
   constexpr int N = BACK ? 3 : 2;
   constexpr int M = C / (int)sizeof(Raw);             // lanes of a copy
-  __shared__ Joint<V> sm;
+  __shared__ Joint<V, MW> sm;
   extern __shared__ __align__(16) unsigned char ring_bytes[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = K > 1 ? (int)tc::cluster_ctarank() : 0;
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__((kMaxWarps + V) * 32, 2) scan_kernel(ScanArgs 
   }
   if (warp >= W) {                                    // there are no such warps where W = 1
     const int v = warp - W;
-    const float carry = join<V>(sm, reinterpret_cast<Map(*)[32]>(ring_bytes), v, steps, K, W, rank, lane, first,
+    const float carry = join<V, MW>(sm, reinterpret_cast<Map(*)[32]>(ring_bytes), v, steps, K, W, rank, lane, first,
                                 tc::WaitCtx{&sm.abort_flag, p.status});
     // tokens behind the last one are identities: carry is the state after it
     if (p.last != nullptr && rank == 0 && ln.valid) p.last[ch + v] = carry;
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__((kMaxWarps + V) * 32, 2) scan_kernel(ScanArgs 
   const int lo = (int)(BACK ? p.dxs.l : p.hs.l), lo2 = (int)p.dgs.l;
 
   Raw* ring = reinterpret_cast<Raw*>(ring_bytes + (K > 1 ? 2 * V * K * 32 * sizeof(Map) : 0)) + threadIdx.x;
-  constexpr int kRow = kMaxWarps * 32;                // a constant, so that a run's words have constant offsets
+  constexpr int kRow = MW * 32;                // a constant, so that a run's words have constant offsets
   auto place = [&](int stage, int n, int i) -> Raw* { return ring + stage * (N * R * kRow) + (n * R + i) * kRow; };
   Raw waiting[C == 2 ? N : 1][R];
   int waiting_stage = -1;
@@ -582,20 +580,20 @@ cudaError_t ask_fits(Fits* fits, const void* kernel, int threads, F&& bytes) {
   return cudaSuccess;
 }
 
-template <typename T, int V, int C, bool BACK>
+template <typename T, int V, int MW, int R, int C, bool BACK>
 cudaError_t go(const ScanArgs& a, cudaStream_t stream) {
-  constexpr int R = kRun, S = kStages;
-  const auto kernel = scan_kernel<T, V, R, S, C, BACK>;
+  constexpr int S = kStages;
+  const auto kernel = scan_kernel<T, V, MW, R, S, C, BACK>;
   const void* id = reinterpret_cast<const void*>(kernel);
   const int64_t slots = (int64_t)a.B * a.H * (a.d / V), tiles = (slots + 31) / 32;
   const int64_t runs = ((int64_t)a.L + R - 1) / R;
   int W = 1, K = 1;
-  while (W < kMaxWarps && W < runs) W *= 2;
-  constexpr size_t ring = (size_t)S * (BACK ? 3 : 2) * R * kMaxWarps * 32 * sizeof(typename Piece<T, V>::Raw);
+  while (W < MW && W < runs) W *= 2;
+  constexpr size_t ring = (size_t)S * (BACK ? 3 : 2) * R * MW * 32 * sizeof(typename Piece<T, V>::Raw);
   auto bytes = [](int k) { return ring + (k > 1 ? 2 * V * k * 32 * sizeof(Map) : 0); };
   cudaError_t e = ensure_dynamic_smem(id, bytes(kMaxCluster));
   if (e != cudaSuccess) return e;
-  if (runs > kMaxWarps) {
+  if (runs > MW) {
     // CTAs of a cluster: a wave of clusters of K takes time as 1 / K.  The
     // smallest K whose waves take at most a tenth longer than the best's: at
     // 32 tiles of 8192 tokens (bf16 forward) K = 8 takes 25.8 us, K = 4 29.4
@@ -651,9 +649,22 @@ cudaError_t go(const ScanArgs& a, bool bf16, int align, cudaStream_t stream) {
   // made of whole pairs, else one by one.  4 x 8 heads x 8192 x 64 bf16
   // forward: 26.0, 32.1 and 48.7 us; fp32 38.4 and 51.5; 2 x 8 x 12288 x 64
   // bf16 backward: 34.0, 45.8 and 58.7.
-  if (!bf16) return align >= 16 ? go<float, 1, 16, BACK>(a, stream) : go<float, 1, 4, BACK>(a, stream);
-  if (align >= 4) return align >= 16 ? go<B16, 2, 16, BACK>(a, stream) : go<B16, 2, 4, BACK>(a, stream);
-  return go<B16, 1, 2, BACK>(a, stream);
+  // Workers of a CTA and tokens of a run.  Longer runs share what a run costs
+  // among more tokens, as far as two runs' gates stay in registers: forward
+  // 4 x 16 against 8 x 8 bf16 24.9 against 26.9 us (4 x 8 x 8192 x 64), 4 x 24
+  // against 8 x 8 fp32 238 against 264 us (65536 x 2048; 4 x 28 247).  The
+  // backward pass, with three arrays in its ring, spills at 16 and keeps 8 x 8
+  // (bf16, 2 x 8 x 12288 x 64: 34.0 us, 4 x 16 35.1, 4 x 12 34.9).
+  if constexpr (BACK) {
+    if (!bf16) return align >= 16 ? go<float, 1, 8, 8, 16, BACK>(a, stream) : go<float, 1, 8, 8, 4, BACK>(a, stream);
+    if (align >= 4)
+      return align >= 16 ? go<B16, 2, 8, 8, 16, BACK>(a, stream) : go<B16, 2, 8, 8, 4, BACK>(a, stream);
+  } else {
+    if (!bf16) return align >= 16 ? go<float, 1, 4, 24, 16, BACK>(a, stream) : go<float, 1, 4, 24, 4, BACK>(a, stream);
+    if (align >= 4)
+      return align >= 16 ? go<B16, 2, 4, 16, 16, BACK>(a, stream) : go<B16, 2, 4, 16, 4, BACK>(a, stream);
+  }
+  return go<B16, 1, 8, 8, 2, BACK>(a, stream);
 }
 
 }  // namespace
