@@ -52,26 +52,37 @@ def declare(lib):
 # little: device indexes instead of devices, the raw handle of the current
 # stream instead of a Stream object.
 
-def _view(what, name, t, shape, dtype, index):
-    """Pointer and strides (None: contiguous) of a view [B, H, L, d] or [B, L, d]."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
-        raise FavorError(f"{what}: {name} must be a {dtype} tensor {list(shape)} on cuda:{index}, "
-                         f"not {t.dtype} {list(t.shape)} on {t.device}")
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise FavorError(f"{what}: {name} must have a unit stride along its last axis")
-    return t.data_ptr(), (_S3(st[0], st[1], st[2]) if len(st) == 4 else _S3(st[0], 0, st[1]))
+def _views(what, names, tensors, shape, dtype, index):
+    """Pointer and strides (None: contiguous) of each view [B, H, L, d] or [B, L, d], in one list."""
+    args = []
+    for t in tensors:
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+            name = names[len(args) // 2]
+            raise FavorError(f"{what}: {name} must be a {dtype} tensor {list(shape)} on cuda:{index}, "
+                             f"not {t.dtype} {list(t.shape)} on {t.device}")
+        args.append(t.data_ptr())
+        if t.is_contiguous():
+            args.append(None)
+            continue
+        st = t.stride()
+        if st[-1] != 1 and shape[-1] > 1:
+            raise FavorError(f"{what}: {names[len(args) // 2]} must have a unit stride along its last axis")
+        args.append(_S3(st[0], st[1], st[2]) if len(st) == 4 else _S3(st[0], 0, st[1]))
+    return args
 
 
-def _flat(what, name, t, shape, index, dtype=torch.float32):
-    """Pointer of a contiguous tensor, None for None."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-        raise FavorError(f"{what}: {name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
-    return t.data_ptr()
+def _flats(what, names, tensors, shape, index, dtype=torch.float32):
+    """Pointers of contiguous tensors of one shape, None for None."""
+    args = []
+    for t in tensors:
+        if t is None:
+            args.append(None)
+        elif t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            raise FavorError(f"{what}: {names[len(args)]} must be a contiguous {dtype} tensor {list(shape)} "
+                             f"on cuda:{index}")
+        else:
+            args.append(t.data_ptr())
+    return args
 
 
 def _status(what, t, index):
@@ -140,8 +151,7 @@ def fwd_gated_scan(X, G, h0=None, O=None, hT=None, dev_status=None, stream=None)
         hT = torch.empty(state, dtype=torch.float32, device=X.device)
         made.append(hT)
     _call(what, dev, stream, made,
-          (*_view(what, "X", X, shape, dt, dev), *_view(what, "G", G, shape, dt, dev),
-           *_view(what, "O", O, shape, dt, dev), _flat(what, "h0", h0, state, dev), _flat(what, "hT", hT, state, dev),
+          (*_views(what, ("X", "G", "O"), (X, G, O), shape, dt, dev), *_flats(what, ("h0", "hT"), (h0, hT), state, dev),
            B, H, L, d, _DT[dt], _status(what, dev_status, dev)))
     return O, hT
 
@@ -166,10 +176,8 @@ def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, dev_
         dh0 = torch.empty(state, dtype=torch.float32, device=G.device)
         made.append(dh0)
     _call(what, dev, stream, made,
-          (*_view(what, "G", G, shape, dt, dev), *_view(what, "O", O, shape, dt, dev),
-           *_view(what, "dO", dO, shape, dt, dev), *_view(what, "dX", dX, shape, dt, dev),
-           *_view(what, "dG", dG, shape, dt, dev), _flat(what, "h0", h0, state, dev),
-           _flat(what, "dhT", dhT, state, dev), _flat(what, "dh0", dh0, state, dev), B, H, L, d, _DT[dt],
+          (*_views(what, ("G", "O", "dO", "dX", "dG"), (G, O, dO, dX, dG), shape, dt, dev),
+           *_flats(what, ("h0", "dhT", "dh0"), (h0, dhT, dh0), state, dev), B, H, L, d, _DT[dt],
            _status(what, dev_status, dev)))
     return dX, dG, dh0
 
@@ -192,8 +200,8 @@ def gated_scan_step(x, g, state, o=None, new_state=None, stream=None):
     if new_state is None:
         new_state = state
     _call(what, dev, stream, made,
-          (_flat(what, "x", x, shape, dev, dt), _flat(what, "g", g, shape, dev, dt), _flat(what, "o", o, shape, dev, dt),
-           _flat(what, "state", state, shape, dev), _flat(what, "new_state", new_state, shape, dev), B, H, d, _DT[dt]))
+          (*_flats(what, ("x", "g", "o"), (x, g, o), shape, dev, dt),
+           *_flats(what, ("state", "new_state"), (state, new_state), shape, dev), B, H, d, _DT[dt]))
     return o, new_state
 
 
@@ -209,8 +217,8 @@ def fwd_layer_norm(X, gamma=None, beta=None, eps=1e-5, Y=None, stream=None):
         Y = torch.empty_like(X, memory_format=_PLAIN)
         made = (Y,)
     _call(what, dev, stream, made,
-          (*_view(what, "X", X, shape, dt, dev), *_view(what, "Y", Y, shape, dt, dev),
-           _flat(what, "gamma", gamma, (d,), dev), _flat(what, "beta", beta, (d,), dev), eps, B, H, L, d, _DT[dt]))
+          (*_views(what, ("X", "Y"), (X, Y), shape, dt, dev),
+           *_flats(what, ("gamma", "beta"), (gamma, beta), (d,), dev), eps, B, H, L, d, _DT[dt]))
     return Y
 
 
@@ -253,9 +261,8 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
             raise FavorError(f"{what}: the workspace must be contiguous on cuda:{dev}")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call(what, dev, stream, made,
-          (*_view(what, "X", X, shape, dt, dev), *_view(what, "dY", dY, shape, dt, dev),
-           *_view(what, "dX", dX, shape, dt, dev), _flat(what, "gamma", gamma, (d,), dev),
-           _flat(what, "dgamma", dgamma, (d,), dev), _flat(what, "dbeta", dbeta, (d,), dev), eps, B, H, L, d, _DT[dt],
+          (*_views(what, ("X", "dY", "dX"), (X, dY, dX), shape, dt, dev),
+           *_flats(what, ("gamma", "dgamma", "dbeta"), (gamma, dgamma, dbeta), (d,), dev), eps, B, H, L, d, _DT[dt],
            ws, nbytes))
     return dX, dgamma, dbeta
 
@@ -303,7 +310,7 @@ def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
     if Qo is None:
         Qo = torch.empty_like(Q, memory_format=_PLAIN)
         made.append(Qo)
-    views = (*_view(what, "Q", Q, Q.shape, dt, dev), *_view(what, "Q's output", Qo, Q.shape, dt, dev))
+    views = _views(what, ("Q", "Q's output"), (Q, Qo), Q.shape, dt, dev)
     Hk = 0
     if K is not None:
         Hk = K.shape[1] if K.dim() == 4 else 0
@@ -313,14 +320,14 @@ def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
         if Ko is None:
             Ko = torch.empty_like(K, memory_format=_PLAIN)
             made.append(Ko)
-        views += (*_view(what, "K", K, shape, dt, dev), *_view(what, "K's output", Ko, shape, dt, dev))
+        views += _views(what, ("K", "K's output"), (K, Ko), shape, dt, dev)
     elif Ko is None:
         views += (None, None, None, None)
     else:
         raise FavorError(f"{what}: an output for keys without keys")
     _call(what, dev, stream, made,
           (*views, B, Hq, Hk, L, d, pos.data_ptr(), pos.shape[1], n, c_sections,
-           _flat(what, "the table (new_rotary_table)", table, (pairs,), dev, torch.int64), pairing, _DT[dt]))
+           *_flats(what, ("the table (new_rotary_table)",), (table,), (pairs,), dev, torch.int64), pairing, _DT[dt]))
     return Qo, Ko
 
 
