@@ -12,11 +12,13 @@
 // stay in registers.
 //
 // Measured (one GB300; copy rate 6770 GB/s): 65536 x 16 rows of 128 bf16 94 us
-// forward, 5.7 TB/s (97 us out of a [B, L, 3, H, d] buffer), 127 us backward,
-// 6.3 TB/s; 32768 rows of 512 fp32 23.8 and 36.8 us, 5.6 and 5.5 TB/s.  Rows
-// whose pointers or strides are no multiples of 16 bytes go element by
-// element: 16384 x 16 rows of 128 bf16 59.6 against 29.8 us.  Small calls are
-// bound by their launches (8 rows of 512: 3.2 us; backward of 64: 6.0).
+// forward, 5.7 TB/s (97 us out of a [B, L, 3, H, d] buffer), 122 us backward,
+// 6.6 TB/s; 32768 rows of 512 fp32 22.8 and 35.6 us, 5.9 and 5.7 TB/s, bf16
+// 13.2 and 24.7 us, of which the two launches, the joins of the columns' sums
+// and the second kernel are about 7.  Rows whose pointers or strides are no
+// multiples of 16 bytes go element by element: 16384 x 16 rows of 128 bf16
+// 59.6 against 29.8 us.  Small calls are bound by their launches (8 rows of
+// 512: 2.9 us; backward of 64 rows: 5.1).
 #include <algorithm>
 
 #include "ops.cuh"
@@ -465,8 +467,7 @@ Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
   const int resident = backward ? (p.threads <= 256 && nv * vw <= 4 ? 1024 : 512) : many ? 1024 : 768;
   const int64_t per_sm = std::max(1, resident / p.threads);
   int64_t ctas = std::min<int64_t>((rows + p.groups - 1) / p.groups, per_sm * sm_count());
-  // every CTA's sums are added up after: rows enough for each to make that
-  // little (3333 rows in 1216 CTAs of 64 threads: 23 us, 10 of them that)
+  // every CTA's sums are added up after: rows enough for each to make that little
   if (backward) ctas = std::min(ctas, std::max<int64_t>(2 * sm_count(), rows / (8 * p.groups)));
   p.ctas = (int)ctas;
   return p;

@@ -19,15 +19,16 @@
 // call needs no workspace and its bits do not depend on timing.
 //
 // Measured (one GB300; copy rate 6770 GB/s): 65536 tokens x 2048 channels fp32
-// 268 us forward, 6.0 TB/s; 4 x 16 heads x 8192 x 128 bf16 115 us backward,
-// 5.8 TB/s: near the memory's rate where the channels fill the SMs' lanes with
-// few CTAs a cluster.  4 x 8 x 8192 x 64 bf16 26 us forward, 3.9 TB/s: there
-// the issue slots are 60 % busy (64 instructions per token and pair of
-// channels, 14 of them the exponentials) and a step takes as long as its
-// chain.  Tried and slower at that size: three CTAs an SM (72 registers spill,
-// 39 us), single channels of bf16 (33 us), the sending and the gathering of
-// maps in two warps (28 us), two kernels' worth of cluster barriers (a barrier
-// with release semantics waits for the stores' acknowledgement, 48 us).
+// 238 us forward, 6.8 TB/s; 8 x 16 heads x 4096 x 128 bf16 77 us forward, 5.2
+// TB/s, and 106 us backward, 6.3 TB/s; 4 x 8 x 8192 x 64 bf16 24.5 us forward,
+// 4.1 TB/s; 2 x 8 x 12288 x 64 bf16 34 us backward, 3.7 TB/s.  bf16 is bound by
+// instructions (54 per token and pair of channels forward, 14 of them the
+// exponentials; 86 backward) and, where a cluster has to be wide to fill the
+// SMs, by a step's chain of maps and states.  Tried and slower at 4 x 8 x 8192
+// x 64, at the time against 26 us: three CTAs an SM (39 us, the registers
+// spill), single channels of bf16 (33), the sending and the gathering of maps
+// in two warps (28), a cluster barrier a step in place of the counted stores
+// (48: its release waits for the global stores' acknowledgement).
 #include <mutex>
 
 #include "ops.cuh"
@@ -596,9 +597,9 @@ cudaError_t go(const ScanArgs& a, cudaStream_t stream) {
   if (runs > MW) {
     // CTAs of a cluster: a wave of clusters of K takes time as 1 / K.  The
     // smallest K whose waves take at most a tenth longer than the best's: at
-    // 32 tiles of 8192 tokens (bf16 forward) K = 8 takes 25.8 us, K = 4 29.4
-    // and K = 9 (a second wave) 40; at 16 tiles of 12288 (bf16 backward)
-    // K = 12 takes 34.5 us, K = 8 46.4, K = 16 (a second wave) 49.
+    // 32 tiles of 8192 tokens (bf16 forward) K = 8 takes 25 us, K = 4 34 and
+    // K = 12 (a second wave) 36; at 16 tiles of 12288 (bf16 backward) K = 12
+    // takes 34 us, K = 8 46 and K = 4 54.
     static std::mutex mu;
     static Fits known[64];
     int dev = 0;
@@ -647,8 +648,8 @@ cudaError_t go(const ScanArgs& a, bool bf16, int align, cudaStream_t stream) {
   // 16-byte copies where every row is made of whole ones (a quarter of the
   // copy instructions), else 4-byte ones; bf16 channels in pairs where rows are
   // made of whole pairs, else one by one.  4 x 8 heads x 8192 x 64 bf16
-  // forward: 26.0, 32.1 and 48.7 us; fp32 38.4 and 51.5; 2 x 8 x 12288 x 64
-  // bf16 backward: 34.0, 45.8 and 58.7.
+  // forward: 24.9, 32.5 and 48.5 us; fp32 36.3 and 59.0; 2 x 8 x 12288 x 64
+  // bf16 backward: 34.1, 45.7 and 58.5.
   // Workers of a CTA and tokens of a run.  Longer runs share what a run costs
   // among more tokens, as far as two runs' gates stay in registers: forward
   // 4 x 16 against 8 x 8 bf16 24.9 against 26.9 us (4 x 8 x 8192 x 64), 4 x 24
