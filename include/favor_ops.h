@@ -40,7 +40,9 @@ extern "C" {
  * favor_fwd_gated_scan — gated linear recurrence over the tokens, each of
  * the B H d channels by itself:
  *   h_t = exp(g_t) h_{t-1} + x_t,   h_{-1} = h0,   hT = h_{L-1}
- * g: logarithm of the gate (<= 0 for a decay; not checked).  Where exp(g_t)
+ * g: logarithm of the gate (<= 0 for a decay; not checked: positive ones are
+ * fine while the products of consecutive gates stay finite in fp32, since a
+ * run of tokens is applied as one map).  Where exp(g_t)
  * is 0 in fp32 (minus infinity, the type's lowest value) the state is
  * dropped, h_t = x_t, whatever it was, infinities and NaN included: such a
  * gate starts a new sequence packed into the same row.  (A state that decays

@@ -129,9 +129,9 @@ __device__ __forceinline__ Vec<V> all(float x) {
 }
 
 // ---- the ring of tokens ---------------------------------------------------------------
-// N arrays, R tokens of each per thread and stage; every thread copies and
-// reads only its own places (word order [stage][array][token][thread]), so
-// that waiting for its own copies is enough.
+// N arrays, R tokens of each per thread and stage, word order
+// [stage][array][token][thread].  Every warp copies and reads only its own
+// places, so that a warp's barrier orders copies and reads.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool in) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));

@@ -6,6 +6,7 @@ evaluation (``*_bound``), plus half a step of the storage type (2^-24 of the
 value for fp32, 2^-8 for bf16), plus the smallest normal number of the type.
 """
 
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -89,13 +90,15 @@ def scan_inputs(shape, dtype, seed, reset=()):
 def test_gated_scan_matches_oracle(cuda_lib, dtype, shape):
     x, g, dh, h0, dhT = scan_inputs(shape, dtype, sum(shape))
     xg, gg, dg_, sg, eg = x.cuda(), g.cuda(), dh.cuda(), h0.cuda(), dhT.cuda()
-    h, hT = cuda_lib.fwd_gated_scan(xg, gg, h0=sg)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h, hT = cuda_lib.fwd_gated_scan(xg, gg, h0=sg, dev_status=status)
     X, G, D, S, E = to_np(x), to_np(g), to_np(dh), to_np(h0), to_np(dhT)
     want, last = orc.gated_scan(X, G, S)
     bound = orc.gated_scan_bound(X, G, S)
     close(h, want, bound, "h")
     close(hT, last, bound[:, :, -1], "hT")
-    dx, dg, dh0 = cuda_lib.bwd_gated_scan(gg, h, dg_, h0=sg, dhT=eg)
+    dx, dg, dh0 = cuda_lib.bwd_gated_scan(gg, h, dg_, h0=sg, dhT=eg, dev_status=status)
+    assert int(status.item()) == 0
     refs, bounds = orc.gated_scan_grad(G, to_np(h), D, S, E), orc.gated_scan_grad_bound(G, to_np(h), D, S, E)
     for name, got, ref, b in zip(("dx", "dg", "dh0"), (dx, dg, dh0), refs, bounds):
         close(got, ref, b, name)
@@ -523,6 +526,23 @@ def test_calls_on_another_stream(cuda_lib):
             for a, b in zip(want, outs):
                 assert torch.equal(a, b)
             del junk
+
+
+def test_two_host_threads_at_once(cuda_lib):
+    # each with its own stream and tensors
+    ts = [_tensors(cuda_lib, seed) for seed in (7, 8)]
+    want = [[o.clone() for o in _all_calls(cuda_lib, t)] for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            outs = [_all_calls(cuda_lib, ts[i]) for _ in range(10)]
+            streams[i].synchronize()
+        return all(torch.equal(a, b) for o in outs for a, b in zip(want[i], o))
+
+    with concurrent.futures.ThreadPoolExecutor(2) as ex:
+        assert list(ex.map(work, (0, 1))) == [True, True]
 
 
 def test_two_graphs_share_a_workspace(cuda_lib):
