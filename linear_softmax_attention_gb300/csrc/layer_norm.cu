@@ -15,10 +15,8 @@
 // forward, 5.7 TB/s (97 us out of a [B, L, 3, H, d] buffer), 122 us backward,
 // 6.6 TB/s; 32768 rows of 512 fp32 22.8 and 35.6 us, 5.9 and 5.7 TB/s, bf16
 // 13.2 and 24.7 us, of which the two launches, the joins of the columns' sums
-// and the second kernel are about 7.  Rows whose pointers or strides are no
-// multiples of 16 bytes go element by element: 16384 x 16 rows of 128 bf16
-// 59.6 against 29.8 us.  Small calls are bound by their launches (8 rows of
-// 512: 2.9 us; backward of 64 rows: 5.1).
+// and the second kernel are about 7.  Small calls are bound by their launches
+// (8 rows of 512: 2.9 us; backward of 64 rows: 5.1).
 #include <algorithm>
 
 #include "ops.cuh"
@@ -31,7 +29,7 @@ constexpr int kWarps = 8;             // of a CTA that shares its rows out by gr
 constexpr int kMaxValues = 16;        // of a row in one thread
 constexpr int kSumRows = 32, kSumThreads = 32 * kSumRows;
 
-// VW values side by side: 16 bytes, or one element
+// VW values side by side: 16 bytes, two elements or one
 template <typename T, int VW> struct Piece;
 template <> struct Piece<float, 4> {
   using Raw = float4;
@@ -61,6 +59,25 @@ template <> struct Piece<__nv_bfloat16, 8> {
       w[i] = *reinterpret_cast<const unsigned*>(&v);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Piece<float, 2> {
+  using Raw = float2;
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = r.x;
+    f[1] = r.y;
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) { return make_float2(f[0], f[1]); }
+};
+template <> struct Piece<__nv_bfloat16, 2> {
+  using Raw = unsigned;
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = __uint_as_float(r << 16);
+    f[1] = __uint_as_float(r & 0xffff0000u);
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[0], f[1]);
+    return *reinterpret_cast<const unsigned*>(&v);
   }
 };
 template <> struct Piece<float, 1> {
@@ -136,7 +153,8 @@ struct Ahead {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(here ? 16 : 0)
                        : "memory");
         else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(here ? 4 : 0)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(sizeof(Raw)),
+                       "r"(here ? (int)sizeof(Raw) : 0)
                        : "memory");
       } else {
         regs[n][j] = here ? *reinterpret_cast<const Raw*>(row + c) : Raw{};
@@ -438,33 +456,37 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float* part
   }
 }
 
+// Values of a piece: 16 bytes where every tensor's rows are made of them,
+// else two elements, else one.  16384 x 16 rows of 128 bf16: 29.0, 39.8 and 52.7
+// us forward, 43.5, 66.6 and 103.9 backward.
+int piece_values(bool bf16, int piece) { return piece >= 16 ? (bf16 ? 8 : 4) : piece >= (bf16 ? 4 : 8) ? 2 : 1; }
+
 // CTAs: as many as the registers let be resident, so that every one walks
 // about the same number of rows
-Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
-  const int vw = vec ? (bf16 ? 8 : 4) : 1;
+Plan make_plan(int64_t rows, int d, int vw, bool backward) {
   const int pieces = (d + vw - 1) / vw, per = kMaxValues / vw;     // pieces of a row, of a thread at most
   Plan p;
-  int nv;
   if (pieces <= 32 * per) {
-    // as many values a thread as there may be: what a row costs beside them (its
-    // address, sums over lanes, root) is then shared by the most of them.  16
-    // values against 8 (65536 x 16 rows of 128 bf16): 94 against 126 us.
+    // 16-byte pieces: as many values a thread as there may be; what a row costs
+    // beside them (its address, sums over lanes, root) is then shared by the
+    // most of them.  16 values against 8 (65536 x 16 rows of 128 bf16): 94
+    // against 126 us.  Smaller pieces: 8 values, so that the lanes' accesses
+    // stay near to one another (3 x 10 x 36507 rows of 106 fp32, backward: 311
+    // us, with 16 values 688, with 4 476).
     p.lanes = 4;
-    while (p.lanes < 32 && p.lanes * per < pieces) p.lanes *= 2;
+    while (p.lanes < 32 && p.lanes * (vw >= 4 ? per : per / 2) < pieces) p.lanes *= 2;
     p.threads = 32 * kWarps;
     p.groups = p.threads / p.lanes;
-    nv = (pieces + p.lanes - 1) / p.lanes;
   } else {
-    // element by element a thread gets through fewer of them: 4 while 256 threads
-    // hold the row (3333 rows of 771 fp32, backward: 19.4 us, with 16 values 23.2)
-    const int most = vw == 1 && pieces <= 256 * 4 ? 4 : per;
+    // smaller pieces: 4 values a thread while 256 threads hold the row (3333
+    // rows of 771 fp32, backward: 19.4 us, with 16 values 23.2)
+    const int most = vw <= 2 && pieces <= 256 * (4 / vw) ? 4 / vw : per;
     p.threads = p.lanes = ((pieces + most - 1) / most + 31) / 32 * 32;
     p.groups = 1;
-    nv = (pieces + p.lanes - 1) / p.lanes;
   }
-  const bool many = p.threads <= 256 && nv * vw <= 8;
+  const int values = (pieces + p.lanes - 1) / p.lanes * vw;
   // threads of an SM
-  const int resident = backward ? (p.threads <= 256 && nv * vw <= 4 ? 1024 : 512) : many ? 1024 : 768;
+  const int resident = backward ? (p.threads <= 256 && values <= 4 ? 1024 : 512) : p.threads <= 256 && values <= 8 ? 1024 : 768;
   const int64_t per_sm = std::max(1, resident / p.threads);
   int64_t ctas = std::min<int64_t>((rows + p.groups - 1) / p.groups, per_sm * sm_count());
   // every CTA's sums are added up after: rows enough for each to make that little
@@ -476,28 +498,39 @@ Plan make_plan(int64_t rows, int d, bool bf16, bool vec, bool backward) {
 // (T, VW, NV, CTA) of a plan; CTA: the most threads of a row's CTA, 0 for groups of
 // lanes (fewer threads may use more registers)
 template <typename F>
-cudaError_t dispatch(const Plan& plan, int d, bool bf16, bool vec, F&& f) {
-  const int vw = vec ? (bf16 ? 8 : 4) : 1;
+cudaError_t dispatch(const Plan& plan, int d, bool bf16, int vw, F&& f) {
   const int nv = ((d + vw - 1) / vw + plan.lanes - 1) / plan.lanes;
 #define FAVOR_NORM(T, VW, NV)                           \
   return plan.lanes <= 32    ? f(Kind<T, VW, NV, 0>{})   \
          : plan.lanes <= 256 ? f(Kind<T, VW, NV, 256>{}) \
          : plan.lanes <= 512 ? f(Kind<T, VW, NV, 512>{}) \
                              : f(Kind<T, VW, NV, 1024>{})
-  if (bf16 && vec) {
+  if (bf16 && vw == 8) {
     if (nv <= 1) { FAVOR_NORM(__nv_bfloat16, 8, 1); }
     FAVOR_NORM(__nv_bfloat16, 8, 2);
   }
-  if (bf16) {
-    if (nv <= 4) { FAVOR_NORM(__nv_bfloat16, 1, 4); }
-    FAVOR_NORM(__nv_bfloat16, 1, 16);
-  }
-  if (vec) {
+  if (!bf16 && vw == 4) {
     if (nv <= 1) { FAVOR_NORM(float, 4, 1); }
     if (nv <= 2) { FAVOR_NORM(float, 4, 2); }
     FAVOR_NORM(float, 4, 4);
   }
+  if (bf16 && vw == 2) {
+    if (nv <= 2) { FAVOR_NORM(__nv_bfloat16, 2, 2); }
+    if (nv <= 4) { FAVOR_NORM(__nv_bfloat16, 2, 4); }
+    FAVOR_NORM(__nv_bfloat16, 2, 8);
+  }
+  if (vw == 2) {
+    if (nv <= 2) { FAVOR_NORM(float, 2, 2); }
+    if (nv <= 4) { FAVOR_NORM(float, 2, 4); }
+    FAVOR_NORM(float, 2, 8);
+  }
+  if (bf16) {
+    if (nv <= 4) { FAVOR_NORM(__nv_bfloat16, 1, 4); }
+    if (nv <= 8) { FAVOR_NORM(__nv_bfloat16, 1, 8); }
+    FAVOR_NORM(__nv_bfloat16, 1, 16);
+  }
   if (nv <= 4) { FAVOR_NORM(float, 1, 4); }
+  if (nv <= 8) { FAVOR_NORM(float, 1, 8); }
   FAVOR_NORM(float, 1, 16);
 #undef FAVOR_NORM
 }
@@ -527,27 +560,30 @@ cudaError_t bwd(Kind<T, VW, NV, CTA>, const NormArgs& a, const Rows& rows, uint3
 
 }  // namespace
 
-cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, bool vec, cudaStream_t stream) {
+cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, int piece, cudaStream_t stream) {
   const uint32_t n = (uint32_t)a.B * a.H * a.L;
   const Strides s[2] = {a.xs, a.ys};
   const Rows rows = make_rows(a.B, a.H, a.L, s, 2);
-  const Plan plan = make_plan(n, a.d, bf16, vec, false);
-  return dispatch(plan, a.d, bf16, vec, [&](auto kind) { return fwd(kind, a, rows, n, plan, stream); });
+  const int vw = piece_values(bf16, piece);
+  const Plan plan = make_plan(n, a.d, vw, false);
+  return dispatch(plan, a.d, bf16, vw, [&](auto kind) { return fwd(kind, a, rows, n, plan, stream); });
 }
 
-// what either kernel of a shape may write, whatever the pointers' alignment
+// what any kernel of a shape may write, whatever the tensors' alignment
 size_t norm_bwd_workspace_bytes(int64_t rows, int d, bool bf16) {
-  const int ctas = std::max(make_plan(rows, d, bf16, false, true).ctas, make_plan(rows, d, bf16, true, true).ctas);
+  int ctas = 0;
+  for (const int vw : {bf16 ? 8 : 4, 2, 1}) ctas = std::max(ctas, make_plan(rows, d, vw, true).ctas);
   return (size_t)ctas * 2 * d * sizeof(float);
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, bool vec, float* ws, cudaStream_t stream) {
+cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int piece, float* ws, cudaStream_t stream) {
   const uint32_t n = (uint32_t)a.B * a.H * a.L;
   const Strides s[3] = {a.xs, a.dys, a.dxs};
   const Rows rows = make_rows(a.B, a.H, a.L, s, 3);
-  const Plan plan = make_plan(n, a.d, bf16, vec, true);
+  const int vw = piece_values(bf16, piece);
+  const Plan plan = make_plan(n, a.d, vw, true);
   const bool sums = a.dgamma != nullptr || a.dbeta != nullptr;
-  cudaError_t e = dispatch(plan, a.d, bf16, vec, [&](auto kind) {
+  cudaError_t e = dispatch(plan, a.d, bf16, vw, [&](auto kind) {
     return bwd(kind, a, rows, n, plan, sums ? ws : nullptr, stream);
   });
   if (e != cudaSuccess || !sums) return e;

@@ -141,8 +141,9 @@ struct NormArgs {
   float eps;
   int B, H, L, d;
 };
-cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, bool vec, cudaStream_t stream);
-cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, bool vec, float* ws, cudaStream_t stream);
+// piece: every tensor's rows are made of pieces of this many bytes (16, two elements or one)
+cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, int piece, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int piece, float* ws, cudaStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t rows, int d, bool bf16);
 
 struct RotaryArgs {

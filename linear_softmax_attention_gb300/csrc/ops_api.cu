@@ -181,10 +181,11 @@ bool scan_fits(std::initializer_list<const View*> views) {
   return true;
 }
 
-// the largest of 16, 4 and 2 bytes that all the views' rows are made of
+// the most bytes, 16 or less, of which all the views' rows are made
 int common_piece(std::initializer_list<const View*> views) {
   int piece = 16;
-  for (const View* v : views) piece = v->pieces(piece) ? piece : piece >= 4 && v->pieces(4) ? 4 : 2;
+  for (const View* v : views)
+    while (piece > v->esz && !v->pieces(piece)) piece /= 2;
   return piece;
 }
 
@@ -389,7 +390,7 @@ favor_status favor_fwd_layer_norm(const void* x, const int64_t* x_strides, void*
   a.H = H;
   a.L = L;
   a.d = d;
-  return done(favor::launch_norm_fwd(a, dt == FAVOR_BF16, vx.pieces(16) && vy.pieces(16),
+  return done(favor::launch_norm_fwd(a, dt == FAVOR_BF16, common_piece({&vx, &vy}),
                                      static_cast<cudaStream_t>(stream)));
 }
 
@@ -446,7 +447,7 @@ favor_status favor_bwd_layer_norm(const void* x, const int64_t* x_strides, const
   a.H = H;
   a.L = L;
   a.d = d;
-  return done(favor::launch_norm_bwd(a, dt == FAVOR_BF16, vx.pieces(16) && vdy.pieces(16) && vdx.pieces(16),
+  return done(favor::launch_norm_bwd(a, dt == FAVOR_BF16, common_piece({&vx, &vdy, &vdx}),
                                      static_cast<float*>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
