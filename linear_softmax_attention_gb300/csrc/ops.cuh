@@ -156,6 +156,6 @@ struct RotaryArgs {
   const uint64_t* table;
   bool halves, inverse;
 };
-cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, bool vec, cudaStream_t stream);
+cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, int piece, cudaStream_t stream);
 
 }  // namespace favor

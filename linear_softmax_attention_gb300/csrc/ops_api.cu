@@ -224,14 +224,14 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   if (favor::self_overlap(vqo) || clash(vqo, vq, true)) return FAVOR_ERR_INVALID_ARG;
   const View vpos = favor::flat_view(pos, (int64_t)n_axes * pos_B * L, 4), vtab = favor::flat_view(table, pairs, 8);
   if (clash(vqo, vpos, false) || clash(vqo, vtab, false)) return FAVOR_ERR_INVALID_ARG;
-  bool vec = vq.pieces(16) && vqo.pieces(16);
+  int piece = common_piece({&vq, &vqo});
   if (keys) {
     if (!favor::make_view(&vk, k, ks, B, Hk, L, d, e) || !favor::make_view(&vko, ko, kos, B, Hk, L, d, e))
       return FAVOR_ERR_INVALID_ARG;
     if (favor::self_overlap(vko) || clash(vko, vk, true) || clash(vko, vq, false) || clash(vqo, vk, false) ||
         clash(vqo, vko, false) || clash(vko, vpos, false) || clash(vko, vtab, false))
       return FAVOR_ERR_INVALID_ARG;
-    vec = vec && vk.pieces(16) && vko.pieces(16);
+    piece = std::min(piece, common_piece({&vk, &vko}));
   }
   a.q = q;
   a.k = k;
@@ -255,7 +255,7 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   a.table = table;
   a.halves = pairing == FAVOR_PAIR_HALVES;
   a.inverse = inverse;
-  return done(favor::launch_rotary(a, dt == FAVOR_BF16, vec, static_cast<cudaStream_t>(stream)));
+  return done(favor::launch_rotary(a, dt == FAVOR_BF16, piece, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

@@ -1,8 +1,8 @@
 // Rotation of queries and keys by positions on one to four axes.
 //
 // Bound by memory: every channel is read and written once.  A thread takes one
-// 16-byte piece of a token's channels (two where the pairs are halves apart)
-// in every head of its share: the sines and cosines of the token are formed
+// piece of a token's channels, 16 bytes or two elements (two pieces where the
+// pairs are halves apart), in every head of its share: the sines and cosines of the token are formed
 // once and used for all of them, and the heads' loads are in flight together.
 // The heads are shared out over more threads only where the tokens are few.
 //
@@ -18,7 +18,8 @@ namespace favor {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;             // heads of a thread whose loads are in flight together
+// heads of a thread whose loads are in flight together
+template <int E> constexpr int kHeadsOf = E > 2 ? 4 : 8;
 
 // The angle of a pair, in half turns: the position times the pair's fraction
 // of a turn per unit, in 64-bit fixed point, wraps to the exact fraction of a
@@ -38,10 +39,10 @@ struct Shared {                       // what q's and k's heads have in common
   void* out;
 };
 
-template <typename T> struct Piece;
-template <> struct Piece<float> {
+// E elements side by side
+template <typename T, int E> struct Piece;
+template <> struct Piece<float, 4> {
   using Raw = float4;
-  static constexpr int E = 4;
   static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
     f[0] = r.x;
     f[1] = r.y;
@@ -50,9 +51,8 @@ template <> struct Piece<float> {
   }
   static __device__ __forceinline__ Raw pack(const float* f) { return make_float4(f[0], f[1], f[2], f[3]); }
 };
-template <> struct Piece<__nv_bfloat16> {
+template <> struct Piece<__nv_bfloat16, 8> {
   using Raw = uint4;
-  static constexpr int E = 8;
   static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
     const unsigned w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -72,6 +72,26 @@ template <> struct Piece<__nv_bfloat16> {
   }
 };
 
+template <> struct Piece<float, 2> {
+  using Raw = float2;
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = r.x;
+    f[1] = r.y;
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) { return make_float2(f[0], f[1]); }
+};
+template <> struct Piece<__nv_bfloat16, 2> {
+  using Raw = unsigned;
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = __uint_as_float(r << 16);
+    f[1] = __uint_as_float(r & 0xffff0000u);
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[0], f[1]);
+    return *reinterpret_cast<const unsigned*>(&v);
+  }
+};
+
 struct Work {
   Shared q, k;
   const int32_t* pos;
@@ -80,6 +100,16 @@ struct Work {
   FastDiv l, items;                   // tokens of a row; pieces (pairs of pieces) of a token
   int tokens, per_cta, pos_B, n_axes, L, P, d, Hq, heads, share;
   float sign;
+};
+
+// a token's channels in the first head of q or k
+template <typename T>
+struct Token {
+  const T* in;
+  T* out;
+  __device__ __forceinline__ Token(const Shared& s, int b, int t)
+      : in(static_cast<const T*>(s.in) + b * s.is.b + t * s.is.l),
+        out(static_cast<T*>(s.out) + b * s.os.b + t * s.os.l) {}
 };
 
 // positions of a token on each axis
@@ -95,11 +125,12 @@ __device__ __forceinline__ int32_t on_axis(const Axes& ax, const int32_t (&at)[F
   return r;
 }
 
-template <typename T, bool HALVES>
+template <typename T, int E, bool HALVES>
 __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
-  using P = Piece<T>;
+  using P = Piece<T, E>;
   using Raw = typename P::Raw;
-  constexpr int E = P::E, N = HALVES ? E : E / 2;      // pairs of a thread
+  constexpr int N = HALVES ? E : E / 2;                // pairs of a thread
+  constexpr int kHeads = kHeadsOf<E>;
   const int items = w.items.d;
   const int within = items <= kThreads ? w.items.div(threadIdx.x) : 0;
   const int64_t token = (int64_t)blockIdx.x * w.per_cta + within;
@@ -108,6 +139,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
   const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
   int32_t at[FAVOR_ROTARY_MAX_AXES];
   token_positions(w, b, t, at);
+  const Token<T> q(w.q, b, t), k(w.k, b, t);
   for (int item = threadIdx.x - within * items; item < items; item += kThreads) {
     const int turning = HALVES ? w.P / E : 2 * w.P / E;
     const bool turns = item < turning;
@@ -128,8 +160,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
       for (int i = 0; i < kHeads; ++i) {
         const int hh = hb + i;
         if (hh < h1) {
-          const Shared& s = hh < w.Hq ? w.q : w.k;
-          const T* in = static_cast<const T*>(s.in) + b * s.is.b + (hh < w.Hq ? hh : hh - w.Hq) * s.is.h + t * s.is.l;
+          const T* in = hh < w.Hq ? q.in + hh * w.q.is.h : k.in + (hh - w.Hq) * w.k.is.h;
           r0[i] = *reinterpret_cast<const Raw*>(in + c0);
           if (HALVES && turns) r1[i] = *reinterpret_cast<const Raw*>(in + c1);
         }
@@ -138,8 +169,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
       for (int i = 0; i < kHeads; ++i) {
         const int hh = hb + i;
         if (hh < h1) {
-          const Shared& s = hh < w.Hq ? w.q : w.k;
-          T* out = static_cast<T*>(s.out) + b * s.os.b + (hh < w.Hq ? hh : hh - w.Hq) * s.os.h + t * s.os.l;
+          T* out = hh < w.Hq ? q.out + hh * w.q.os.h : k.out + (hh - w.Hq) * w.k.os.h;
           if (turns) {
             float u[E], v[E], a[E], c[E];
             P::unpack(r0[i], u);
@@ -171,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
 // Any strides and sizes: a thread per pair, or channel behind the pairs
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool halves) {
+  constexpr int kHeads = kHeadsOf<1>;
   const int items = w.items.d;
   const int within = items <= kThreads ? w.items.div(threadIdx.x) : 0;
   const int64_t token = (int64_t)blockIdx.x * w.per_cta + within;
@@ -179,6 +210,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool hal
   const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
   int32_t at[FAVOR_ROTARY_MAX_AXES];
   token_positions(w, b, t, at);
+  const Token<T> q(w.q, b, t), k(w.k, b, t);
   for (int p = threadIdx.x - within * items; p < items; p += kThreads) {
     const bool turns = p < w.P;
     const int iu = !turns ? p + w.P : halves ? p : 2 * p, iv = !turns ? iu : halves ? p + w.P : 2 * p + 1;
@@ -193,8 +225,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool hal
       for (int i = 0; i < kHeads; ++i) {
         const int hh = hb + i;
         if (hh < h1) {
-          const Shared& s = hh < w.Hq ? w.q : w.k;
-          const T* in = static_cast<const T*>(s.in) + b * s.is.b + (hh < w.Hq ? hh : hh - w.Hq) * s.is.h + t * s.is.l;
+          const T* in = hh < w.Hq ? q.in + hh * w.q.is.h : k.in + (hh - w.Hq) * w.k.is.h;
           u[i] = in[iu];
           v[i] = in[iv];
         }
@@ -203,8 +234,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool hal
       for (int i = 0; i < kHeads; ++i) {
         const int hh = hb + i;
         if (hh < h1) {
-          const Shared& s = hh < w.Hq ? w.q : w.k;
-          T* out = static_cast<T*>(s.out) + b * s.os.b + (hh < w.Hq ? hh : hh - w.Hq) * s.os.h + t * s.os.l;
+          T* out = hh < w.Hq ? q.out + hh * w.q.os.h : k.out + (hh - w.Hq) * w.k.os.h;
           if (turns) {
             const float x = to_f32(u[i]), y = to_f32(v[i]);
             out[iu] = from_f32<T>(x * cs - y * sn);
@@ -220,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool hal
 
 }  // namespace
 
-cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, bool vec, cudaStream_t stream) {
+cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, int piece, cudaStream_t stream) {
   Work w{};
   w.q = Shared{a.qs, a.qos, a.q, a.qo};
   w.k = Shared{a.ks, a.kos, a.k, a.ko};
@@ -238,12 +268,13 @@ cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, bool vec, cudaStream_t
   w.Hq = a.Hq;
   w.heads = a.Hq + a.Hk;
   w.sign = a.inverse ? -1.f : 1.f;
-  // Whole pieces: each half of the pairs (all of them, side by side) is made of
-  // 16 bytes, as are the rows.  Else pair by pair (16384 x 16 heads of 128 bf16:
-  // 55.4 against 32.4 us).
-  const int E = bf16 ? 8 : 4;
-  const bool pieces = vec && (a.halves ? a.pairs % E == 0 : 2 * a.pairs % E == 0);
-  const int items = !pieces ? a.d - a.pairs : a.halves ? a.pairs / E + (a.d - 2 * a.pairs) / E : a.d / E;
+  // Pieces of 16 bytes, else of two elements, where the rows and each half of
+  // the pairs (all of them, where they are side by side) are made of whole
+  // ones, else pair by pair.  BYBY
+  const int e = bf16 ? 2 : 4;
+  auto whole = [&](int n) { return piece >= n * e && (a.halves ? a.pairs % n == 0 : 2 * a.pairs % n == 0); };
+  const int E = whole(16 / e) ? 16 / e : whole(2) ? 2 : 1;
+  const int items = E == 1 ? a.d - a.pairs : a.halves ? a.pairs / E + (a.d - 2 * a.pairs) / E : a.d / E;
   w.items = FastDiv((uint32_t)items);
   w.per_cta = std::max(1, kThreads / items);
   // Enough threads for every SM's 2048: fewer heads each where tokens are few
@@ -254,14 +285,20 @@ cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, bool vec, cudaStream_t
   w.share = (int)((w.heads + parts - 1) / parts);
   const dim3 grid((unsigned)(((int64_t)w.tokens + w.per_cta - 1) / w.per_cta),
                   (unsigned)((w.heads + w.share - 1) / w.share));
-  if (pieces) {
-    if (bf16 && a.halves) rotary_pieces_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(w);
-    else if (bf16) rotary_pieces_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(w);
-    else if (a.halves) rotary_pieces_kernel<float, true><<<grid, kThreads, 0, stream>>>(w);
-    else rotary_pieces_kernel<float, false><<<grid, kThreads, 0, stream>>>(w);
-  } else {
-    if (bf16) rotary_pairs_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(w, a.halves);
+  using B16 = __nv_bfloat16;
+  if (E == 1) {
+    if (bf16) rotary_pairs_kernel<B16><<<grid, kThreads, 0, stream>>>(w, a.halves);
     else rotary_pairs_kernel<float><<<grid, kThreads, 0, stream>>>(w, a.halves);
+  } else if (E == 2) {
+    if (bf16 && a.halves) rotary_pieces_kernel<B16, 2, true><<<grid, kThreads, 0, stream>>>(w);
+    else if (bf16) rotary_pieces_kernel<B16, 2, false><<<grid, kThreads, 0, stream>>>(w);
+    else if (a.halves) rotary_pieces_kernel<float, 2, true><<<grid, kThreads, 0, stream>>>(w);
+    else rotary_pieces_kernel<float, 2, false><<<grid, kThreads, 0, stream>>>(w);
+  } else {
+    if (bf16 && a.halves) rotary_pieces_kernel<B16, 8, true><<<grid, kThreads, 0, stream>>>(w);
+    else if (bf16) rotary_pieces_kernel<B16, 8, false><<<grid, kThreads, 0, stream>>>(w);
+    else if (a.halves) rotary_pieces_kernel<float, 4, true><<<grid, kThreads, 0, stream>>>(w);
+    else rotary_pieces_kernel<float, 4, false><<<grid, kThreads, 0, stream>>>(w);
   }
   return cudaGetLastError();
 }
