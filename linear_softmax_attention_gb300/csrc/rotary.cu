@@ -7,9 +7,9 @@
 // The heads are shared out over more threads only where the tokens are few.
 //
 // Measured (one GB300; copy rate 6770 GB/s): 2 x 12288 tokens x (8 + 8) heads
-// of 64 fp32 35.7 us, 5.6 TB/s; 65536 tokens x (16 + 4) heads of 128 bf16 on
-// three axes 107 us, 6.2 TB/s.  With one head a token's sines are not shared
-// (65536 x (1 + 1) heads of 64 bf16: 13.6 us, 2.5 TB/s).
+// of 64 fp32 34.0 us, 5.9 TB/s; 65536 tokens x (16 + 4) heads of 128 bf16 on
+// three axes 105 us, 6.4 TB/s.  With one head a token's sines are not shared
+// (65536 x (1 + 1) heads of 64 bf16: 12.6 us, 2.7 TB/s).
 #include <algorithm>
 
 #include "ops.cuh"
@@ -21,12 +21,33 @@ constexpr int kThreads = 256;
 // heads of a thread whose loads are in flight together
 template <int E> constexpr int kHeadsOf = E > 2 ? 4 : 8;
 
-// The angle of a pair, in half turns: the position times the pair's fraction
-// of a turn per unit, in 64-bit fixed point, wraps to the exact fraction of a
-// turn; its upper 32 bits as a signed number are the angle to 2^-32 turns.
-__device__ __forceinline__ float half_turns(int32_t pos, uint64_t per_unit) {
+// Sine and cosine of a pair's angle.  The position times the pair's fraction of
+// a turn per unit, in 64-bit fixed point, wraps to the exact fraction of a
+// turn, of which the upper 32 bits are kept.  The nearest quarter turn is taken
+// off exactly, in whole numbers; what is left, z in [-pi/4, pi/4], goes into
+// the Taylor series of sin (to z^9) and cos (to z^10), whose remainders there
+// are below 2e-9 and 2e-10, and the quarters turn the two.
+__device__ __forceinline__ void sine_cosine(int32_t pos, uint64_t per_unit, float* sn, float* cs) {
   const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * per_unit;
-  return static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+  const uint32_t u = static_cast<uint32_t>(turn >> 32);
+  const uint32_t quarter = (u + (1u << 29)) >> 30;
+  const float z = static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * (6.283185307179586f * 0x1p-32f);
+  const float z2 = z * z;
+  float s = 1.f / 362880;
+  s = fmaf(s, z2, -1.f / 5040);
+  s = fmaf(s, z2, 1.f / 120);
+  s = fmaf(s, z2, -1.f / 6);
+  s = fmaf(s * z2, z, z);
+  float c = -1.f / 3628800;
+  c = fmaf(c, z2, 1.f / 40320);
+  c = fmaf(c, z2, -1.f / 720);
+  c = fmaf(c, z2, 1.f / 24);
+  c = fmaf(c, z2, -0.5f);
+  c = fmaf(c, z2, 1.f);
+  const bool odd = quarter & 1;
+  const float a = odd ? c : s, b = odd ? s : c;
+  *sn = __uint_as_float(__float_as_uint(a) ^ ((quarter & 2) << 30));
+  *cs = __uint_as_float(__float_as_uint(b) ^ (((quarter + 1) & 2) << 30));
 }
 
 struct Axes {
@@ -98,7 +119,7 @@ struct Work {
   const uint64_t* table;
   Axes ax;
   FastDiv l, items;                   // tokens of a row; pieces (pairs of pieces) of a token
-  int tokens, per_cta, pos_B, n_axes, L, P, d, Hq, heads, share;
+  int tokens, per_cta, pos_B, L, P, Hq, heads, share;
   float sign;
 };
 
@@ -112,17 +133,13 @@ struct Token {
         out(static_cast<T*>(s.out) + b * s.os.b + t * s.os.l) {}
 };
 
-// positions of a token on each axis
-__device__ __forceinline__ void token_positions(const Work& w, int b, int t, int32_t (&at)[FAVOR_ROTARY_MAX_AXES]) {
-#pragma unroll
-  for (int a = 0; a < FAVOR_ROTARY_MAX_AXES; ++a)
-    at[a] = a < w.n_axes ? w.pos[((int64_t)a * w.pos_B + (w.pos_B > 1 ? b : 0)) * w.L + t] : 0;
-}
-__device__ __forceinline__ int32_t on_axis(const Axes& ax, const int32_t (&at)[FAVOR_ROTARY_MAX_AXES], int p) {
-  int32_t r = at[0];
-#pragma unroll
-  for (int a = 1; a < FAVOR_ROTARY_MAX_AXES; ++a) r = p >= ax.end[a - 1] ? at[a] : r;
-  return r;
+// A token's position on the axis of pair p; `axis` and `at`: of the pair before
+// (-1: none), so that a thread loads once per axis
+__device__ __forceinline__ void position(const Work& w, int b, int t, int p, int* axis, int32_t* at) {
+  const int a = (p >= w.ax.end[0]) + (p >= w.ax.end[1]) + (p >= w.ax.end[2]);
+  if (a == *axis) return;
+  *axis = a;
+  *at = w.pos[((int64_t)a * w.pos_B + (w.pos_B > 1 ? b : 0)) * w.L + t];
 }
 
 template <typename T, int E, bool HALVES>
@@ -137,8 +154,6 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
   if (within >= w.per_cta || token >= w.tokens) return;
   const int b = (int)w.l.div((uint32_t)token), t = (int)token - b * w.L;
   const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
-  int32_t at[FAVOR_ROTARY_MAX_AXES];
-  token_positions(w, b, t, at);
   const Token<T> q(w.q, b, t), k(w.k, b, t);
   for (int item = threadIdx.x - within * items; item < items; item += kThreads) {
     const int turning = HALVES ? w.P / E : 2 * w.P / E;
@@ -146,11 +161,14 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
     // first channel of the piece, and of the second half's
     const int c0 = HALVES && !turns ? 2 * w.P + (item - turning) * E : item * E, c1 = c0 + w.P;
     float cs[N], sn[N];
+    int axis = -1;
+    int32_t at = 0;
     if (turns) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int p = HALVES ? c0 + i : c0 / 2 + i;
-        sincospif(half_turns(on_axis(w.ax, at, p), w.table[p]), &sn[i], &cs[i]);
+        position(w, b, t, p, &axis, &at);
+        sine_cosine(at, w.table[p], &sn[i], &cs[i]);
         sn[i] *= w.sign;
       }
     }
@@ -208,15 +226,16 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool hal
   if (within >= w.per_cta || token >= w.tokens) return;
   const int b = (int)w.l.div((uint32_t)token), t = (int)token - b * w.L;
   const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
-  int32_t at[FAVOR_ROTARY_MAX_AXES];
-  token_positions(w, b, t, at);
   const Token<T> q(w.q, b, t), k(w.k, b, t);
   for (int p = threadIdx.x - within * items; p < items; p += kThreads) {
     const bool turns = p < w.P;
     const int iu = !turns ? p + w.P : halves ? p : 2 * p, iv = !turns ? iu : halves ? p + w.P : 2 * p + 1;
     float cs = 1.f, sn = 0.f;
     if (turns) {
-      sincospif(half_turns(on_axis(w.ax, at, p), w.table[p]), &sn, &cs);
+      int axis = -1;
+      int32_t at = 0;
+      position(w, b, t, p, &axis, &at);
+      sine_cosine(at, w.table[p], &sn, &cs);
       sn *= w.sign;
     }
     for (int hb = h0; hb < h1; hb += kHeads) {
@@ -261,16 +280,15 @@ cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, int piece, cudaStream_
   w.l = FastDiv((uint32_t)a.L);
   w.tokens = a.B * a.L;
   w.pos_B = a.pos_B;
-  w.n_axes = a.n_axes;
   w.L = a.L;
   w.P = a.pairs;
-  w.d = a.d;
   w.Hq = a.Hq;
   w.heads = a.Hq + a.Hk;
   w.sign = a.inverse ? -1.f : 1.f;
   // Pieces of 16 bytes, else of two elements, where the rows and each half of
   // the pairs (all of them, where they are side by side) are made of whole
-  // ones, else pair by pair.  BYBY
+  // ones, else pair by pair (16384 x 16 heads of 128 bf16: 31.2, 32.8 and 43.2 us
+  // for halves, 31.0, 38.4 and 43.7 for adjacent pairs).
   const int e = bf16 ? 2 : 4;
   auto whole = [&](int n) { return piece >= n * e && (a.halves ? a.pairs % n == 0 : 2 * a.pairs % n == 0); };
   const int E = whole(16 / e) ? 16 / e : whole(2) ? 2 : 1;
