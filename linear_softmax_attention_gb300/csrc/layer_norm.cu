@@ -486,7 +486,7 @@ Plan make_plan(int64_t rows, int d, int vw, bool backward) {
   }
   const int values = (pieces + p.lanes - 1) / p.lanes * vw;
   // threads of an SM
-  const int resident = backward ? (p.threads <= 256 && values <= 4 ? 1024 : 512) : p.threads <= 256 && values <= 8 ? 1024 : 768;
+  const int resident = p.threads <= 256 && values <= (backward ? 4 : 8) ? 1024 : backward ? 512 : 768;
   const int64_t per_sm = std::max(1, resident / p.threads);
   int64_t ctas = std::min<int64_t>((rows + p.groups - 1) / p.groups, per_sm * sm_count());
   // every CTA's sums are added up after: rows enough for each to make that little

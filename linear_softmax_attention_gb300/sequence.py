@@ -110,22 +110,32 @@ def _sizes(what, name, t, four_only=False):
     return B, H, L, d, t.dtype, t.get_device()
 
 
-def _call(what, index, stream, made, args):
-    """The entry point `what` on device `index`.  made: tensors allocated here
-    on the current stream, for use on `stream`."""
+def _call(what, index, args):
+    """The entry point `what` on device `index`, on its current stream."""
     if index != _current_device():
         with torch.cuda.device(index):
-            return _call(what, index, stream, made, args)
-    handle = _raw_stream(index)
-    if stream is not None and stream.cuda_stream != handle:
-        if stream.device.index != index:
-            raise FavorError(f"{what}: the stream belongs to {stream.device}, the tensors to cuda:{index}")
-        handle = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
-    code = getattr(load(), what)(*args, handle)
+            return _call(what, index, args)
+    code = getattr(load(), what)(*args, _raw_stream(index))
     if code != 0:
         _check(code, what)
+
+
+def _on(stream, fn, t, *args):
+    """fn(t, *args) with `stream` as the current one of t's device: what is
+    allocated there comes from that stream's memory, which no other stream's
+    pending work reads.  The results may then be used on the stream that was
+    current before."""
+    if not t.is_cuda or stream.device != t.device:
+        raise FavorError(f"{fn.__name__}: the stream belongs to {stream.device}, the tensors to {t.device}")
+    current = torch.cuda.current_stream(t.device)
+    if stream == current:
+        return fn(t, *args)
+    with torch.cuda.stream(stream):
+        out = fn(t, *args)
+    for o in out if isinstance(out, tuple) else (out,):
+        if o is not None:
+            o.record_stream(current)
+    return out
 
 
 def new_gated_scan_state(B: int, H: int, d: int, device="cuda") -> torch.Tensor:
@@ -139,18 +149,17 @@ def fwd_gated_scan(X, G, h0=None, O=None, hT=None, dev_status=None, stream=None)
     Returns (O, hT): every h_t in X's dtype and layout, and the last one in
     fp32.  A gate of minus infinity starts a new sequence; G = 0 with X = 0
     carries the state over padding.  O may be X or G, hT may be h0."""
+    if stream is not None:
+        return _on(stream, fwd_gated_scan, X, G, h0, O, hT, dev_status)
     what = "favor_fwd_gated_scan"
     B, H, L, d, dt, dev = _sizes(what, "X", X)
     shape = X.shape
     state = (B, H, d) if len(shape) == 4 else (B, d)
-    made = []
     if O is None:
         O = torch.empty_like(X)
-        made.append(O)
     if hT is None:
         hT = torch.empty(state, dtype=torch.float32, device=X.device)
-        made.append(hT)
-    _call(what, dev, stream, made,
+    _call(what, dev,
           (*_views(what, ("X", "G", "O"), (X, G, O), shape, dt, dev), *_flats(what, ("h0", "hT"), (h0, hT), state, dev),
            B, H, L, d, _DT[dt], _status(what, dev_status, dev)))
     return O, hT
@@ -161,21 +170,19 @@ def bwd_gated_scan(G, O, dO, h0=None, dhT=None, dX=None, dG=None, dh0=None, dev_
     and dhT (None: zeros); O is its output and h0 its initial state.  dX may
     be dO, dG may be G, dh0 may be dhT.  For a gate broadcast over an axis sum
     dG over it."""
+    if stream is not None:
+        return _on(stream, bwd_gated_scan, G, O, dO, h0, dhT, dX, dG, dh0, dev_status)
     what = "favor_bwd_gated_scan"
     B, H, L, d, dt, dev = _sizes(what, "G", G)
     shape = G.shape
     state = (B, H, d) if len(shape) == 4 else (B, d)
-    made = []
     if dX is None:
         dX = torch.empty_like(dO)
-        made.append(dX)
     if dG is None:
         dG = torch.empty_like(G)
-        made.append(dG)
     if dh0 is None:
         dh0 = torch.empty(state, dtype=torch.float32, device=G.device)
-        made.append(dh0)
-    _call(what, dev, stream, made,
+    _call(what, dev,
           (*_views(what, ("G", "O", "dO", "dX", "dG"), (G, O, dO, dX, dG), shape, dt, dev),
            *_flats(what, ("h0", "dhT", "dh0"), (h0, dhT, dh0), state, dev), B, H, L, d, _DT[dt],
            _status(what, dev_status, dev)))
@@ -186,6 +193,8 @@ def gated_scan_step(x, g, state, o=None, new_state=None, stream=None):
     """One token: x, g contiguous [B, H, d], state fp32 [B, H, d].  Writes
     exp(g) state + x to new_state (None: in place) and returns (o, new_state),
     o the new state in x's dtype."""
+    if stream is not None:
+        return _on(stream, gated_scan_step, x, g, state, o, new_state)
     what = "favor_gated_scan_step"
     dt, shape, dev = x.dtype, x.shape, x.get_device()
     if dev < 0 or dt not in _DT or len(shape) != 3:
@@ -193,13 +202,11 @@ def gated_scan_step(x, g, state, o=None, new_state=None, stream=None):
     B, H, d = shape
     if B < 1 or H < 1 or d < 1 or B > _INT or H > _INT or d > _INT:
         raise FavorError(f"{what}: x has an empty or oversized axis: {list(shape)}")
-    made = ()
     if o is None:
         o = torch.empty_like(x, memory_format=_PLAIN)
-        made = (o,)
     if new_state is None:
         new_state = state
-    _call(what, dev, stream, made,
+    _call(what, dev,
           (*_flats(what, ("x", "g", "o"), (x, g, o), shape, dev, dt),
            *_flats(what, ("state", "new_state"), (state, new_state), shape, dev), B, H, d, _DT[dt]))
     return o, new_state
@@ -209,14 +216,14 @@ def fwd_layer_norm(X, gamma=None, beta=None, eps=1e-5, Y=None, stream=None):
     """Layer norm of X [B, H, L, d] (or [B, L, d]) over d, with gamma and beta
     (fp32 [d], None: 1 and 0).  Returns Y, contiguous where none is given (as
     the attention takes it); Y may be X."""
+    if stream is not None:
+        return _on(stream, fwd_layer_norm, X, gamma, beta, eps, Y)
     what = "favor_fwd_layer_norm"
     B, H, L, d, dt, dev = _sizes(what, "X", X)
     shape = X.shape
-    made = ()
     if Y is None:
         Y = torch.empty_like(X, memory_format=_PLAIN)
-        made = (Y,)
-    _call(what, dev, stream, made,
+    _call(what, dev,
           (*_views(what, ("X", "Y"), (X, Y), shape, dt, dev),
            *_flats(what, ("gamma", "beta"), (gamma, beta), (d,), dev), eps, B, H, L, d, _DT[dt]))
     return Y
@@ -236,23 +243,20 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
     """Gradients (dX, dgamma, dbeta) of fwd_layer_norm for dY; X is its input.
     dgamma and dbeta are fp32 [d], summed over all rows; weight_grads=False
     leaves them out (None, None).  dX may be dY or X."""
+    if stream is not None:
+        return _on(stream, bwd_layer_norm, X, dY, gamma, eps, dX, dgamma, dbeta, workspace, None, weight_grads)
     what = "favor_bwd_layer_norm"
     B, H, L, d, dt, dev = _sizes(what, "X", X)
     shape = X.shape
-    made = []
     if dX is None:
         dX = torch.empty_like(X, memory_format=_PLAIN)
-        made.append(dX)
     if weight_grads:
         if dgamma is None:
             dgamma = torch.empty(d, dtype=torch.float32, device=X.device)
-            made.append(dgamma)
         if dbeta is None:
             dbeta = torch.empty(d, dtype=torch.float32, device=X.device)
-            made.append(dbeta)
         if workspace is None:
             workspace = torch.empty(bwd_layer_norm_workspace_bytes(B, H, L, d, dt), dtype=torch.uint8, device=X.device)
-            made.append(workspace)
     elif dgamma is not None or dbeta is not None:
         raise FavorError(f"{what}: dgamma or dbeta given with weight_grads=False")
     ws, nbytes = None, 0
@@ -260,7 +264,7 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise FavorError(f"{what}: the workspace must be contiguous on cuda:{dev}")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(what, dev, stream, made,
+    _call(what, dev,
           (*_views(what, ("X", "dY", "dX"), (X, dY, dX), shape, dt, dev),
            *_flats(what, ("gamma", "dgamma", "dbeta"), (gamma, dgamma, dbeta), (d,), dev), eps, B, H, L, d, _DT[dt],
            ws, nbytes))
@@ -296,7 +300,9 @@ def _sections(sections):
     return sections, (ctypes.c_int * len(sections))(*sections), sum(sections)
 
 
-def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
+def _rotary(Q, K, what, pos, table, sections, pairing, Qo, Ko, stream):
+    if stream is not None:
+        return _on(stream, _rotary, Q, K, what, pos, table, sections, pairing, Qo, Ko, None)
     B, Hq, L, d, dt, dev = _sizes(what, "Q", Q, True)
     sections, c_sections, pairs = _sections(sections if type(sections) is tuple else tuple(sections))
     pairing = PAIRINGS.get(pairing)
@@ -306,10 +312,8 @@ def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
     if (pos.dtype is not torch.int32 or pos.get_device() != dev or not pos.is_contiguous()
             or (pos.shape != (n, B, L) and pos.shape != (n, 1, L))):
         raise FavorError(f"{what}: positions must be contiguous int32 [{n}, {B} or 1, {L}] on cuda:{dev}")
-    made = []
     if Qo is None:
         Qo = torch.empty_like(Q, memory_format=_PLAIN)
-        made.append(Qo)
     views = _views(what, ("Q", "Q's output"), (Q, Qo), Q.shape, dt, dev)
     Hk = 0
     if K is not None:
@@ -319,13 +323,12 @@ def _rotary(what, Q, K, pos, table, sections, pairing, Qo, Ko, stream):
         shape = (B, Hk, L, d)
         if Ko is None:
             Ko = torch.empty_like(K, memory_format=_PLAIN)
-            made.append(Ko)
         views += _views(what, ("K", "K's output"), (K, Ko), shape, dt, dev)
     elif Ko is None:
         views += (None, None, None, None)
     else:
         raise FavorError(f"{what}: an output for keys without keys")
-    _call(what, dev, stream, made,
+    _call(what, dev,
           (*views, B, Hq, Hk, L, d, pos.data_ptr(), pos.shape[1], n, c_sections,
            *_flats(what, ("the table (new_rotary_table)",), (table,), (pairs,), dev, torch.int64), pairing, _DT[dt]))
     return Qo, Ko
@@ -338,10 +341,10 @@ def fwd_rotary(Q, K, pos, table, sections, pairing="adjacent", Qo=None, Ko=None,
     (channels 2p and 2p + 1) or "halves" (p and p + pairs); channels behind
     the pairs are copied.  Returns (Qo, Ko), contiguous where none is given;
     Qo may be Q, Ko may be K."""
-    return _rotary("favor_fwd_rotary", Q, K, pos, table, sections, pairing, Qo, Ko, stream)
+    return _rotary(Q, K, "favor_fwd_rotary", pos, table, sections, pairing, Qo, Ko, stream)
 
 
 def bwd_rotary(dQo, dKo, pos, table, sections, pairing="adjacent", dQ=None, dK=None, stream=None):
     """Gradients (dQ, dK) of fwd_rotary's inputs for those of its outputs: the
     rotation by the opposite angles; arguments as there."""
-    return _rotary("favor_bwd_rotary", dQo, dKo, pos, table, sections, pairing, dQ, dK, stream)
+    return _rotary(dQo, dKo, "favor_bwd_rotary", pos, table, sections, pairing, dQ, dK, stream)

@@ -528,6 +528,36 @@ def test_calls_on_another_stream(cuda_lib):
             del junk
 
 
+def test_outputs_on_another_stream_keep_off_the_current_ones_memory(cuda_lib):
+    # a tensor of the current stream is freed while that stream has yet to read
+    # it: what a call on another stream allocates must not take its place
+    f = cuda_lib
+    shape = (1, 4, 4096, 64)
+    x, g, dh, h0, _ = (t.cuda() for t in scan_inputs(shape, F32, 1))
+    w = torch.ones(64, device="cuda")
+    pos = torch.arange(4096, device="cuda", dtype=torch.int32).view(1, 1, -1)
+    table, new = f.new_rotary_table((32,)), torch.empty_like(h0)
+    side = torch.cuda.Stream()
+    calls = [lambda: f.fwd_gated_scan(x, g, stream=side), lambda: f.bwd_gated_scan(g, x, dh, stream=side),
+             lambda: f.fwd_layer_norm(x, w, stream=side), lambda: f.bwd_layer_norm(x, dh, w, stream=side),
+             lambda: f.fwd_rotary(x, dh, pos, table, (32,), stream=side),
+             lambda: f.gated_scan_step(h0, h0, h0, new_state=new, stream=side)]
+    for call in calls:
+        for _ in range(2):
+            torch.cuda.synchronize()
+            olds = [torch.full(shape, 3.0, device="cuda") for _ in range(4)]
+            olds += [torch.full((1, 4, 64), 3.0, device="cuda") for _ in range(3)]
+            kept = [torch.empty_like(o) for o in olds]
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)                        # about 10 ms before the copies
+            for a, b in zip(kept, olds):
+                a.copy_(b)
+            del olds, a, b
+            call()
+            torch.cuda.synchronize()
+            assert all((k == 3.0).all() for k in kept)
+
+
 def test_two_host_threads_at_once(cuda_lib):
     # each with its own stream and tensors
     ts = [_tensors(cuda_lib, seed) for seed in (7, 8)]
@@ -627,7 +657,8 @@ def test_refusals_of_the_binding(cuda_lib):
         lambda: f.fwd_rotary(x, x, pos[:1], t["table"], (16, 16)), lambda: f.fwd_rotary(x, x, pos, t["table"], (20, 20)),
         lambda: f.fwd_rotary(x, x, pos, t["table"].double(), (16, 16)),
         lambda: f.fwd_rotary(x, x, pos, t["table"], (16, 16), pairing="other"),
-        lambda: f.fwd_rotary(x, x[:1], pos, t["table"], (16, 16)), lambda: f.fwd_rotary(x, x[0], pos, t["table"], (16, 16)),
+        lambda: f.fwd_rotary(x, x[:1], pos, t["table"], (16, 16)),
+        lambda: f.fwd_rotary(x, x[0], pos, t["table"], (16, 16)),
         lambda: f.fwd_rotary(x, None, pos, t["table"], (16, 16), Ko=x),
         lambda: f.fwd_rotary(x, g, pos, t["table"], (16, 16), Qo=g),
         lambda: f.fwd_rotary(x, x, pos.expand(2, 2, 8)[:, :, ::2], t["table"], (16, 16)),
