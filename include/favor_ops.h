@@ -16,7 +16,7 @@
  *    Offsets are 64-bit: tensors beyond 2^31 elements are fine.
  *  - Pointers are aligned to their element.  Tensors whose pointers and
  *    strides are multiples of 16 bytes and whose rows are whole 16-byte
- *    pieces run on the vectorised kernels, all others on scalar ones.
+ *    pieces run fastest, then those made of two elements, then all others.
  *  - An output may be the very input it replaces (same pointer and strides)
  *    where the call says so.  Any other overlap of an output with an input
  *    or another output is FAVOR_ERR_INVALID_ARG; two views with the same

@@ -46,7 +46,8 @@ def gen(seed):
 def view(t, layout, g=None):
     """The values of t [B, H, L, d] on the GPU in a memory layout: "plain";
     "tokens", a view of [B, L, H, d]; "joint", one of three parts of
-    [B, L, 3, H, d]; "odd", rows of d + 3 starting one element in."""
+    [B, L, 3, H, d]; "even", rows of d + 2 starting two elements in; "odd",
+    rows of d + 3 starting one element in."""
     t = t.cuda()
     B, H, L, d = t.shape
     if layout == "plain":
@@ -57,13 +58,14 @@ def view(t, layout, g=None):
         buf = torch.full((B, L, 3, H, d), float("nan"), dtype=t.dtype, device="cuda")
         out = buf[:, :, 1].transpose(1, 2)
     else:
-        buf = torch.full((B, H, L, d + 3), float("nan"), dtype=t.dtype, device="cuda")
-        out = buf[..., 1:d + 1]
+        more, at = (2, 2) if layout == "even" else (3, 1)
+        buf = torch.full((B, H, L, d + more), float("nan"), dtype=t.dtype, device="cuda")
+        out = buf[..., at:] if layout == "even" else buf[..., at:d + at]
     out.copy_(t)
     return out
 
 
-LAYOUTS = ["plain", "tokens", "joint", "odd"]
+LAYOUTS = ["plain", "tokens", "joint", "even", "odd"]
 
 
 # ---- gated scan -----------------------------------------------------------------
@@ -124,7 +126,7 @@ def test_gated_scan_layouts(cuda_lib, dtype, layout, shape):
     for name, got, ref, b in zip(("dx", "dg", "dh0"), (dx, dg, dh0), orc.gated_scan_grad(G, hn, D),
                                  orc.gated_scan_grad_bound(G, hn, D)):
         close(got, ref, b, name)
-    if layout in ("joint", "odd"):                                # what lies between the rows is left as it was
+    if layout in ("joint", "even", "odd"):                                # what lies between the rows is left as it was
         for t in (out, dxo, dgo):
             whole = t._base
             assert int(torch.isnan(whole).sum()) == whole.numel() - t.numel()
@@ -302,7 +304,7 @@ def test_layer_norm_layouts_and_in_place(cuda_lib, dtype, layout, shape):
             assert torch.equal(a, b)
     cuda_lib.fwd_layer_norm(xv, wd, zd, Y=xv)
     assert torch.equal(xv, y)
-    if layout in ("joint", "odd"):
+    if layout in ("joint", "even", "odd"):
         for t in (out, xv):
             assert int(torch.isnan(t._base).sum()) == t._base.numel() - t.numel()
 
@@ -430,7 +432,7 @@ def test_rotary_layouts_and_in_place(cuda_lib, dtype, halves, layout, case):
         for t in (got[i], plain[i], (qv, kv)[i]):
             close(t, to_np(want[i]), b)
     assert plain[0].is_contiguous() and plain[1].is_contiguous()
-    if layout in ("joint", "odd"):
+    if layout in ("joint", "even", "odd"):
         for t in (qo, ko, qv, kv):
             assert int(torch.isnan(t._base).sum()) == t._base.numel() - t.numel()
 
