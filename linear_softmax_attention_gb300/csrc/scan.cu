@@ -455,9 +455,10 @@ __global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint
           *reinterpret_cast<Raw*>(po + (int64_t)i * lo) = P::pack(c);
         }
       }
-      if (!BACK || none(odd)) return;
+      // forward: a state that grew out of fp32 inside the run is no more finite at its end
+      if (none(BACK ? odd : residue(c, odd))) return;
     }
-    // the others, and those whose dg an h that is not finite has touched
+    // the others, those whose state overflows and those whose dg an h that is not finite has touched
     if (!ln.valid) return;
     Vec<V> c = in;
 #pragma unroll

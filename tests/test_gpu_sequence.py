@@ -165,6 +165,34 @@ def test_gated_scan_closed_gates_stop_infinities_and_nan(cuda_lib, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 7])
+def test_gated_scan_closed_gates_stop_an_overflow(cuda_lib, dtype, d):
+    """Finite inputs whose sum leaves fp32 inside a run: infinite as far as the next closed gate."""
+    shape, top = (1, 2, 2100, d), 3e38
+    x, g = torch.ones(shape, dtype=dtype, device="cuda"), torch.zeros(shape, dtype=dtype, device="cuda")
+    x[:, :, :102] = 0
+    x[:, :, 100] = top
+    g[:, :, 102] = -float("inf")
+    h0 = torch.full((1, 2, d), top, device="cuda")
+    h, hT = cuda_lib.fwd_gated_scan(x, g, h0=h0)
+    count = torch.arange(1, 2100 - 102 + 1, device="cuda", dtype=F32)
+    assert torch.equal(h[:, :, 102:], count.to(dtype)[:, None].expand(1, 2, -1, d))     # whole numbers: exact
+    assert torch.equal(hT, torch.full_like(h0, 2100 - 102))
+    assert torch.isinf(h[:, :, 100:102]).all() and (h[:, :, :100] == torch.tensor(top, dtype=dtype)).all()
+    # against time: the gradients behind token 102 grow too large at 104 and count from 101 down again
+    dh = torch.ones(shape, dtype=dtype, device="cuda")
+    dh[:, :, 103:] = 0
+    dh[:, :, 104] = top
+    h = torch.zeros_like(x)
+    dx, dg, dh0 = cuda_lib.bwd_gated_scan(g, h, dh, dhT=h0)
+    count = torch.arange(102, 0, -1, device="cuda", dtype=F32)
+    assert torch.equal(dx[:, :, :102], count.to(dtype)[:, None].expand(1, 2, -1, d))
+    assert torch.equal(dh0, torch.full_like(dh0, 102))
+    assert torch.isinf(dx[:, :, 102:105]).all() and (dx[:, :, 105:] == torch.tensor(top, dtype=dtype)).all()
+    assert (dg[:, :, :103] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gated_scan_padding_in_place_and_broadcast_gate(cuda_lib, dtype):
     shape = (2, 3, 333, 16)
     x, g, dh, h0, _ = scan_inputs(shape, dtype, 3)
