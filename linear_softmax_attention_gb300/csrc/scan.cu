@@ -330,6 +330,10 @@ __global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint
     const int v = warp - W;
     const float carry = join<V, MW>(sm, reinterpret_cast<Map(*)[32]>(ring_bytes), v, steps, K, W, rank, lane, first,
                                 tc::WaitCtx{&sm.abort_flag, p.status});
+    // A CTA whose wait ran out keeps its shared memory until the others of its
+    // cluster have ended, whose maps may still be on their way to it (threads
+    // that have exited count as arrived).
+    if (K > 1 && __any_sync(0xffffffffu, *static_cast<volatile int*>(&sm.abort_flag))) tc::cluster_sync();
     // tokens behind the last one are identities: carry is the state after it
     if (p.last != nullptr && rank == 0 && ln.valid) p.last[ch + v] = carry;
     return;
