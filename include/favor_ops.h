@@ -143,7 +143,7 @@ size_t favor_bwd_layer_norm_workspace_bytes(int B, int H, int L, int d, favor_dt
  *    their sum is P >= 1, 2 P <= d.
  *  - pairing: FAVOR_PAIR_ADJACENT (channels 2p and 2p + 1) or
  *    FAVOR_PAIR_HALVES (channels p and p + P).
- * Supported: B Hq L and B Hk L < 2^31, d <= 16384.
+ * Supported: B Hq L and B Hk L < 2^31, Hq + Hk <= 2^31 - 16, d <= 16384.
  */
 typedef enum favor_pairing { FAVOR_PAIR_ADJACENT = 0, FAVOR_PAIR_HALVES = 1 } favor_pairing;
 #define FAVOR_ROTARY_MAX_AXES 4

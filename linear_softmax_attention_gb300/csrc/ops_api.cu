@@ -216,8 +216,9 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   if (pairs < 1 || 2 * pairs > d) return FAVOR_ERR_INVALID_ARG;
   const int64_t lim = int64_t(1) << 31;
   if (d > favor::kNormMaxD || (int64_t)B * Hq >= lim || (int64_t)B * Hq * L >= lim) return FAVOR_ERR_UNSUPPORTED;
-  if (keys && ((int64_t)Hq + Hk >= lim || (int64_t)B * Hk >= lim || (int64_t)B * Hk * L >= lim))
-    return FAVOR_ERR_UNSUPPORTED;
+  if (keys && ((int64_t)B * Hk >= lim || (int64_t)B * Hk * L >= lim)) return FAVOR_ERR_UNSUPPORTED;
+  // the kernels' steps over the heads stay inside 32 bits
+  if ((int64_t)Hq + (keys ? Hk : 0) > lim - 16) return FAVOR_ERR_UNSUPPORTED;
   const int e = elem(dt);
   View vq, vqo, vk{}, vko{};
   if (!favor::make_view(&vq, q, qs, B, Hq, L, d, e) || !favor::make_view(&vqo, qo, qos, B, Hq, L, d, e))

@@ -2,9 +2,10 @@
 //
 // Bound by memory: every channel is read and written once.  A thread takes one
 // piece of a token's channels, 16 bytes or two elements (two pieces where the
-// pairs are halves apart), in every head of its share: the sines and cosines of the token are formed
-// once and used for all of them, and the heads' loads are in flight together.
-// The heads are shared out over more threads only where the tokens are few.
+// pairs are halves apart), in every head of its share: the sines and cosines
+// of the token are formed once and used for all of them, and the heads' loads
+// are in flight together.  The heads are shared out over more threads only
+// where the tokens are few.
 //
 // Measured (one GB300; copy rate 6770 GB/s): 2 x 12288 tokens x (8 + 8) heads
 // of 64 fp32 34.0 us, 5.9 TB/s; 65536 tokens x (16 + 4) heads of 128 bf16 on

@@ -169,6 +169,8 @@ def test_rotary_refusals(lib, name):  # noqa: F811
     assert call(qo=0x6000) == BAD                           # over the table
     assert call(d=20000) == UNSUPPORTED
     assert call(Hq=1 << 16, L=1 << 15) == UNSUPPORTED
+    assert call(B=1, Hq=(1 << 31) - 9, L=1, k=None, ko=None, Hk=0) == UNSUPPORTED
+    assert call(B=1, Hq=(1 << 31) - 19, L=1, Hk=4) == UNSUPPORTED
 
 
 @no_gpu
