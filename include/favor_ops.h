@@ -45,10 +45,13 @@ extern "C" {
  * run of tokens is applied as one map).  Where exp(g_t)
  * is 0 in fp32 (minus infinity, the type's lowest value) the state is
  * dropped, h_t = x_t, whatever it was, infinities and NaN included: such a
- * gate starts a new sequence packed into the same row.  (A state that decays
- * below fp32 over many tokens counts as 0 as well.)  A token with g = 0 and
- * x = 0 carries the state over, which is how padding behind a short sequence
- * leaves hT at its last token.
+ * gate starts a new sequence packed into the same row.  Infinities and NaN end
+ * there alone.  The gates of a run of tokens are multiplied in fp32 before they
+ * meet the state (the runs, of at most 96 tokens, follow the shape, the
+ * tensors' alignment and the device): a product below fp32's normal numbers has
+ * fewer bits or is 0, so that a finite state h is off by at most 2^-143 |h|.
+ * A token with g = 0 and x = 0 carries the state over, which is how padding
+ * behind a short sequence leaves hT at its last token.
  * h0: fp32 [B, H, d] contiguous, NULL for zeros.  hT: the same, NULL if not
  * wanted; hT may be h0.  h may be x or g.  h is rounded to dt once, the
  * state is carried in fp32.  dev_status: a bounded wait of a cluster's CTAs

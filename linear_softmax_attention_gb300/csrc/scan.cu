@@ -79,8 +79,12 @@ __device__ __forceinline__ Vec<V> residue(const Vec<V>& a, const Vec<V>& r) {
   for (int v = 0; v < V; ++v) zero.f[v] = 0.f;
   return fma_(a, zero, r);
 }
-__device__ __forceinline__ bool none(const Vec<1>& r) { return r.f[0] == 0.f; }
-__device__ __forceinline__ bool none(const Vec<2>& r) { return r.f[0] + r.f[1] == 0.f; }
+__device__ __forceinline__ float sum(const Vec<1>& r) { return r.f[0]; }
+__device__ __forceinline__ float sum(const Vec<2>& r) { return r.f[0] + r.f[1]; }
+__device__ __forceinline__ float product(const Vec<1>& r) { return r.f[0]; }
+__device__ __forceinline__ float product(const Vec<2>& r) { return r.f[0] * r.f[1]; }
+template <int V>
+__device__ __forceinline__ bool none(const Vec<V>& r) { return sum(r) == 0.f; }
 template <int V>
 __device__ __forceinline__ bool finite(const Vec<V>& a) {
   Vec<V> zero;
@@ -145,18 +149,25 @@ __device__ __forceinline__ void wait_but() {
 }
 
 // ---- joining the runs ----------------------------------------------------------------------
-// The map (A, s) of one channel
+// The map (A, s) of one channel.  A = -0: a closed gate, what was before is
+// dropped.  A = +0: open gates whose product is below fp32; nothing finite gets
+// through, but infinities and NaN do.  Where one of several gates is closed the
+// product of their A is a 0, and the "or" of their signs its sign.
 struct alignas(8) Map {
   float A, s;
 };
-// after `m`, the map `x`
-__device__ __forceinline__ Map then(const Map& m, const Map& x) { return {m.A * x.A, fmaf(x.A, m.s, x.s)}; }
-// the same where infinities or NaN are about: a closed gate drops what was before it
-__device__ __forceinline__ float through(const Map& x, float h) { return x.A == 0.f ? x.s : fmaf(x.A, h, x.s); }
-__device__ __forceinline__ Map then_checked(const Map& m, const Map& x) {
-  return {x.A == 0.f ? 0.f : m.A * x.A, through(x, m.s)};
-}
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+__device__ __forceinline__ bool closed(float A) { return __float_as_uint(A) == 0x80000000u; }
+__device__ __forceinline__ uint32_t sign(float A) { return __float_as_uint(A) & 0x80000000u; }
+// after `m`, the map `x` (signs are set once all are multiplied)
+__device__ __forceinline__ Map then(const Map& m, const Map& x) { return {m.A * x.A, fmaf(x.A, m.s, x.s)}; }
+// the same where infinities or NaN are about
+__device__ __forceinline__ float through(const Map& x, float h) {
+  return closed(x.A) ? x.s : fmaf(x.A == 0.f && !finite(h) ? 1.f : x.A, h, x.s);
+}
+__device__ __forceinline__ Map then_checked(const Map& m, const Map& x) {
+  return {closed(x.A) ? -0.f : m.A * x.A, through(x, m.s)};
+}
 
 // A map into another CTA of the cluster, counted there by the barrier `bar`.
 // (A cluster barrier with release semantics instead would wait, every step,
@@ -211,9 +222,13 @@ __device__ float join(Joint<V, MW>& sm, Map (*cta)[32], int v, int steps, int K,
     float h = carry;
     if (K > 1) {
       Map total = m[0];
+      uint32_t shut = sign(m[0].A);
 #pragma unroll
       for (int w = 1; w < MW; ++w)
-        if (w < W) total = then(total, m[w]);
+        if (w < W) {
+          total = then(total, m[w]);
+          shut |= sign(m[w].A);
+        }
       // 0 times an infinity or NaN is NaN and stays so: only then are closed gates looked for
       if (!(finite(total.s) && finite(total.A))) {
         total = m[0];
@@ -221,6 +236,7 @@ __device__ float join(Joint<V, MW>& sm, Map (*cta)[32], int v, int steps, int K,
         for (int w = 1; w < MW; ++w)
           if (w < W) total = then_checked(total, m[w]);
       }
+      total.A = __uint_as_float((__float_as_uint(total.A) & 0x7fffffffu) | shut);
       const uint32_t at = tc::smem_addr(&there[rank][lane]) - me, bar_at = tc::smem_addr(bar) - me;
 #pragma unroll 1
       for (int r0 = 0; r0 < K; r0 += kFold) {
@@ -415,17 +431,28 @@ __global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint
       A = mul_(A, a[i]);
     }
     // An infinity or NaN lives on in s and A to the end of the run (0 times it
-    // is NaN): only then is each token looked at for a closed gate.
-    const bool plain = none(residue(s, residue(A, all<V>(0.f))));
-    if (!plain) {
-      A = all<V>(1.f);
-      s = all<V>(0.f);
+    // is NaN): only then, or where a product is 0, is each gate looked at.
+    const Vec<V> r = residue(s, residue(A, all<V>(0.f)));
+    bool plain = true;
+    if (!(product(A) > sum(r))) {
+      plain = sum(r) == 0.f;
+      if (!plain) {
+        A = all<V>(1.f);
+        s = all<V>(0.f);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const Vec<V> x = get(stage, 1, i);
-        if constexpr (BACK) s = apply(a[i], all<V>(0.f), add_(x, s));
-        else s = apply(a[i], x, s);
-        A = apply(a[i], all<V>(0.f), A);
+        for (int i = 0; i < R; ++i) {
+          const Vec<V> x = get(stage, 1, i);
+          if constexpr (BACK) s = apply(a[i], all<V>(0.f), add_(x, s));
+          else s = apply(a[i], x, s);
+          A = apply(a[i], all<V>(0.f), A);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        bool shut = false;
+#pragma unroll
+        for (int i = 0; i < R; ++i) shut = shut || a[i].f[v] == 0.f;
+        if (shut) A.f[v] = -0.f;
       }
     }
     if (W > 1) {
@@ -510,11 +537,10 @@ __global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint
 #pragma unroll
       for (int v = 0; v < V; ++v) in.f[v] = p.first[ch + v];
     finish(0, u, a, in, plain);
-    const Vec<V> end = apply(A, s, in);
     wait_but<0>();
     if (p.last != nullptr && ln.valid)
 #pragma unroll
-      for (int v = 0; v < V; ++v) p.last[ch + v] = end.f[v];
+      for (int v = 0; v < V; ++v) p.last[ch + v] = through(Map{A.f[v], s.f[v]}, in.f[v]);
     return;
   }
   int stage = 0, n = 0;

@@ -1,0 +1,57 @@
+"""The sequence operators where their inputs leave the ordinary range, against
+the fp64 oracle, with the tolerances of ``test_gpu_sequence``."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from helpers import to_np
+from test_gpu_sequence import BF16, F32, close, scan_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", [-0.5, -2.0, -6.0, -14.0])
+@pytest.mark.parametrize("L,d", [(7, 5), (20, 64), (3000, 8), (3000, 7), (60, 64)])
+def test_open_gates_pass_infinities_and_nan_on(cuda_lib, dtype, low, L, d):
+    """Gates whose products over a few tokens are below fp32 and which are
+    open all the same: an infinity or NaN ends at a closed gate alone."""
+    shape = (1, 3, L, d)
+    x, g, dh, h0, dhT = scan_inputs(shape, dtype, L)
+    g[:] = low
+    at, shut = L // 3, L - L // 4
+    g[:, :, shut] = -float("inf")
+    x[:, 0, at], x[:, 1, at], h0[:, 2] = float("inf"), float("nan"), -float("inf")
+    X, G, S = to_np(x), to_np(g), to_np(h0)
+    h, hT = cuda_lib.fwd_gated_scan(x.cuda(), g.cuda(), h0=h0.cuda())
+    with np.errstate(invalid="ignore"):
+        want, last = orc.gated_scan(X, G, S)
+        bound = orc.gated_scan_bound(X, G, S)
+        assert np.isposinf(want[:, 0, at:shut]).all() and np.isfinite(want[:, :, shut:]).all()
+        # behind the closed gate what came before does not count
+        bound[:, :, shut:] = orc.gated_scan_bound(X[:, :, shut:], G[:, :, shut:])
+        close(h, want, bound, "h")
+        close(hT, last, bound[:, :, -1], "hT")
+    # against time: from a late token to the closed gate, and from in front of it to the first token
+    g[:, :, shut], g[:, :, at] = low, -float("inf")
+    dh[:, 0, shut], dh[:, 1, shut], dhT[:, 2] = -float("inf"), float("nan"), float("inf")
+    dh[:, 0, at // 2] = float("inf")
+    G, D, E = to_np(g), to_np(dh), to_np(dhT)
+    hn = torch.ones_like(x)
+    dx, dg, dh0 = cuda_lib.bwd_gated_scan(g.cuda(), hn.cuda(), dh.cuda(), dhT=dhT.cuda())
+    with np.errstate(invalid="ignore"):
+        refs = orc.gated_scan_grad(G, to_np(hn), D, dhT=E)
+        assert np.isposinf(refs[0][:, 2, at:]).all() and np.isfinite(refs[0][:, 1:, :at]).all()
+        assert np.isposinf(refs[2][:, 0]).all()
+        bounds = [np.nan_to_num(b, nan=0.0, posinf=0.0) for b in
+                  orc.gated_scan_grad_bound(G, to_np(hn), D, dhT=E)]
+        short = orc.gated_scan_grad_bound(G[:, :, :at], to_np(hn)[:, :, :at], np.nan_to_num(D[:, :, :at], posinf=0.0))
+        for b, c in zip(bounds, short):
+            if b.ndim == 4:
+                b[:, :, :at] = c
+            else:
+                b[:] = c
+        for name, got, ref, b in zip(("dx", "dg", "dh0"), (dx, dg, dh0), refs, bounds):
+            close(got, ref, b, name)
