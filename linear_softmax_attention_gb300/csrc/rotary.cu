@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pieces_kernel(Work w) {
   const int64_t token = (int64_t)blockIdx.x * w.per_cta + within;
   if (within >= w.per_cta || token >= w.tokens) return;
   const int b = (int)w.l.div((uint32_t)token), t = (int)token - b * w.L;
-  const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
+  const int h0 = blockIdx.y * w.share, h1 = h0 + min(w.share, w.heads - h0);
   const Token<T> q(w.q, b, t), k(w.k, b, t);
   for (int item = threadIdx.x - within * items; item < items; item += kThreads) {
     const int turning = HALVES ? w.P / E : 2 * w.P / E;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(Work w, bool hal
   const int64_t token = (int64_t)blockIdx.x * w.per_cta + within;
   if (within >= w.per_cta || token >= w.tokens) return;
   const int b = (int)w.l.div((uint32_t)token), t = (int)token - b * w.L;
-  const int h0 = blockIdx.y * w.share, h1 = min(w.heads, h0 + w.share);
+  const int h0 = blockIdx.y * w.share, h1 = h0 + min(w.share, w.heads - h0);
   const Token<T> q(w.q, b, t), k(w.k, b, t);
   for (int p = threadIdx.x - within * items; p < items; p += kThreads) {
     const bool turns = p < w.P;
@@ -303,7 +303,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, int piece, cudaStream_
   const int64_t parts = std::min<int64_t>(std::min(w.heads, 65535), std::max<int64_t>(1, want / threads));
   w.share = (int)((w.heads + parts - 1) / parts);
   const dim3 grid((unsigned)(((int64_t)w.tokens + w.per_cta - 1) / w.per_cta),
-                  (unsigned)((w.heads + w.share - 1) / w.share));
+                  (unsigned)(((int64_t)w.heads + w.share - 1) / w.share));
   using B16 = __nv_bfloat16;
   if (E == 1) {
     if (bf16) rotary_pairs_kernel<B16><<<grid, kThreads, 0, stream>>>(w, a.halves);

@@ -55,3 +55,18 @@ def test_open_gates_pass_infinities_and_nan_on(cuda_lib, dtype, low, L, d):
                 b[:] = c
         for name, got, ref, b in zip(("dx", "dg", "dh0"), (dx, dg, dh0), refs, bounds):
             close(got, ref, b, name)
+
+
+@pytest.mark.parametrize("d,P", [(2, 1), (10, 5)])
+def test_rotary_as_many_heads_as_there_may_be(cuda_lib, d, P):
+    # the steps from share to share of the heads end just below 2^31; d = 10: 43 GB, in place
+    H = (1 << 31) - 16
+    free, _ = torch.cuda.mem_get_info()
+    assert free > 60 << 30
+    x = torch.ones((1, H, 1, d), dtype=BF16, device="cuda")
+    pos = torch.ones((1, 1, 1), dtype=torch.int32, device="cuda")
+    table = cuda_lib.new_rotary_table((P,), freqs=[0.5 * np.pi] * P)         # a quarter turn: (1, 1) -> (-1, 1)
+    y, _ = cuda_lib.fwd_rotary(x, None, pos, table, (P,), Qo=x)
+    want = torch.tensor([-1.0, 1.0] * P, device="cuda").to(BF16)
+    for part in y.view(H, d).split(1 << 27):
+        assert bool((part == want).all())
