@@ -31,6 +31,23 @@ extern "C" {
 favor_status favor_selftest_wait_timeout(int32_t* status, int32_t* returned, int64_t* times_ns,
                                          void* stream);
 
+/*
+ * favor_selftest_scan_timeout — favor_fwd_gated_scan (favor_ops.h; contiguous
+ * tensors, no initial state) with another limit of the waits inside a cluster,
+ * `wait_cycles` SM cycles (0 to the library's 2.2e9; 0: every wait runs out at
+ * once), and with every wait of the CTA of rank `quits` of each cluster running
+ * out at once (-1: of none).  A wait that runs out stores FAVOR_ERR_TIMEOUT
+ * into *status (if it is still 0); h and hT are then wrong, and the kernel ends
+ * all the same: the CTA goes on without its cluster, and the others' waits for
+ * it run out in turn.
+ *
+ * Errors: those of favor_fwd_gated_scan; FAVOR_ERR_INVALID_ARG for a NULL
+ * status or a limit outside its range.
+ */
+favor_status favor_selftest_scan_timeout(const void* x, const void* g, void* h, float* hT, int B, int H, int L,
+                                         int d, favor_dtype dt, int64_t wait_cycles, int quits, int32_t* status,
+                                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ __all__ = [
     "bwd_bidir", "bwd_causal", "bwd_workspace_bytes", "selftest_wait_timeout",
     "fwd_gated_scan", "bwd_gated_scan", "gated_scan_step", "new_gated_scan_state", "fwd_layer_norm",
     "bwd_layer_norm", "bwd_layer_norm_workspace_bytes", "fwd_rotary", "bwd_rotary", "new_rotary_table",
+    "selftest_scan_timeout",
 ]
 
 F32 = 0
@@ -362,4 +363,4 @@ def bwd_causal(Q, K, V, dO, omega, qk_scale, workspace=None, feature_map="prf", 
 from . import sequence                                                   # noqa: E402  (uses load and FavorError)
 from .sequence import (bwd_gated_scan, bwd_layer_norm, bwd_layer_norm_workspace_bytes, bwd_rotary,  # noqa: E402
                        fwd_gated_scan, fwd_layer_norm, fwd_rotary, gated_scan_step, new_gated_scan_state,
-                       new_rotary_table)
+                       new_rotary_table, selftest_scan_timeout)

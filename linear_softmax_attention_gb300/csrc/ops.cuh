@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "favor_ops.h"
+#include "tc_ptx.cuh"
 
 namespace favor {
 
@@ -126,6 +127,8 @@ struct ScanArgs {
   float* last;                        // hT (forward), dh0 (backward), or NULL
   int32_t* status;
   int B, H, L, d;
+  long long wait_cycles = tc::kWaitLimitCycles;   // limit of a wait inside a cluster
+  int quits = -1;                     // a CTA of each cluster whose waits run out at once (a test's), -1: none
 };
 // align: pieces of this many bytes (16, 4 or 2) make up every row of every tensor
 cudaError_t launch_scan(const ScanArgs& a, bool backward, bool bf16, int align, cudaStream_t stream);

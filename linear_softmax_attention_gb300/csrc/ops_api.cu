@@ -3,6 +3,7 @@
 #include <cmath>
 #include <initializer_list>
 
+#include "favor_selftest.h"
 #include "ops.cuh"
 
 namespace favor {
@@ -260,13 +261,9 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   return done(favor::launch_rotary(a, dt == FAVOR_BF16, piece, static_cast<cudaStream_t>(stream)));
 }
 
-}  // namespace
-
-extern "C" {
-
-favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides, const void* g, const int64_t* g_strides,
-                                  void* h, const int64_t* h_strides, const float* h0, float* hT, int B, int H, int L,
-                                  int d, favor_dtype dt, int32_t* dev_status, void* stream) {
+favor_status fwd_gated_scan(const void* x, const int64_t* x_strides, const void* g, const int64_t* g_strides,
+                            void* h, const int64_t* h_strides, const float* h0, float* hT, int B, int H, int L, int d,
+                            favor_dtype dt, long long wait_cycles, int quits, int32_t* dev_status, void* stream) {
   const favor_status st = sizes_ok(B, H, L, d, dt);
   if (st != FAVOR_OK) return st;
   if (!flat_ok(h0) || !flat_ok(hT)) return FAVOR_ERR_INVALID_ARG;
@@ -295,8 +292,29 @@ favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides, const
   a.H = H;
   a.L = L;
   a.d = d;
+  a.wait_cycles = wait_cycles;
+  a.quits = quits;
   return done(favor::launch_scan(a, false, dt == FAVOR_BF16, common_piece({&vx, &vg, &vh}),
                                  static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+favor_status favor_fwd_gated_scan(const void* x, const int64_t* x_strides, const void* g, const int64_t* g_strides,
+                                  void* h, const int64_t* h_strides, const float* h0, float* hT, int B, int H, int L,
+                                  int d, favor_dtype dt, int32_t* dev_status, void* stream) {
+  return fwd_gated_scan(x, x_strides, g, g_strides, h, h_strides, h0, hT, B, H, L, d, dt, favor::tc::kWaitLimitCycles,
+                        -1, dev_status, stream);
+}
+
+favor_status favor_selftest_scan_timeout(const void* x, const void* g, void* h, float* hT, int B, int H, int L, int d,
+                                         favor_dtype dt, int64_t wait_cycles, int quits, int32_t* status,
+                                         void* stream) {
+  if (status == nullptr || wait_cycles < 0 || wait_cycles > favor::tc::kWaitLimitCycles) return FAVOR_ERR_INVALID_ARG;
+  return fwd_gated_scan(x, nullptr, g, nullptr, h, nullptr, nullptr, hT, B, H, L, d, dt, wait_cycles, quits, status,
+                        stream);
 }
 
 favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides, const void* h, const int64_t* h_strides,

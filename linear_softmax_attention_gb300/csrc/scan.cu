@@ -178,6 +178,22 @@ __device__ __forceinline__ void send(uint32_t at, const Map& m, uint32_t bar) {
                : "memory");
 }
 
+// Bounded wait for the cluster's maps; `limit` cycles, 0: as if they were over.
+__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, long long limit, const tc::WaitCtx& ctx) {
+  const uint32_t a = tc::smem_addr(bar);
+  if (limit > 0) {
+    if (tc::mbar_try_wait(a, parity)) return true;
+    const long long t0 = tc::sm_cycles();
+    do {
+      if (tc::mbar_try_wait(a, parity)) return true;
+      if (*ctx.abort_flag) return false;
+    } while (tc::sm_cycles() - t0 <= limit);
+  }
+  *ctx.abort_flag = 1;
+  report_status(ctx.status, FAVOR_ERR_TIMEOUT);
+  return false;
+}
+
 template <int V, int MW>
 struct Joint {
   Map warp[2][V][MW][32];      // the runs' maps, from the workers
@@ -202,10 +218,14 @@ constexpr int kBarMaps = 1, kBarStates = 3;
 // maps only after they have read the states of the step two before, and a CTA
 // sends its map of step n + 2 only when it has every CTA's of step n + 1,
 // which they send after their reads of step n.  cta: the CTAs' maps,
-// [2][V][K][32].  Returns the state behind the last step.
+// [2][V][K][32].  Returns the state behind the last step.  After a wait that
+// ran out the warp only keeps its workers going: the barrier's phase is not
+// over, so it is not armed again, and a map of a later step could end the wait
+// of another CTA for this one.
 template <int V, int MW>
 __device__ float join(Joint<V, MW>& sm, Map (*cta)[32], int v, int steps, int K, int W, int rank, int lane, float carry,
-                      const tc::WaitCtx& ctx) {
+                      long long limit, const tc::WaitCtx& ctx) {
+  bool alive = true;
   const uint32_t me = tc::smem_addr(&sm);
   const uint32_t peer = K > 1 && lane < K ? tc::map_to_rank(me, lane) : 0;
   const int threads = (W + V) * 32;
@@ -213,14 +233,14 @@ __device__ float join(Joint<V, MW>& sm, Map (*cta)[32], int v, int steps, int K,
     const int buf = n & 1;
     Map(*const there)[32] = cta + (buf * V + v) * K;
     uint64_t* const bar = &sm.bar[buf][v];
-    if (K > 1 && lane == 0) tc::mbar_arrive_expect_tx(bar, K * 32 * (int)sizeof(Map));
+    if (K > 1 && alive && lane == 0) tc::mbar_arrive_expect_tx(bar, K * 32 * (int)sizeof(Map));
     bar_sync(kBarMaps + buf, threads);
     Map m[MW];
 #pragma unroll
     for (int w = 0; w < MW; ++w)
       if (w < W) m[w] = sm.warp[buf][v][w][lane];
     float h = carry;
-    if (K > 1) {
+    if (K > 1 && alive) {
       Map total = m[0];
       uint32_t shut = sign(m[0].A);
 #pragma unroll
@@ -247,7 +267,7 @@ __device__ float join(Joint<V, MW>& sm, Map (*cta)[32], int v, int steps, int K,
         for (int r = 0; r < kFold; ++r)
           if (r0 + r < K) send(to[r] + at, total, to[r] + bar_at);
       }
-      tc::mbar_wait(bar, (n >> 1) & 1, ctx);
+      alive = __all_sync(0xffffffffu, wait_maps(bar, (n >> 1) & 1, limit, ctx));
       float r = carry;
 #pragma unroll 1
       for (int c0 = 0; c0 < K; c0 += kFold) {
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint
   if (warp >= W) {                                    // there are no such warps where W = 1
     const int v = warp - W;
     const float carry = join<V, MW>(sm, reinterpret_cast<Map(*)[32]>(ring_bytes), v, steps, K, W, rank, lane, first,
-                                tc::WaitCtx{&sm.abort_flag, p.status});
+                                rank == p.quits ? 0 : p.wait_cycles, tc::WaitCtx{&sm.abort_flag, p.status});
     // A CTA whose wait ran out keeps its shared memory until the others of its
     // cluster have ended, whose maps may still be on their way to it (threads
     // that have exited count as arrived).

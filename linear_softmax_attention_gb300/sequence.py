@@ -46,6 +46,8 @@ def declare(lib):
                  "fwd_rotary", "bwd_rotary"):
         getattr(lib, "favor_" + name).restype = i
     lib.favor_bwd_layer_norm_workspace_bytes.restype = size
+    lib.favor_selftest_scan_timeout.argtypes = [vp] * 4 + [i] * 5 + [ctypes.c_int64, i, vp, vp]
+    lib.favor_selftest_scan_timeout.restype = i
 
 
 # Small calls are bound by the host's time, so the helpers below ask torch for
@@ -210,6 +212,20 @@ def gated_scan_step(x, g, state, o=None, new_state=None, stream=None):
           (*_flats(what, ("x", "g", "o"), (x, g, o), shape, dev, dt),
            *_flats(what, ("state", "new_state"), (state, new_state), shape, dev), B, H, d, _DT[dt]))
     return o, new_state
+
+
+def selftest_scan_timeout(X, G, wait_cycles, quits=-1):
+    """favor_selftest_scan_timeout: fwd_gated_scan of contiguous X and G with
+    another limit of its clusters' waits, and with those of CTA `quits` of each
+    cluster running out at once.  Returns (O, hT, status) after synchronising."""
+    what = "favor_selftest_scan_timeout"
+    B, H, L, d, dt, dev = _sizes(what, "X", X, True)
+    O = torch.empty_like(X, memory_format=_PLAIN)
+    hT = torch.empty((B, H, d), dtype=torch.float32, device=X.device)
+    status = torch.zeros(1, dtype=torch.int32, device=X.device)
+    _call(what, dev, (*_flats(what, ("X", "G", "O"), (X, G, O), X.shape, dev, dt), hT.data_ptr(), B, H, L, d, _DT[dt],
+                      wait_cycles, quits, status.data_ptr()))
+    return O, hT, int(status.item())
 
 
 def fwd_layer_norm(X, gamma=None, beta=None, eps=1e-5, Y=None, stream=None):

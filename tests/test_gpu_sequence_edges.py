@@ -70,3 +70,22 @@ def test_rotary_as_many_heads_as_there_may_be(cuda_lib, d, P):
     want = torch.tensor([-1.0, 1.0] * P, device="cuda").to(BF16)
     for part in y.view(H, d).split(1 << 27):
         assert bool((part == want).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 1, 6000, 64), (2, 40, 3000, 64)])
+@pytest.mark.parametrize("cycles,quits", [(0, -1), (2_000_000, 0), (2_000_000, 1)])
+def test_gated_scan_ends_when_its_clusters_waits_run_out(cuda_lib, dtype, shape, cycles, quits):
+    """Every wait, or those of one CTA of each cluster, as if over at once: the
+    others' (2 million cycles, a millisecond) run out in turn, the status says
+    so, and the calls after it are right."""
+    x, g, _, _, _ = (t.cuda() for t in scan_inputs(shape, dtype, 1))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want, last = cuda_lib.fwd_gated_scan(x, g, dev_status=status)
+    for _ in range(3):
+        assert cuda_lib.selftest_scan_timeout(x, g, cycles, quits)[2] == 4      # FAVOR_ERR_TIMEOUT
+        h, hT = cuda_lib.fwd_gated_scan(x, g, dev_status=status)
+        assert torch.equal(h, want) and torch.equal(hT, last)
+    h, hT, code = cuda_lib.selftest_scan_timeout(x, g, 2_200_000_000)           # the library's own limit
+    assert code == 0 and torch.equal(h, want) and torch.equal(hT, last)
+    assert int(status.item()) == 0

@@ -254,3 +254,12 @@ def test_binding_refuses_cpu_tensors():
                  lambda: favor.fwd_rotary(x, x, pos, table, (8,)), lambda: favor.bwd_rotary(x, None, pos, table, (8,))]:
         with pytest.raises(favor.FavorError, match="CUDA tensor"):
             call()
+
+
+def test_scan_timeout_hook_refusals(lib):  # noqa: F811
+    def call(x=0x1000, g=0x2000, h=0x3000, hT=0x5000, L=8, dt=0, cycles=0, status=0x6000):
+        return lib.favor_selftest_scan_timeout(x, g, h, hT, 1, 2, L, 8, dt, cycles, -1, status, None)
+
+    for bad in (dict(x=None), dict(g=None), dict(h=None), dict(status=None), dict(L=0), dict(dt=2), dict(cycles=-1),
+                dict(cycles=2_200_000_001), dict(hT=0x3000)):
+        assert call(**bad) == BAD
