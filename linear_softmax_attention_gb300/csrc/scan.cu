@@ -178,14 +178,15 @@ __device__ __forceinline__ void send(uint32_t at, const Map& m, uint32_t bar) {
                : "memory");
 }
 
-// Bounded wait for the cluster's maps; `limit` cycles, 0: as if they were over.
+// Bounded wait for the cluster's maps, which acquires what the other CTAs have
+// written; `limit` cycles, 0: as if they were over.
 __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, long long limit, const tc::WaitCtx& ctx) {
   const uint32_t a = tc::smem_addr(bar);
   if (limit > 0) {
-    if (tc::mbar_try_wait(a, parity)) return true;
+    if (tc::mbar_try_wait_cluster(a, parity)) return true;
     const long long t0 = tc::sm_cycles();
     do {
-      if (tc::mbar_try_wait(a, parity)) return true;
+      if (tc::mbar_try_wait_cluster(a, parity)) return true;
       if (*ctx.abort_flag) return false;
     } while (tc::sm_cycles() - t0 <= limit);
   }

@@ -4,7 +4,9 @@ the launch, which on a machine without a GPU is status 3; the tests that rely
 on that use addresses that are never followed and skip where a GPU is."""
 
 import ctypes
+import os
 import random
+import re
 
 import numpy as np
 import pytest
@@ -263,3 +265,12 @@ def test_scan_timeout_hook_refusals(lib):  # noqa: F811
     for bad in (dict(x=None), dict(g=None), dict(h=None), dict(status=None), dict(L=0), dict(dt=2), dict(cycles=-1),
                 dict(cycles=2_200_000_001), dict(hT=0x3000)):
         assert call(**bad) == BAD
+
+
+def test_waits_for_other_ctas_stores_acquire_at_cluster_scope():
+    # st.async from another CTA releases at cluster scope: a wait of CTA scope would not order the reads behind it,
+    # which no run shows
+    csrc = os.path.join(os.path.dirname(favor.__file__), "csrc")
+    scan = open(os.path.join(csrc, "scan.cu")).read()
+    assert "st.async" in scan and re.findall(r"mbar_(?:try_|test_)?wait\w*\(", scan)
+    assert set(re.findall(r"mbar_(?:try_|test_)?wait\w*", scan)) == {"mbar_try_wait_cluster"}
