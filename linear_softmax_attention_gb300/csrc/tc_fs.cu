@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) fs_output_kernel(const __grid_con
         if (wg == wg_fin) {
           // finalise my columns: every partial rescaled to the largest
           // reference; mine first, then the others in rank order
-          if (ok) ok = mbar_wait(&land_full[par], (j >> 1) & 1, wctx);
+          if (ok) ok = mbar_wait_cluster(&land_full[par], (j >> 1) & 1, wctx);
           const uint8_t* land = sm + C::kLand + par * C::kLandTile;
           float bmax = bias;
           for (int sl = 0; sl < NC - 1; ++sl)
@@ -1185,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1) fs_causal_kernel(const __grid_con
         if (wg == wg_fin) {
           // my columns: every partial rescaled to the largest reference; mine
           // first, then the others in rank order
-          if (ok) ok = mbar_wait(&land_full[buf], (j / C::NB) & 1, wctx);
+          if (ok) ok = mbar_wait_cluster(&land_full[buf], (j / C::NB) & 1, wctx);
           const uint8_t* land = sm + C::kLand + buf * C::kLandChunk;
           float bmax = bias;
           for (int sl = 0; sl < NC - 1; ++sl)

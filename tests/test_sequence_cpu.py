@@ -274,3 +274,5 @@ def test_waits_for_other_ctas_stores_acquire_at_cluster_scope():
     scan = open(os.path.join(csrc, "scan.cu")).read()
     assert "st.async" in scan and re.findall(r"mbar_(?:try_|test_)?wait\w*\(", scan)
     assert set(re.findall(r"mbar_(?:try_|test_)?wait\w*", scan)) == {"mbar_try_wait_cluster"}
+    fs = open(os.path.join(csrc, "tc_fs.cu")).read()
+    assert set(re.findall(r"(mbar_\w*wait\w*)\(&land_(?:full|free)", fs)) == {"mbar_wait_cluster"}
