@@ -205,11 +205,14 @@ struct Joint {
 
 // Hardware barriers between the workers and the joiners: "maps" of a step are
 // there (the joiners wait), "states" of a step are there (the workers wait);
-// two of each, by the step's parity.
+// two of each, by the step's parity.  The instructions want the warp together,
+// which lanes with and without infinities have left.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 constexpr int kBarMaps = 1, kBarStates = 3;
