@@ -473,10 +473,10 @@ __global__ void __launch_bounds__((MW + V) * 32, 2) scan_kernel(ScanArgs p, uint
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        bool shut = false;
+        float least = a[0].f[v];
 #pragma unroll
-        for (int i = 0; i < R; ++i) shut = shut || a[i].f[v] == 0.f;
-        if (shut) A.f[v] = -0.f;
+        for (int i = 1; i < R; ++i) least = fminf(least, a[i].f[v]);
+        if (least == 0.f) A.f[v] = -0.f;
       }
     }
     if (W > 1) {
