@@ -126,7 +126,7 @@ def _on(stream, fn, t, *args):
     """fn(t, *args) with `stream` as the current one of t's device: what is
     allocated there comes from that stream's memory, which no other stream's
     pending work reads.  The results may then be used on the stream that was
-    current before."""
+    current before, and the arguments let go: their memory waits for the call."""
     if not t.is_cuda or stream.device != t.device:
         raise FavorError(f"{fn.__name__}: the stream belongs to {stream.device}, the tensors to {t.device}")
     current = torch.cuda.current_stream(t.device)
@@ -134,6 +134,9 @@ def _on(stream, fn, t, *args):
         return fn(t, *args)
     with torch.cuda.stream(stream):
         out = fn(t, *args)
+    for a in (t, *args):
+        if isinstance(a, torch.Tensor):
+            a.record_stream(stream)
     for o in out if isinstance(out, tuple) else (out,):
         if o is not None:
             o.record_stream(current)

@@ -89,3 +89,36 @@ def test_gated_scan_ends_when_its_clusters_waits_run_out(cuda_lib, dtype, shape,
     h, hT, code = cuda_lib.selftest_scan_timeout(x, g, 2_200_000_000)           # the library's own limit
     assert code == 0 and torch.equal(h, want) and torch.equal(hT, last)
     assert int(status.item()) == 0
+
+
+def test_arguments_may_be_let_go_after_a_call_on_another_stream(cuda_lib):
+    # the other stream has yet to begin when the arguments are freed on the
+    # current one, whose next tensors of their sizes must not take their place
+    f = cuda_lib
+    shape = (1, 4, 4096, 64)
+    x, g, dh, h0, _ = (t.cuda() for t in scan_inputs(shape, F32, 1))
+    w = torch.ones(64, device="cuda")
+    pos = torch.arange(4096, device="cuda", dtype=torch.int32).view(1, 1, -1)
+    table = f.new_rotary_table((32,))
+    ws = torch.empty(f.bwd_layer_norm_workspace_bytes(1, 4, 4096, 64, F32), dtype=torch.uint8, device="cuda")
+    calls = [(f.fwd_gated_scan, (x, g, h0), {}), (f.bwd_gated_scan, (g, x, dh, h0, h0), {}),
+             (f.fwd_layer_norm, (x, w, w), {}), (f.bwd_layer_norm, (x, dh, w), dict(workspace=ws)),
+             (f.fwd_rotary, (x, dh, pos, table, (32,)), {}), (f.bwd_rotary, (x, dh, pos, table, (32,)), {}),
+             (f.gated_scan_step, (h0, h0, h0), {})]
+    side = torch.cuda.Stream()
+    clone = (lambda v: v.clone() if isinstance(v, torch.Tensor) else v)
+    for call, args, more in calls:
+        want = call(*map(clone, args), **{k: clone(v) for k, v in more.items()})
+        want = want if isinstance(want, tuple) else (want,)
+        a, kw = [clone(v) for v in args], {k: clone(v) for k, v in more.items()}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                        # about 10 ms
+        got = call(*a, **kw, stream=side)
+        sizes = [(v.shape, v.dtype) for v in (*a, *kw.values()) if isinstance(v, torch.Tensor)]
+        del a, kw
+        junk = [torch.full(s, 7, dtype=t, device="cuda") for s, t in sizes]
+        torch.cuda.synchronize()
+        for u, v in zip(got if isinstance(got, tuple) else (got,), want):
+            assert torch.equal(u, v), call.__name__
+        del junk
