@@ -123,7 +123,9 @@ favor_status favor_bwd_layer_norm(const void* x, const int64_t* x_strides,
                                   const float* gamma, float* dgamma, float* dbeta, float eps,
                                   int B, int H, int L, int d, favor_dtype dt,
                                   void* workspace, size_t ws_bytes, void* stream);
-/* 0 for arguments outside the supported shapes. */
+/* The size follows the current device's number of SMs: asked for with the
+ * device current that the call runs on.  0 for arguments outside the supported
+ * shapes. */
 size_t favor_bwd_layer_norm_workspace_bytes(int B, int H, int L, int d, favor_dtype dt);
 
 /*

@@ -248,7 +248,12 @@ def fwd_layer_norm(X, gamma=None, beta=None, eps=1e-5, Y=None, stream=None):
     return Y
 
 
-def bwd_layer_norm_workspace_bytes(B: int, H: int, L: int, d: int, dtype) -> int:
+def bwd_layer_norm_workspace_bytes(B: int, H: int, L: int, d: int, dtype, device=None) -> int:
+    """Bytes of bwd_layer_norm's workspace on `device` (None: the current
+    one), whose number of SMs it depends on."""
+    if device is not None and device != _current_device():
+        with torch.cuda.device(device):
+            return bwd_layer_norm_workspace_bytes(B, H, L, d, dtype)
     n = 0
     if min(B, H, L, d) > 0 and max(B, H, L, d) <= _INT:
         n = load().favor_bwd_layer_norm_workspace_bytes(B, H, L, d, _DT[dtype])
@@ -275,7 +280,8 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
         if dbeta is None:
             dbeta = torch.empty(d, dtype=torch.float32, device=X.device)
         if workspace is None:
-            workspace = torch.empty(bwd_layer_norm_workspace_bytes(B, H, L, d, dt), dtype=torch.uint8, device=X.device)
+            workspace = torch.empty(bwd_layer_norm_workspace_bytes(B, H, L, d, dt, dev), dtype=torch.uint8,
+                                    device=X.device)
     elif dgamma is not None or dbeta is not None:
         raise FavorError(f"{what}: dgamma or dbeta given with weight_grads=False")
     ws, nbytes = None, 0

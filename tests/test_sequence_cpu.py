@@ -276,3 +276,51 @@ def test_waits_for_other_ctas_stores_acquire_at_cluster_scope():
     assert set(re.findall(r"mbar_(?:try_|test_)?wait\w*", scan)) == {"mbar_try_wait_cluster"}
     fs = open(os.path.join(csrc, "tc_fs.cu")).read()
     assert set(re.findall(r"(mbar_\w*wait\w*)\(&land_(?:full|free)", fs)) == {"mbar_wait_cluster"}
+
+
+def test_layer_norm_workspace_is_sized_on_the_tensors_device(monkeypatch):
+    # devices of a process may differ in their number of SMs; a library and tensors that stand in for device 1,
+    # while device 0 is current
+    from linear_softmax_attention_gb300 import sequence
+
+    class OnDevice1(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    def tensor(*shape, dtype=torch.float32, device=None):
+        return torch.zeros(shape[0] if len(shape) == 1 and isinstance(shape[0], tuple) else shape,
+                           dtype=dtype).as_subclass(OnDevice1)
+
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Library:
+        def favor_bwd_layer_norm_workspace_bytes(self, *_):
+            seen.append(("size", current[0]))
+            return 4096 if current[0] == 1 else 256
+
+        def favor_bwd_layer_norm(self, *args):
+            seen.append(("call", current[0], args[-2]))
+            return 0
+
+    monkeypatch.setattr(sequence, "load", Library)
+    monkeypatch.setattr(sequence, "_current_device", lambda: current[0])
+    monkeypatch.setattr(sequence, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch, "empty", tensor)
+    x = tensor(1, 2, 8, 16)
+    favor.bwd_layer_norm(x, x)
+    assert seen == [("size", 1), ("call", 1, 4096)] and current == [0]
+    assert favor.bwd_layer_norm_workspace_bytes(1, 2, 8, 16, torch.float32) == 256
+    assert favor.bwd_layer_norm_workspace_bytes(1, 2, 8, 16, torch.float32, device=1) == 4096
