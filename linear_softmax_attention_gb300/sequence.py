@@ -296,9 +296,30 @@ def bwd_layer_norm(X, dY, gamma=None, eps=1e-5, dX=None, dgamma=None, dbeta=None
     return dX, dgamma, dbeta
 
 
+_PI_BITS = 1200          # frequencies are below 2^1024: beyond 2^64 turns' fraction of the largest
+
+
+@functools.lru_cache(maxsize=None)
+def _two_pi():
+    """2 pi 2^_PI_BITS in whole numbers, by Machin's formula."""
+    guard = 32
+    one = 1 << (_PI_BITS + guard)
+
+    def arctan_of_inverse(x):
+        total, power, k = 0, one // x, 1
+        while power:
+            total += power // k if k % 4 == 1 else -(power // k)
+            power //= x * x
+            k += 2
+        return total
+
+    return 8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)) >> guard
+
+
 def new_rotary_table(sections, base: float = 10000.0, freqs=None, device="cuda") -> torch.Tensor:
     """Table of the rotary calls: int64 [P] (the bits of a uint64), each pair's
-    fraction of a turn per unit of position, a turn being 2^64.  Pair j of an
+    fraction of a turn per unit of position, a turn being 2^64, rounded once
+    from the frequency in 64-bit floating point.  Pair j of an
     axis with n pairs turns by base^(-j / n) radians, or, with ``freqs`` (P
     numbers), pair p by freqs[p]."""
     sections = _sections(tuple(int(n) for n in sections))[0]
@@ -312,7 +333,9 @@ def new_rotary_table(sections, base: float = 10000.0, freqs=None, device="cuda")
     for f in freqs:
         if not math.isfinite(f):
             raise FavorError("new_rotary_table: frequencies must be finite")
-        word = round(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % (1 << 64)
+        n, m = f.as_integer_ratio()                  # n / m radians: 2^64 n / (m 2 pi), to the nearest
+        den = m * _two_pi()
+        word = ((n << (_PI_BITS + 65)) + den) // (2 * den) % (1 << 64)
         words.append(word - (1 << 64) if word >= 1 << 63 else word)
     return torch.tensor(words, dtype=torch.int64, device=device)
 

@@ -7,6 +7,7 @@ import ctypes
 import os
 import random
 import re
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -324,3 +325,12 @@ def test_layer_norm_workspace_is_sized_on_the_tensors_device(monkeypatch):
     assert seen == [("size", 1), ("call", 1, 4096)] and current == [0]
     assert favor.bwd_layer_norm_workspace_bytes(1, 2, 8, 16, torch.float32) == 256
     assert favor.bwd_layer_norm_workspace_bytes(1, 2, 8, 16, torch.float32, device=1) == 4096
+
+
+def test_rotary_table_words_are_exact():
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    freqs = [1.0, 0.1, 1e-4, 1e-30, -7.5, np.pi, 123456.789, 1e30]
+    want = [round(Fraction(f) / (2 * pi) * 2 ** 64) % 2 ** 64 for f in freqs]
+    table = favor.new_rotary_table((len(freqs),), freqs=freqs, device="cpu")
+    assert [w % 2 ** 64 for w in table.tolist()] == want
+    assert favor.new_rotary_table((2,), freqs=[1.7e308, 5e-324], device="cpu").shape == (2,)
