@@ -324,7 +324,13 @@ def new_rotary_table(sections, base: float = 10000.0, freqs=None, device="cuda")
     numbers), pair p by freqs[p]."""
     sections = _sections(tuple(int(n) for n in sections))[0]
     if freqs is None:
-        freqs = [float(base) ** (-j / n) for n in sections for j in range(n)]
+        base = float(base)
+        if not (math.isfinite(base) and base > 0):
+            raise FavorError(f"new_rotary_table: the base must be positive and finite, not {base}")
+        try:
+            freqs = [base ** (-j / n) for n in sections for j in range(n)]
+        except OverflowError:
+            raise FavorError(f"new_rotary_table: frequencies of base {base} are out of range") from None
     else:
         freqs = [float(f) for f in freqs]
         if len(freqs) != sum(sections):

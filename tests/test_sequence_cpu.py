@@ -334,3 +334,9 @@ def test_rotary_table_words_are_exact():
     table = favor.new_rotary_table((len(freqs),), freqs=freqs, device="cpu")
     assert [w % 2 ** 64 for w in table.tolist()] == want
     assert favor.new_rotary_table((2,), freqs=[1.7e308, 5e-324], device="cpu").shape == (2,)
+
+
+@pytest.mark.parametrize("base", [0.0, -10000.0, float("nan"), float("inf"), 5e-324])
+def test_rotary_table_refuses_bases_without_frequencies(base):
+    with pytest.raises(favor.FavorError):
+        favor.new_rotary_table((64,), base=base, device="cpu")
