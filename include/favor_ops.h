@@ -99,7 +99,9 @@ favor_status favor_gated_scan_step(const void* x, const void* g, void* h,
  * favor_fwd_layer_norm — over the last axis of each row:
  *   y = (x - mean) / sqrt(var + eps) * gamma + beta,  var = mean (x - mean)^2
  * gamma, beta: fp32 [d], each NULL for 1 and 0.  eps > 0 and finite.  y may
- * be x.  Supported: d <= 16384, B H L < 2^31.
+ * be x.  A row whose sum or sum of squares leaves fp32 (values beyond about
+ * 2^57) is NaN, as one with infinities or NaN is; rows do not touch one another.
+ * Supported: d <= 16384, B H L < 2^31.
  */
 favor_status favor_fwd_layer_norm(const void* x, const int64_t* x_strides,
                                   void* y, const int64_t* y_strides,

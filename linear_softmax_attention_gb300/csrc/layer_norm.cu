@@ -276,6 +276,9 @@ __device__ __forceinline__ void load_weights(float (&w)[NV][VW], const float* p,
   }
 }
 
+// 1 / sqrt(x); NaN for infinity: a variance that has left fp32 gives no zeros
+__device__ __forceinline__ float inverse_root(float x) { return fmaf(x, 0.f, rsqrtf(x)); }
+
 template <typename T, int VW, int NV, int CTA>
 __global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : NV * VW > 8 ? 3 : 4)
     norm_fwd_kernel(NormArgs p, Rows rows, uint32_t n, Plan plan) {
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : N
     ahead.advance();
     float v[1] = {centre<VW, NV, CTA>(x, lane, lanes, p.d, inv_d, scratch)};
     row_sum<1, CTA>(v, lanes, scratch + 32);
-    const float rstd = rsqrtf(fmaf(v[0], inv_d, p.eps));
+    const float rstd = inverse_root(fmaf(v[0], inv_d, p.eps));
     T* y = static_cast<T*>(p.y) + rows.offset(1, r);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(CTA > 0 ? CTA : 32 * kWarps, CTA > 256 ? 1 : N
     s[1] = s1.x + s1.y;
     s[2] = s2.x + s2.y;
     row_sum<3, CTA>(s, lanes, scratch + 32);
-    const float rstd = rsqrtf(fmaf(s[0], inv_d, p.eps));
+    const float rstd = inverse_root(fmaf(s[0], inv_d, p.eps));
     const float2 m1 = twice(-s[1] * inv_d), m2 = twice(-s[2] * rstd * inv_d);
     T* dx = static_cast<T*>(p.dx) + rows.offset(2, r);
 #pragma unroll

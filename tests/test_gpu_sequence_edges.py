@@ -7,7 +7,7 @@ import torch
 
 import oracle as orc
 from helpers import to_np
-from test_gpu_sequence import BF16, F32, close, scan_inputs
+from test_gpu_sequence import BF16, F32, close, gen, norm_inputs, scan_inputs, view
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,34 @@ def test_arguments_may_be_let_go_after_a_call_on_another_stream(cuda_lib):
         for u, v in zip(got if isinstance(got, tuple) else (got,), want):
             assert torch.equal(u, v), call.__name__
         del junk
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["plain", "tokens", "odd"])
+@pytest.mark.parametrize("shape", [(1, 2, 9, 64), (2, 1, 40, 33), (1, 3, 20, 16), (1, 1, 37, 771), (2, 1, 5, 1000),
+                                   (1, 1, 3, 8192), (1, 1, 3, 4099)])
+def test_layer_norm_of_rows_whose_squares_leave_fp32(cuda_lib, dtype, layout, shape):
+    """They are NaN, never zeros; the rows beside them, of all other sizes, are right."""
+    _, dy, gamma, beta = norm_inputs(shape, dtype, 2)
+    r = gen(3)
+    rows, d = shape[0] * shape[1] * shape[2], shape[3]
+    x = torch.rand(shape, generator=r) + 0.5
+    x[..., ::2] *= -1
+    # squares are summed up to d (1.5 2^54)^2 < 2^125 in the good rows, from 2^130 on in the others
+    scale = torch.randint(-40, 55, (rows,), generator=r)
+    bad = torch.arange(rows) % 3 == 1
+    scale[bad] = torch.randint(67, 127, (int(bad.sum()),), generator=r)
+    x = torch.ldexp(x, scale.view(shape[:3] + (1,))).to(dtype)
+    X, D, W, Z = (to_np(t) for t in (x, dy, gamma, beta))
+    xv, dv, wd, zd = view(x, layout), view(dy, layout), gamma.cuda(), beta.cuda()
+    bad = bad.view(shape[:3])
+    good = ~bad.numpy()
+    y = cuda_lib.fwd_layer_norm(xv, wd, zd, 1e-3)
+    dx, dgamma, dbeta = cuda_lib.bwd_layer_norm(xv, dv, wd, 1e-3)
+    for got in (y, dx):
+        assert torch.isnan(got[bad.cuda()]).all()
+    assert torch.isnan(dgamma).all()
+    close(y[~bad.cuda()], orc.layer_norm(X, W, Z, 1e-3)[good], orc.layer_norm_bound(X, W, Z, 1e-3)[good], "y")
+    close(dx[~bad.cuda()], orc.layer_norm_grad(X, D, W, 1e-3)[0][good],
+          orc.layer_norm_grad_bound(X, D, W, 1e-3)[0][good], "dx")
+    close(dbeta, orc.layer_norm_grad(X, D, W, 1e-3)[2], orc.layer_norm_grad_bound(X, D, W, 1e-3)[2], "dbeta")
