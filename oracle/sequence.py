@@ -133,7 +133,9 @@ def layer_norm_grad_bound(x, dy, gamma=None, eps=1e-5):
     mag = n + m1 + np.abs(xh) * m2
     dx = r * (e1 + np.abs(xh) * e2 + e * m2 + 5 * u * mag) + r * mag * rel
     axes = tuple(range(x.ndim - 1))
-    depth = 128 + x[..., 0].size // 64                                         # rows of one partial sum, and the joins
+    # additions that a row passes through: those of its thread's rows (with one row to a CTA and 64 CTAs; the
+    # kernels run more) and the joins; the exact sums of many rows are tested with whole numbers
+    depth = 128 + x[..., 0].size // 64
     dgamma = (depth * u * np.abs(dy * xh) + np.abs(dy) * e).sum(axes)
     return dx, dgamma, depth * u * np.abs(dy).sum(axes)
 

@@ -153,3 +153,29 @@ def test_layer_norm_of_rows_whose_squares_leave_fp32(cuda_lib, dtype, layout, sh
     close(dx[~bad.cuda()], orc.layer_norm_grad(X, D, W, 1e-3)[0][good],
           orc.layer_norm_grad_bound(X, D, W, 1e-3)[0][good], "dx")
     close(dbeta, orc.layer_norm_grad(X, D, W, 1e-3)[2], orc.layer_norm_grad_bound(X, D, W, 1e-3)[2], "dbeta")
+
+
+@pytest.mark.parametrize("rows,d,odd", [((1 << 24) + 5, 128, False), (1 << 20, 34, True), (70001, 774, True),
+                                        (50021, 2050, False), (3001, 12290, True), (300, 512, False)])
+def test_layer_norm_weight_sums_miss_no_row(cuda_lib, rows, d, odd):
+    """Rows of +1 and -1 with eps = 3: the variance is 1, 1 / sqrt(4) a half, and
+    every sum a whole number of halves, ones or (dbeta of column 1) twos within 24
+    bits: exact in fp32 in any order.  Half of the rows count at a time, each in
+    one of the two."""
+    def tensor():
+        t = torch.zeros((1, 1, rows, d + (3 if odd else 0)), device="cuda")
+        return t[..., 1:d + 1] if odd else t
+    x, dy = tensor(), tensor()
+    x[..., ::2], x[..., 1::2] = 1.0, -1.0
+    assert torch.equal(cuda_lib.fwd_layer_norm(x[:, :, :50], eps=3.0), 0.5 * x[:, :, :50])
+    dx = torch.empty_like(x)
+    for parity in (0, 1):
+        dy.zero_()
+        dy[:, :, parity::2] = 1.0
+        dy[..., 1] *= 2.0
+        _, dgamma, dbeta = cuda_lib.bwd_layer_norm(x, dy, eps=3.0, dX=dx)
+        n = float((rows + 1 - parity) // 2)
+        want = torch.full((d,), n, device="cuda")
+        want[1] = 2 * n
+        assert torch.equal(dbeta, want)
+        assert torch.equal(dgamma, 0.5 * want * x[0, 0, 0])
