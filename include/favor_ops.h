@@ -24,8 +24,12 @@
  *    element, other pairs by their byte ranges.
  *  - B, H, L, d >= 1.  Calls allocate nothing and do not synchronise; all
  *    launches are asynchronous on `stream`, and results do not depend on
- *    timing (no floating-point atomics).  NaN and infinities pass through
- *    as the formulas have them unless stated.
+ *    timing (no floating-point atomics).  The order of sums (a row's, the
+ *    rows', a scan's runs of tokens) is fixed by the shape, the type, the
+ *    device and the tensors' alignment (16 bytes, two elements or one, as
+ *    above): the same values at another alignment may differ in their last
+ *    bits.  NaN and infinities pass through as the formulas have them unless
+ *    stated.
  */
 #ifndef FAVOR_OPS_H_
 #define FAVOR_OPS_H_
@@ -85,7 +89,8 @@ favor_status favor_bwd_gated_scan(const void* g, const int64_t* g_strides,
                                   int32_t* dev_status, void* stream);
 
 /*
- * favor_gated_scan_step — one token: x, g and h contiguous [B, H, d],
+ * favor_gated_scan_step — one token: x, g and h contiguous [B, H, d] (this call
+ * alone takes no strides),
  *   new_state = exp(g) state + x (fp32 [B, H, d]),  h = new_state rounded to dt
  * new_state may be state, and h may be x or g.  State and h equal row t of
  * the forward call over the whole sequence, given the state of the tokens
@@ -114,10 +119,10 @@ favor_status favor_fwd_layer_norm(const void* x, const int64_t* x_strides,
  *   dx = (n - mean n - xh mean(n xh)) / sqrt(var + eps)
  *   dgamma = sum over the rows of dy xh,  dbeta = sum over the rows of dy
  * dgamma, dbeta: fp32 [d], overwritten, each NULL if not wanted.  dx may be
- * dy or x.  The rows are summed in an order fixed by the shape and the
- * device.  Workspace of favor_bwd_layer_norm_workspace_bytes(...) bytes,
- * 256-byte aligned (0 bytes, and NULL allowed, where dgamma and dbeta are
- * both NULL); calls that share one must be ordered on one stream.
+ * dy or x.  The rows are summed in a fixed order (see above).  Workspace of
+ * favor_bwd_layer_norm_workspace_bytes(...) bytes, 256-byte aligned (0 bytes,
+ * and NULL allowed, where dgamma and dbeta are both NULL); calls that share one
+ * must be ordered on one stream.
  */
 favor_status favor_bwd_layer_norm(const void* x, const int64_t* x_strides,
                                   const void* dy, const int64_t* dy_strides,
