@@ -1,22 +1,29 @@
 // Layer norm over the last axis, forward and backward with the reduction of
 // the weight's gradient.
 //
-// Bound by memory: a row is read once, kept in registers (at most 16 values a
-// thread), its mean and then its centred second moment summed from there, and
+// Bound by memory: a row is read once, kept in the thread (at most 16 values of
+// it), its mean and then its centred second moment summed from there, and
 // written once; the backward pass recomputes both from x instead of reading
 // them.  Rows of up to 512 values belong to a group of 4 to 32 lanes of a
 // warp, longer ones to a CTA.  The CTAs walk the rows with a stride; each
 // thread copies its pieces of the next rows ahead into its own places in
 // shared memory (48 to 64 KB in flight per SM, which registers alone could not
 // hold), while gamma and beta, and in the backward pass the columns' sums,
-// stay in registers.
+// stay in the thread, too.  They are in registers but where 16 values meet a
+// limit of 64 of them (CTAs of more than 512 threads: rows above 8192), or come
+// one by one (odd rows of 257 to 512 values and from 1025 on): the backward pass
+// then spills 350 to 960 bytes a thread, the forward pass up to 200.
 //
-// Measured (one GB300; copy rate 6770 GB/s): 65536 x 16 rows of 128 bf16 94 us
-// forward, 5.7 TB/s (97 us out of a [B, L, 3, H, d] buffer), 122 us backward,
-// 6.6 TB/s; 32768 rows of 512 fp32 22.8 and 35.6 us, 5.9 and 5.7 TB/s, bf16
-// 13.2 and 24.7 us, of which the two launches, the joins of the columns' sums
+// Measured (one GB300; copy rate 6779 GB/s): 65536 x 16 rows of 128 bf16 94 us
+// forward, 5.7 TB/s (98 us out of a [B, L, 3, H, d] buffer), 123 us backward,
+// 6.6 TB/s; 32768 rows of 512 fp32 22.9 and 35.6 us, 5.9 and 5.7 TB/s, bf16
+// 13.2 and 24.8 us, of which the two launches, the joins of the columns' sums
 // and the second kernel are about 7.  Small calls are bound by their launches
-// (8 rows of 512: 2.9 us; backward of 64 rows: 5.1).
+// (8 rows of 512: 2.7 us; backward of 64 rows: 5.1).  480 MB by width, forward
+// and backward (floors 142 and 212 us): fp32 2048 to 8192 152 to 154 and 214 to
+// 221 us, 12288 151 and 406, 333 288 and 830, 771 237 and 465, 1025 312 and 1105,
+// 4099 287 and 1376; bf16 2048 to 8192 149 to 163 and 233 to 272, 12288 161 and
+// 535, 333 542 and 2096, 771 449 and 875, 1025 548 and 2605, 4099 542 and 3176.
 #include <algorithm>
 
 #include "ops.cuh"
@@ -98,7 +105,8 @@ struct Plan {
 };
 
 // Sums of N values over the threads of a row; every one of them gets them.
-// scratch: [2][32][N] for a CTA's rows, flipped by the caller's parity.
+// scratch: [32][N] for a CTA's rows; a call must not follow one on the same
+// scratch with no call on another between them, whose barrier the reads need.
 template <int N, int CTA>
 __device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float* scratch) {
 #pragma unroll

@@ -7,7 +7,7 @@
 // are in flight together.  The heads are shared out over more threads only
 // where the tokens are few.
 //
-// Measured (one GB300; copy rate 6770 GB/s): 2 x 12288 tokens x (8 + 8) heads
+// Measured (one GB300; copy rate 6779 GB/s): 2 x 12288 tokens x (8 + 8) heads
 // of 64 fp32 34.0 us, 5.9 TB/s; 65536 tokens x (16 + 4) heads of 128 bf16 on
 // three axes 105 us, 6.4 TB/s.  With one head a token's sines are not shared
 // (65536 x (1 + 1) heads of 64 bf16: 12.6 us, 2.7 TB/s).

@@ -18,13 +18,16 @@
 // Nothing is read twice and nothing is passed through global memory, so the
 // call needs no workspace and its bits do not depend on timing.
 //
-// Measured (one GB300; copy rate 6770 GB/s): 65536 tokens x 2048 channels fp32
-// 238 us forward, 6.8 TB/s; 8 x 16 heads x 4096 x 128 bf16 77 us forward, 5.2
-// TB/s, and 106 us backward, 6.3 TB/s; 4 x 8 x 8192 x 64 bf16 24.5 us forward,
-// 4.1 TB/s; 2 x 8 x 12288 x 64 bf16 34 us backward, 3.7 TB/s.  bf16 is bound by
-// instructions (54 per token and pair of channels forward, 14 of them the
-// exponentials; 86 backward) and, where a cluster has to be wide to fill the
-// SMs, by a step's chain of maps and states.  Tried and slower at 4 x 8 x 8192
+// Measured (one GB300; copy rate 6779 GB/s): 65536 tokens x 2048 channels fp32
+// 240 to 244 us forward, 6.6 TB/s; 8 x 16 heads x 4096 x 128 bf16 78 us forward,
+// 5.1 TB/s, and 106 us backward, 6.3 TB/s; 4 x 8 x 8192 x 64 bf16 25 us forward,
+// 4.0 TB/s; 2 x 8 x 12288 x 64 bf16 35.5 us backward, 3.5 TB/s.  What holds the
+// last two back is how little is resident: 256 CTAs of 6 warps (forward) and
+// 192 of 10 (backward) leave 7 and 14 SMs empty and 34 and 84 with one CTA; on
+// those with two, 56 and 68 % of the issue slots are used, by 3 to 5 warps a
+// scheduler that otherwise wait for fixed latencies, the step's barriers and
+// the fetching of instructions (54 and 86 of them per token and pair of
+// channels).  Tried and slower at 4 x 8 x 8192
 // x 64, at the time against 26 us: three CTAs an SM (39 us, the registers
 // spill), single channels of bf16 (33), the sending and the gathering of maps
 // in two warps (28), a cluster barrier a step in place of the counted stores
@@ -651,10 +654,23 @@ cudaError_t go(const ScanArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (runs > MW) {
     // CTAs of a cluster: a wave of clusters of K takes time as 1 / K.  The
-    // smallest K whose waves take at most a tenth longer than the best's: at
-    // 32 tiles of 8192 tokens (bf16 forward) K = 8 takes 25 us, K = 4 34 and
-    // K = 12 (a second wave) 36; at 16 tiles of 12288 (bf16 backward) K = 12
-    // takes 34 us, K = 8 46 and K = 4 54.
+    // smallest K whose waves take at most a tenth longer than the best's.  A
+    // GB300 holds 304 CTAs at once, but only 152, 97, 74, 58, 46, 38, 36, 30, 28,
+    // 23, 23, 19, 14, 14, 14 clusters of 2, 3, .. 16.  Every K measured, in us
+    // (V = forward, A = backward; K = 4, 6, 8, 9, 12, 13, 16):
+    //   V bf16  16 tiles x 12288   48.1  33.8  32.8  32.0 *25.3  26.2  37.0
+    //   V bf16  32 tiles x 8192    35.7  31.7 *25.5  41.4  37.3  37.0  44.3
+    //   V bf16  64 tiles x 8192   *43.3  59.9  48.3  65.3  56.5  70.7  74.4
+    //   V fp32  64 tiles x 8192   *36.5  48.0  40.8  51.5  50.2  63.3  66.7
+    //   A bf16  16 tiles x 12288   54.6  38.7  46.4  43.7 *34.1  35.9  46.6
+    //   A bf16  32 tiles x 8192    38.8  43.0 *35.6  48.9  47.5  49.0  53.1
+    //   A fp32  64 tiles x 8192   *51.1  67.6  55.6  69.0  62.6  77.0  80.8
+    //   A fp32  19 tiles x 1777    12.1   9.9  11.1  11.1  *9.2   9.6  12.5
+    // (* the rule's; the fastest of all sixteen in each).  At 256 tiles it is 1
+    // (78.4, K = 2 84.0; backward 106.4 and 114.3).  The rule is off at 8 tiles x
+    // 16384, where 12 takes 25.4 and 30.3 us and it has 16 take 26.9 and 37.5;
+    // of the sizes it does not try, 5 would be faster at 48 tiles x 8192 (36.9,
+    // with 4 42.0).
     static std::mutex mu;
     static Fits known[64];
     int dev = 0;
