@@ -179,3 +179,35 @@ def test_layer_norm_weight_sums_miss_no_row(cuda_lib, rows, d, odd):
         want[1] = 2 * n
         assert torch.equal(dbeta, want)
         assert torch.equal(dgamma, 0.5 * want * x[0, 0, 0])
+
+
+def test_calls_on_another_stream_are_captured(cuda_lib):
+    # a graph whose capture forks to the other stream and joins it again; arguments are let go inside it
+    f = cuda_lib
+    x, g, dh, h0, _ = (t.cuda() for t in scan_inputs((2, 2, 700, 64), BF16, 4))
+    w = torch.ones(64, device="cuda")
+    pos = torch.arange(700, device="cuda", dtype=torch.int32).view(1, 1, -1)
+    table = f.new_rotary_table((32,))
+
+    def calls(**kw):
+        n = f.fwd_layer_norm(x, w, **kw)
+        q, k = f.fwd_rotary(n, dh, pos, table, (32,), **kw)
+        h, hT = f.fwd_gated_scan(q, g, h0, **kw)
+        grads = f.bwd_gated_scan(g, h, k, h0, **kw)
+        return [h, hT, *grads, *f.bwd_layer_norm(x, grads[0], w, **kw)]
+
+    want = calls()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        outs = calls(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
