@@ -1,8 +1,9 @@
 /*
  * favor_ops.h — C ABI of the sequence operators beside the FAVOR+ attention
  * (favor.h): what happens to queries and keys before the feature map (layer
- * norm, rotary positions) and the gated linear recurrence, the decayed
- * sibling of the causal pass's prefix sum.
+ * norm, rotary positions, both in one pass with a root-mean-square norm), the
+ * gated linear recurrence, the decayed sibling of the causal pass's prefix
+ * sum, and causal linear attention with a decay per head.
  *
  * Conventions shared by every call (those of favor.h unless stated here):
  *  - Tensors are [B, H, L, d], d fastest with unit stride, of dtype `dt`
@@ -173,6 +174,132 @@ favor_status favor_bwd_rotary(const void* dq_out, const int64_t* dq_out_strides,
                               int B, int Hq, int Hk, int L, int d,
                               const int32_t* pos, int pos_B, int n_axes, const int* sections,
                               const uint64_t* table, favor_pairing pairing, favor_dtype dt, void* stream);
+
+/*
+ * favor_fwd_qk_norm_rotary — root-mean-square norm of each head's queries and
+ * keys and their rotation by positions, in one pass over the rows:
+ *   y = R(pos) (x w / sqrt(mean x^2 + eps))
+ * with w = q_weight for q and k_weight for k (fp32 [d], NULL for 1) and the
+ * rotation R of favor_fwd_rotary, whose arguments (pos, sections, table,
+ * pairing) and limits these are.  eps > 0 and finite.  The normed row is kept
+ * in fp32 and rounded once, after the rotation.  q_out may be q, k_out may be k.
+ * A row whose sum of squares leaves fp32 (values beyond about 2^60) is NaN, as
+ * one with infinities or NaN is; rows do not touch one another.
+ * Supported: d <= 512, besides the limits of favor_fwd_rotary.
+ */
+favor_status favor_fwd_qk_norm_rotary(const void* q, const int64_t* q_strides, void* q_out,
+                                      const int64_t* q_out_strides, const void* k, const int64_t* k_strides,
+                                      void* k_out, const int64_t* k_out_strides, const float* q_weight,
+                                      const float* k_weight, float eps, int B, int Hq, int Hk, int L, int d,
+                                      const int32_t* pos, int pos_B, int n_axes, const int* sections,
+                                      const uint64_t* table, favor_pairing pairing, favor_dtype dt, void* stream);
+
+/*
+ * favor_bwd_qk_norm_rotary — its gradients for dy = dL/dy (dq_out, dk_out);
+ * with z = R(pos)^T dy, r = 1 / sqrt(mean x^2 + eps) (recomputed from x) and
+ * xh = x r:
+ *   dx = r (z w - xh mean(z w xh)),  dw = sum over the rows of z xh
+ * dq_weight, dk_weight: fp32 [d], overwritten, each NULL if not wanted; summed
+ * over all rows of q (of k) in a fixed order.  dq may be dq_out or q, dk may be
+ * dk_out or k.  k, dk_out and dk may all be NULL (no keys; k_weight and
+ * dk_weight are then ignored).
+ * Workspace of favor_bwd_qk_norm_rotary_workspace_bytes(...) bytes, 256-byte
+ * aligned (0 bytes, and NULL allowed, where neither dq_weight nor dk_weight is
+ * wanted); calls that share one must be ordered on one stream.
+ */
+favor_status favor_bwd_qk_norm_rotary(const void* q, const int64_t* q_strides, const void* dq_out,
+                                      const int64_t* dq_out_strides, void* dq, const int64_t* dq_strides,
+                                      const void* k, const int64_t* k_strides, const void* dk_out,
+                                      const int64_t* dk_out_strides, void* dk, const int64_t* dk_strides,
+                                      const float* q_weight, const float* k_weight, float* dq_weight,
+                                      float* dk_weight, float eps, int B, int Hq, int Hk, int L, int d,
+                                      const int32_t* pos, int pos_B, int n_axes, const int* sections,
+                                      const uint64_t* table, favor_pairing pairing, favor_dtype dt, void* workspace,
+                                      size_t ws_bytes, void* stream);
+/* The size follows the current device's number of SMs: asked for with the
+ * device current that the call runs on.  0 for arguments outside the supported
+ * shapes; Hk = 0: no keys. */
+size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, int d, favor_dtype dt);
+
+/*
+ * favor_fwd_decay_attention — causal linear attention whose memory fades by
+ * one factor per head and token, l = exp(g_h):
+ *   S_t = l S_{t-1} + k_t v_t^T,  S_{-1} = S0,  o_t = scale S_t^T q_t
+ *   (o_t = scale sum_{s<=t} l^(t-s) (q_t . k_s) v_s + scale l^(t+1) S0^T q_t)
+ * with neither a feature map nor a normaliser: the heads' outputs are normed
+ * by the layer (favor_fwd_layer_norm).
+ *  - g: device fp32 [H], the logarithms of the decays, <= 0 (not checked).  0 is
+ *    plain causal linear attention; with minus infinity a token sees itself
+ *    alone.  (A positive g gives the formula's values while l^128 and the
+ *    states stay finite in fp32.)  The decays are constants of the heads and
+ *    have no gradient.
+ *  - lengths: device int32 [B], the tokens of each sequence, or NULL for L
+ *    each; values are clamped to [0, L].  Rows of q, k and v at and behind a
+ *    sequence's end are not used, whatever they hold, and its rows of o there
+ *    are 0.
+ *  - S0, ST: fp32 [B, H, d, d] contiguous (first index the key's channel, second
+ *    the value's), S0 NULL for zeros, ST NULL if not wanted: the state after
+ *    each sequence's last token (S0 where it has none).  ST may be S0.
+ *  - workspace: favor_decay_attention_workspace_bytes(...) bytes, 256-byte
+ *    aligned (NULL allowed where that is 0); calls that share one must be
+ *    ordered on one stream.
+ *  - dev_status: a bounded wait that ran out is reported there
+ *    (FAVOR_ERR_TIMEOUT).
+ * Infinities and NaN in a token of k or v reach its own and later rows of its
+ * head, in a token of q its own row.  No output may overlap an input (but ST
+ * may be S0).
+ * With fp32 tensors everything is fp32.  With bf16 tensors ST is accurate to
+ * fp32's sums with factors of 2^-17, while o passes, beside its own rounding,
+ * through weights and states rounded to bf16 (each term is off by at most 2^-8
+ * or so of its size).
+ * Supported: d <= 128, B H < 2^20, L <= 2^30.
+ */
+favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
+                                       const int64_t* k_strides, const void* v, const int64_t* v_strides, void* o,
+                                       const int64_t* o_strides, const float* g, const int32_t* lengths,
+                                       const float* S0, float* ST, float scale, int B, int H, int L, int d,
+                                       favor_dtype dt, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                       void* stream);
+
+/*
+ * favor_bwd_decay_attention — its gradients for do = dL/do and dST = dL/dST
+ * (fp32 [B, H, d, d], NULL for zeros):
+ *   R_t = l R_{t+1} + scale q_t do_t^T  (R behind the last token: dST, unfaded)
+ *   dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dS0 = l R_0
+ * from the forward call's q, k, v, g, lengths, scale and S0 (S_t is formed
+ * again).  dS0: fp32 [B, H, d, d], NULL if not wanted; dS0 may be dST.  Rows of
+ * dq, dk and dv at and behind a sequence's end are 0.  No other output may
+ * overlap an input or another output.  Workspace and dev_status as above, with
+ * `backward` set in the size.
+ */
+favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
+                                       const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                                       const void* d_o, const int64_t* do_strides, void* dq,
+                                       const int64_t* dq_strides, void* dk, const int64_t* dk_strides, void* dv,
+                                       const int64_t* dv_strides, const float* g, const int32_t* lengths,
+                                       const float* S0, const float* dST, float* dS0, float scale, int B, int H,
+                                       int L, int d, favor_dtype dt, void* workspace, size_t ws_bytes,
+                                       int32_t* dev_status, void* stream);
+/* The size follows the current device's number of SMs: asked for with the
+ * device current that the call runs on.  0: none is needed, or the arguments
+ * are outside the supported shapes. */
+size_t favor_decay_attention_workspace_bytes(int B, int H, int L, int d, favor_dtype dt, int backward);
+
+/*
+ * favor_decay_attention_step — one token of each sequence:
+ *   new_state = l state + k v^T,  o = scale new_state^T q
+ * q, k, v, o: [B, H, d] with d fastest and, each, an int64_t[2] of the element
+ * strides of B and H, or NULL for a contiguous tensor.  state, new_state: fp32
+ * [B, H, d, d]; new_state may be state.  o may not overlap anything else.
+ * Everything is fp32 but the rounding of o: row t of the forward call, given
+ * the state of the tokens before it.
+ * Supported: d <= 128, B H < 2^20.
+ */
+favor_status favor_decay_attention_step(const void* q, const int64_t* q_strides, const void* k,
+                                        const int64_t* k_strides, const void* v, const int64_t* v_strides, void* o,
+                                        const int64_t* o_strides, const float* g, const float* state,
+                                        float* new_state, float scale, int B, int H, int d, favor_dtype dt,
+                                        void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,9 @@ __all__ = [
     "bwd_bidir", "bwd_causal", "bwd_workspace_bytes", "selftest_wait_timeout",
     "fwd_gated_scan", "bwd_gated_scan", "gated_scan_step", "new_gated_scan_state", "fwd_layer_norm",
     "bwd_layer_norm", "bwd_layer_norm_workspace_bytes", "fwd_rotary", "bwd_rotary", "new_rotary_table",
-    "selftest_scan_timeout",
+    "selftest_scan_timeout", "fwd_qk_norm_rotary", "bwd_qk_norm_rotary", "bwd_qk_norm_rotary_workspace_bytes",
+    "fwd_decay_attention", "bwd_decay_attention", "decay_attention_step", "new_decay_state",
+    "decay_attention_workspace_bytes",
 ]
 
 F32 = 0
@@ -99,6 +101,7 @@ def load():
     lib.favor_decode_prefill_workspace_bytes.restype = c_size
     lib.favor_decode_prefill_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int]
     sequence.declare(lib)
+    decay.declare(lib)
     _lib = lib
     return lib
 
@@ -361,6 +364,10 @@ def bwd_causal(Q, K, V, dO, omega, qk_scale, workspace=None, feature_map="prf", 
 
 
 from . import sequence                                                   # noqa: E402  (uses load and FavorError)
-from .sequence import (bwd_gated_scan, bwd_layer_norm, bwd_layer_norm_workspace_bytes, bwd_rotary,  # noqa: E402
-                       fwd_gated_scan, fwd_layer_norm, fwd_rotary, gated_scan_step, new_gated_scan_state,
-                       new_rotary_table, selftest_scan_timeout)
+from .sequence import (bwd_gated_scan, bwd_layer_norm, bwd_layer_norm_workspace_bytes, bwd_qk_norm_rotary,  # noqa: E402
+                       bwd_qk_norm_rotary_workspace_bytes, bwd_rotary, fwd_gated_scan, fwd_layer_norm,
+                       fwd_qk_norm_rotary, fwd_rotary, gated_scan_step, new_gated_scan_state, new_rotary_table,
+                       selftest_scan_timeout)
+from . import decay                                                      # noqa: E402
+from .decay import (bwd_decay_attention, decay_attention_step, decay_attention_workspace_bytes,  # noqa: E402
+                    fwd_decay_attention, new_decay_state)

@@ -161,4 +161,21 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, int piece, cudaStream_t stream);
 
+constexpr int kQkNormMaxD = 512;
+struct QkNormArgs {
+  const void *q, *k, *dqo, *dko;      // dqo, dko: backward, the gradients of the outputs
+  void *qo, *ko;                      // forward: the outputs; backward: dq, dk
+  Strides qs, ks, dqos, dkos, qos, kos;
+  const float *wq, *wk;
+  float *dwq, *dwk;
+  float eps;
+  int B, Hq, Hk, L, d;                // Hk = 0: no keys
+  const int32_t* pos;
+  int pos_B, n_axes, sections[FAVOR_ROTARY_MAX_AXES], pairs;
+  const uint64_t* table;
+  bool halves;
+};
+cudaError_t launch_qk_norm(const QkNormArgs& a, bool bf16, int piece, bool backward, float* ws, cudaStream_t stream);
+size_t qk_norm_workspace_bytes(const QkNormArgs& a);
+
 }  // namespace favor

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <initializer_list>
 
+#include "decay.cuh"
 #include "favor_selftest.h"
 #include "ops.cuh"
 
@@ -194,11 +195,10 @@ favor_status done(cudaError_t e) { return e == cudaSuccess ? FAVOR_OK : FAVOR_ER
 
 bool positive(float x) { return std::isfinite(x) && x > 0.f; }
 
-favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* qos, const void* k, const int64_t* ks,
-                    void* ko, const int64_t* kos, int B, int Hq, int Hk, int L, int d, const int32_t* pos, int pos_B,
-                    int n_axes, const int* sections, const uint64_t* table, favor_pairing pairing, bool inverse,
-                    favor_dtype dt, void* stream) {
-  const bool keys = k != nullptr || ko != nullptr;
+// Sizes, positions and pairs of a rotation; counts the pairs.
+favor_status turns_ok(int B, int Hq, int Hk, bool keys, int L, int d, const int32_t* pos, int pos_B, int n_axes,
+                      const int* sections, const uint64_t* table, favor_pairing pairing, favor_dtype dt, int* counts,
+                      int* n_pairs) {
   favor_status st = sizes_ok(B, Hq, L, d, dt);
   if (st == FAVOR_OK && keys) st = sizes_ok(B, Hk, L, d, dt);
   if (st != FAVOR_OK) return st;
@@ -207,19 +207,32 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   if (pos_B != 1 && pos_B != B) return FAVOR_ERR_INVALID_ARG;
   if (pos == nullptr || reinterpret_cast<uintptr_t>(pos) % 4 != 0) return FAVOR_ERR_INVALID_ARG;
   if (table == nullptr || reinterpret_cast<uintptr_t>(table) % 8 != 0) return FAVOR_ERR_INVALID_ARG;
-  favor::RotaryArgs a{};
   int64_t pairs = 0;
   for (int i = 0; i < n_axes; ++i) {
     if (sections[i] < 0) return FAVOR_ERR_INVALID_ARG;
-    a.sections[i] = sections[i];
+    counts[i] = sections[i];
     pairs += sections[i];
   }
   if (pairs < 1 || 2 * pairs > d) return FAVOR_ERR_INVALID_ARG;
+  *n_pairs = static_cast<int>(pairs);
   const int64_t lim = int64_t(1) << 31;
   if (d > favor::kNormMaxD || (int64_t)B * Hq >= lim || (int64_t)B * Hq * L >= lim) return FAVOR_ERR_UNSUPPORTED;
   if (keys && ((int64_t)B * Hk >= lim || (int64_t)B * Hk * L >= lim)) return FAVOR_ERR_UNSUPPORTED;
   // the kernels' steps over the heads stay inside 32 bits
   if ((int64_t)Hq + (keys ? Hk : 0) > lim - 16) return FAVOR_ERR_UNSUPPORTED;
+  return FAVOR_OK;
+}
+
+favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* qos, const void* k, const int64_t* ks,
+                    void* ko, const int64_t* kos, int B, int Hq, int Hk, int L, int d, const int32_t* pos, int pos_B,
+                    int n_axes, const int* sections, const uint64_t* table, favor_pairing pairing, bool inverse,
+                    favor_dtype dt, void* stream) {
+  const bool keys = k != nullptr || ko != nullptr;
+  favor::RotaryArgs a{};
+  const favor_status st =
+      turns_ok(B, Hq, Hk, keys, L, d, pos, pos_B, n_axes, sections, table, pairing, dt, a.sections, &a.pairs);
+  if (st != FAVOR_OK) return st;
+  const int pairs = a.pairs;
   const int e = elem(dt);
   View vq, vqo, vk{}, vko{};
   if (!favor::make_view(&vq, q, qs, B, Hq, L, d, e) || !favor::make_view(&vqo, qo, qos, B, Hq, L, d, e))
@@ -254,7 +267,6 @@ favor_status rotary(const void* q, const int64_t* qs, void* qo, const int64_t* q
   a.pos = pos;
   a.pos_B = pos_B;
   a.n_axes = n_axes;
-  a.pairs = static_cast<int>(pairs);
   a.table = table;
   a.halves = pairing == FAVOR_PAIR_HALVES;
   a.inverse = inverse;
@@ -296,6 +308,157 @@ favor_status fwd_gated_scan(const void* x, const int64_t* x_strides, const void*
   a.quits = quits;
   return done(favor::launch_scan(a, false, dt == FAVOR_BF16, common_piece({&vx, &vg, &vh}),
                                  static_cast<cudaStream_t>(stream)));
+}
+
+// ---- norms of queries and keys with their rotation --------------------------------
+bool qk_norm_sizes(int B, int Hq, int Hk, int L, int d) {
+  const int64_t lim = int64_t(1) << 31;
+  return d <= favor::kQkNormMaxD && (int64_t)B * Hq < lim && (int64_t)B * Hq * L < lim && (int64_t)B * Hk < lim &&
+         (int64_t)B * Hk * L < lim && (int64_t)Hq + Hk <= lim - 16;
+}
+
+struct QkSide {
+  const void *x, *dy;
+  void* out;
+  const int64_t *xs, *dys, *os;
+  const float* w;
+  float* dw;
+  int heads;
+  View vx, vdy, vout;
+};
+
+favor_status qk_norm(QkSide* side, bool keys, float eps, int B, int L, int d, const int32_t* pos, int pos_B,
+                     int n_axes, const int* sections, const uint64_t* table, favor_pairing pairing, favor_dtype dt,
+                     bool backward, void* workspace, size_t ws_bytes, void* stream) {
+  favor::QkNormArgs a{};
+  const favor_status st = turns_ok(B, side[0].heads, side[1].heads, keys, L, d, pos, pos_B, n_axes, sections, table,
+                                   pairing, dt, a.sections, &a.pairs);
+  if (st != FAVOR_OK) return st;
+  if (!positive(eps)) return FAVOR_ERR_INVALID_ARG;
+  if (d > favor::kQkNormMaxD) return FAVOR_ERR_UNSUPPORTED;
+  const int e = elem(dt), n = keys ? 2 : 1;
+  a.B = B;
+  a.Hq = side[0].heads;
+  a.Hk = keys ? side[1].heads : 0;
+  a.L = L;
+  a.d = d;
+  const bool sums = backward && (side[0].dw != nullptr || (keys && side[1].dw != nullptr));
+  const size_t need = sums ? favor::qk_norm_workspace_bytes(a) : 0;
+  if (need > 0 &&
+      (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || ws_bytes < need))
+    return FAVOR_ERR_INVALID_ARG;
+  const View vpos = favor::flat_view(pos, (int64_t)n_axes * pos_B * L, 4), vtab = favor::flat_view(table, a.pairs, 8);
+  const View vw = favor::flat_view(workspace, (int64_t)need, 1);
+  int piece = 16;
+  for (int i = 0; i < n; ++i) {
+    QkSide& s = side[i];
+    if (!flat_ok(s.w) || !flat_ok(s.dw) || !favor::make_view(&s.vx, s.x, s.xs, B, s.heads, L, d, e) ||
+        !favor::make_view(&s.vout, s.out, s.os, B, s.heads, L, d, e) ||
+        (backward && !favor::make_view(&s.vdy, s.dy, s.dys, B, s.heads, L, d, e)))
+      return FAVOR_ERR_INVALID_ARG;
+    piece = std::min(piece, common_piece({&s.vx, &s.vout}));
+    if (backward) piece = std::min(piece, common_piece({&s.vdy}));
+    if (!backward) s.dw = nullptr;
+  }
+  for (int i = 0; i < n; ++i) {
+    const QkSide& s = side[i];
+    if (favor::self_overlap(s.vout) || clash(s.vout, vpos, false) || clash(s.vout, vtab, false) ||
+        (need > 0 && (clash(vw, vpos, false) || clash(vw, vtab, false))))
+      return FAVOR_ERR_INVALID_ARG;
+    if (s.dw != nullptr && (clash(vpos, s.dw, d) || clash(vtab, s.dw, d))) return FAVOR_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j) {
+      const QkSide& o = side[j];
+      if (clash(s.vout, o.vx, i == j) || (backward && clash(s.vout, o.vdy, i == j)) || clash(s.vout, o.w, d) ||
+          clash(s.vout, o.dw, d) || (j != i && clash(s.vout, o.vout, false)))
+        return FAVOR_ERR_INVALID_ARG;
+      if (s.dw != nullptr && (clash(o.vx, s.dw, d) || clash(o.vdy, s.dw, d) || clash(s.dw, d, o.w, d, false) ||
+                              (j != i && clash(s.dw, d, o.dw, d, false))))
+        return FAVOR_ERR_INVALID_ARG;
+    }
+    if (need > 0 && (favor::overlap(vw, s.vx) || favor::overlap(vw, s.vdy) || favor::overlap(vw, s.vout) ||
+                     clash(vw, s.w, d) || clash(vw, s.dw, d)))
+      return FAVOR_ERR_INVALID_ARG;
+  }
+  const QkSide& q = side[0];
+  a.q = q.x;
+  a.dqo = q.dy;
+  a.qo = q.out;
+  a.qs = q.vx.strides();
+  a.qos = q.vout.strides();
+  if (backward) a.dqos = q.vdy.strides();
+  a.wq = q.w;
+  a.dwq = q.dw;
+  if (keys) {
+    const QkSide& k = side[1];
+    a.k = k.x;
+    a.dko = k.dy;
+    a.ko = k.out;
+    a.ks = k.vx.strides();
+    a.kos = k.vout.strides();
+    if (backward) a.dkos = k.vdy.strides();
+    a.wk = k.w;
+    a.dwk = k.dw;
+  }
+  a.eps = eps;
+  a.pos = pos;
+  a.pos_B = pos_B;
+  a.n_axes = n_axes;
+  a.table = table;
+  a.halves = pairing == FAVOR_PAIR_HALVES;
+  return done(favor::launch_qk_norm(a, dt == FAVOR_BF16, piece, backward, static_cast<float*>(workspace),
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+// ---- causal linear attention with a decay per head --------------------------------
+favor_status decay_sizes(int B, int H, int L, int d, favor_dtype dt) {
+  const favor_status st = sizes_ok(B, H, L, d, dt);
+  if (st != FAVOR_OK) return st;
+  if (d > favor::kDecayMaxD || (int64_t)B * H >= (1 << 20) || L > (1 << 30)) return FAVOR_ERR_UNSUPPORTED;
+  return FAVOR_OK;
+}
+
+favor::DecayShape decay_shape(const float* g, const int32_t* lengths, int32_t* status, int B, int H, int L, int d) {
+  favor::DecayShape s{};
+  s.g = g;
+  s.lengths = lengths;
+  s.status = status;
+  s.B = B;
+  s.H = H;
+  s.L = L;
+  s.d = d;
+  return s;
+}
+
+int64_t decay_states(const favor::DecayShape& s) { return (int64_t)s.BH() * s.segs * s.d * s.d; }
+
+// the flat operands of a call: what may not meet an output
+struct Flat {
+  View v[8];
+  int n = 0;
+  bool add(const void* p, int64_t count, int esz = 4) {
+    if (p == nullptr) return true;
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return false;
+    v[n++] = favor::flat_view(p, count, esz);
+    return true;
+  }
+  bool meets(const View& out) const {
+    for (int i = 0; i < n; ++i)
+      if (favor::overlap(v[i], out)) return true;
+    return false;
+  }
+};
+
+size_t decay_workspace(int B, int H, int L, int d, bool backward) {
+  favor::DecayShape s = decay_shape(nullptr, nullptr, nullptr, B, H, L, d);
+  favor::decay_simt_plan(&s);
+  const int64_t states = s.segs > 1 ? decay_states(s) : 0;
+  return (size_t)states * (backward ? 2 : 1) * sizeof(float);
+}
+
+favor_status workspace_ok(const void* ws, size_t have, size_t need) {
+  if (need == 0) return FAVOR_OK;
+  if (ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || have < need) return FAVOR_ERR_INVALID_ARG;
+  return FAVOR_OK;
 }
 
 }  // namespace
@@ -487,6 +650,248 @@ favor_status favor_bwd_rotary(const void* dq_out, const int64_t* dq_out_strides,
                               void* stream) {
   return rotary(dq_out, dq_out_strides, dq, dq_strides, dk_out, dk_out_strides, dk, dk_strides, B, Hq, Hk, L, d, pos,
                 pos_B, n_axes, sections, table, pairing, true, dt, stream);
+}
+
+favor_status favor_fwd_qk_norm_rotary(const void* q, const int64_t* q_strides, void* q_out,
+                                      const int64_t* q_out_strides, const void* k, const int64_t* k_strides,
+                                      void* k_out, const int64_t* k_out_strides, const float* q_weight,
+                                      const float* k_weight, float eps, int B, int Hq, int Hk, int L, int d,
+                                      const int32_t* pos, int pos_B, int n_axes, const int* sections,
+                                      const uint64_t* table, favor_pairing pairing, favor_dtype dt, void* stream) {
+  QkSide side[2] = {{q, nullptr, q_out, q_strides, nullptr, q_out_strides, q_weight, nullptr, Hq, {}, {}, {}},
+                    {k, nullptr, k_out, k_strides, nullptr, k_out_strides, k_weight, nullptr, Hk, {}, {}, {}}};
+  return qk_norm(side, k != nullptr || k_out != nullptr, eps, B, L, d, pos, pos_B, n_axes, sections, table, pairing,
+                 dt, false, nullptr, 0, stream);
+}
+
+favor_status favor_bwd_qk_norm_rotary(const void* q, const int64_t* q_strides, const void* dq_out,
+                                      const int64_t* dq_out_strides, void* dq, const int64_t* dq_strides,
+                                      const void* k, const int64_t* k_strides, const void* dk_out,
+                                      const int64_t* dk_out_strides, void* dk, const int64_t* dk_strides,
+                                      const float* q_weight, const float* k_weight, float* dq_weight,
+                                      float* dk_weight, float eps, int B, int Hq, int Hk, int L, int d,
+                                      const int32_t* pos, int pos_B, int n_axes, const int* sections,
+                                      const uint64_t* table, favor_pairing pairing, favor_dtype dt, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  QkSide side[2] = {{q, dq_out, dq, q_strides, dq_out_strides, dq_strides, q_weight, dq_weight, Hq, {}, {}, {}},
+                    {k, dk_out, dk, k_strides, dk_out_strides, dk_strides, k_weight, dk_weight, Hk, {}, {}, {}}};
+  return qk_norm(side, k != nullptr || dk_out != nullptr || dk != nullptr, eps, B, L, d, pos, pos_B, n_axes, sections,
+                 table, pairing, dt, true, workspace, ws_bytes, stream);
+}
+
+size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, int d, favor_dtype dt) {
+  if (sizes_ok(B, Hq, L, d, dt) != FAVOR_OK || Hk < 0 || !qk_norm_sizes(B, Hq, Hk, L, d)) return 0;
+  favor::QkNormArgs a{};
+  a.B = B;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.L = L;
+  a.d = d;
+  return favor::qk_norm_workspace_bytes(a);
+}
+
+size_t favor_decay_attention_workspace_bytes(int B, int H, int L, int d, favor_dtype dt, int backward) {
+  if (decay_sizes(B, H, L, d, dt) != FAVOR_OK) return 0;
+  return decay_workspace(B, H, L, d, backward != 0);
+}
+
+favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
+                                       const int64_t* k_strides, const void* v, const int64_t* v_strides, void* o,
+                                       const int64_t* o_strides, const float* g, const int32_t* lengths,
+                                       const float* S0, float* ST, float scale, int B, int H, int L, int d,
+                                       favor_dtype dt, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                       void* stream) {
+  favor_status st = decay_sizes(B, H, L, d, dt);
+  if (st != FAVOR_OK) return st;
+  if (g == nullptr || !std::isfinite(scale)) return FAVOR_ERR_INVALID_ARG;
+  const int e = elem(dt);
+  View vq, vk, vv, vo;
+  if (!favor::make_view(&vq, q, q_strides, B, H, L, d, e) || !favor::make_view(&vk, k, k_strides, B, H, L, d, e) ||
+      !favor::make_view(&vv, v, v_strides, B, H, L, d, e) || !favor::make_view(&vo, o, o_strides, B, H, L, d, e))
+    return FAVOR_ERR_INVALID_ARG;
+  const int64_t states = (int64_t)B * H * d * d;
+  const size_t need = decay_workspace(B, H, L, d, false);
+  st = workspace_ok(workspace, ws_bytes, need);
+  if (st != FAVOR_OK) return st;
+  Flat flat;
+  if (!flat.add(g, H) || !flat.add(lengths, B) || !flat.add(S0, states) || !flat_ok(ST)) return FAVOR_ERR_INVALID_ARG;
+  const View ws_view = favor::flat_view(workspace, (int64_t)need, 1);
+  if (favor::self_overlap(vo) || flat.meets(vo) || clash(vo, ST, states) ||
+      (need > 0 && (favor::overlap(vo, ws_view) || flat.meets(ws_view) || clash(ws_view, ST, states))))
+    return FAVOR_ERR_INVALID_ARG;
+  for (const View* in : {&vq, &vk, &vv})
+    if (favor::overlap(vo, *in) || clash(*in, ST, states) || (need > 0 && favor::overlap(*in, ws_view)))
+      return FAVOR_ERR_INVALID_ARG;
+  if (ST != nullptr) {
+    if (ST == S0) --flat.n;                              // S0 was added last
+    if (flat.meets(favor::flat_view(ST, states, 4))) return FAVOR_ERR_INVALID_ARG;
+  }
+  const auto strm = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dt == FAVOR_BF16;
+  const int piece = common_piece({&vq, &vk, &vv});
+  favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
+  favor::decay_simt_plan(&s);
+  float* ws = s.segs > 1 ? static_cast<float*>(workspace) : nullptr;
+  if (ws != nullptr) {
+    const favor::DecayGain gain{k, v, vk.strides(), vv.strides(), ws, 1.f, false};
+    cudaError_t err = favor::decay_simt_gains(&gain, 1, s, bf16, piece, strm);
+    const favor::DecayScan scan{ws, S0, ST, false};
+    if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
+    if (err != cudaSuccess) return FAVOR_ERR_CUDA;
+  }
+  favor::DecayPass p{};
+  p.a = q;
+  p.b = k;
+  p.c = v;
+  p.o = o;
+  p.as = vq.strides();
+  p.bs = vk.strides();
+  p.cs = vv.strides();
+  p.os = vo.strides();
+  p.start = ws != nullptr ? ws : S0;
+  p.last = ws != nullptr ? nullptr : ST;
+  p.s_w = p.s_r = scale;
+  p.s_u = 1.f;
+  return done(favor::decay_simt_pass(p, s, bf16, piece, strm));
+}
+
+favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
+                                       const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                                       const void* d_o, const int64_t* do_strides, void* dq,
+                                       const int64_t* dq_strides, void* dk, const int64_t* dk_strides, void* dv,
+                                       const int64_t* dv_strides, const float* g, const int32_t* lengths,
+                                       const float* S0, const float* dST, float* dS0, float scale, int B, int H,
+                                       int L, int d, favor_dtype dt, void* workspace, size_t ws_bytes,
+                                       int32_t* dev_status, void* stream) {
+  favor_status st = decay_sizes(B, H, L, d, dt);
+  if (st != FAVOR_OK) return st;
+  if (g == nullptr || !std::isfinite(scale)) return FAVOR_ERR_INVALID_ARG;
+  const int e = elem(dt);
+  View in[4], out[3];
+  const void* inp[4] = {q, k, v, d_o};
+  const int64_t* ins[4] = {q_strides, k_strides, v_strides, do_strides};
+  void* outp[3] = {dq, dk, dv};
+  const int64_t* outs[3] = {dq_strides, dk_strides, dv_strides};
+  for (int i = 0; i < 4; ++i)
+    if (!favor::make_view(&in[i], inp[i], ins[i], B, H, L, d, e)) return FAVOR_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (!favor::make_view(&out[i], outp[i], outs[i], B, H, L, d, e) || favor::self_overlap(out[i]))
+      return FAVOR_ERR_INVALID_ARG;
+  const int64_t states = (int64_t)B * H * d * d;
+  const size_t need = decay_workspace(B, H, L, d, true);
+  st = workspace_ok(workspace, ws_bytes, need);
+  if (st != FAVOR_OK) return st;
+  // all that an output may not meet: the flat operands, the inputs and the other outputs
+  Flat flat;
+  if (!flat.add(g, H) || !flat.add(lengths, B) || !flat.add(S0, states) || !flat.add(dST, states) || !flat_ok(dS0))
+    return FAVOR_ERR_INVALID_ARG;
+  const View ws_view = favor::flat_view(workspace, (int64_t)need, 1);
+  if (need > 0 && flat.meets(ws_view)) return FAVOR_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (flat.meets(out[i]) || clash(out[i], dS0, states) || (need > 0 && favor::overlap(out[i], ws_view)))
+      return FAVOR_ERR_INVALID_ARG;
+    for (const View& v_in : in)
+      if (favor::overlap(out[i], v_in)) return FAVOR_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (favor::overlap(out[i], out[j])) return FAVOR_ERR_INVALID_ARG;
+  }
+  for (const View& v_in : in)
+    if (clash(v_in, dS0, states) || (need > 0 && favor::overlap(v_in, ws_view))) return FAVOR_ERR_INVALID_ARG;
+  if (dS0 != nullptr) {
+    const View vd = favor::flat_view(dS0, states, 4);
+    if (dS0 == dST) --flat.n;                            // dST was added last
+    if (flat.meets(vd) || (need > 0 && favor::overlap(ws_view, vd))) return FAVOR_ERR_INVALID_ARG;
+  }
+  const auto strm = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dt == FAVOR_BF16;
+  const int piece = common_piece({&in[0], &in[1], &in[2], &in[3]});
+  favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
+  favor::decay_simt_plan(&s);
+  float* ws = s.segs > 1 ? static_cast<float*>(workspace) : nullptr;
+  float* ws_r = ws != nullptr ? ws + decay_states(s) : nullptr;
+  if (ws != nullptr) {
+    const favor::DecayGain gains[2] = {{k, v, in[1].strides(), in[2].strides(), ws, 1.f, false},
+                                       {q, d_o, in[0].strides(), in[3].strides(), ws_r, scale, true}};
+    cudaError_t err = favor::decay_simt_gains(gains, 2, s, bf16, piece, strm);
+    const favor::DecayScan scans[2] = {{ws, S0, nullptr, false}, {ws_r, dST, dS0, true}};
+    if (err == cudaSuccess) err = favor::decay_scan_states(scans, 2, s, strm);
+    if (err != cudaSuccess) return FAVOR_ERR_CUDA;
+  }
+  // dq, dk, dv: rows a, b, c among q, k, v, do.  dv comes last: it leaves dS0,
+  // which may be the dST that dk reads
+  const int abc[3][3] = {{3, 2, 1}, {2, 3, 0}, {1, 0, 3}};
+  for (int i = 0; i < 3; ++i) {
+    const View &a = in[abc[i][0]], &b = in[abc[i][1]], &c = in[abc[i][2]];
+    favor::DecayPass p{};
+    p.a = a.p;
+    p.b = b.p;
+    p.c = c.p;
+    p.o = outp[i];
+    p.as = a.strides();
+    p.bs = b.strides();
+    p.cs = c.strides();
+    p.os = out[i].strides();
+    p.rev = i > 0;
+    p.transposed = i < 2;
+    p.start = i == 0 ? (ws != nullptr ? ws : S0) : (ws != nullptr ? ws_r : dST);
+    p.last = i == 2 && ws == nullptr ? dS0 : nullptr;
+    p.s_w = scale;
+    p.s_r = i == 0 ? scale : 1.f;
+    p.s_u = i == 0 ? 1.f : scale;
+    const cudaError_t err = favor::decay_simt_pass(p, s, bf16, piece, strm);
+    if (err != cudaSuccess) return FAVOR_ERR_CUDA;
+  }
+  return FAVOR_OK;
+}
+
+favor_status favor_decay_attention_step(const void* q, const int64_t* q_strides, const void* k,
+                                        const int64_t* k_strides, const void* v, const int64_t* v_strides, void* o,
+                                        const int64_t* o_strides, const float* g, const float* state,
+                                        float* new_state, float scale, int B, int H, int d, favor_dtype dt,
+                                        void* stream) {
+  const favor_status st = decay_sizes(B, H, 1, d, dt);
+  if (st != FAVOR_OK) return st;
+  if (g == nullptr || state == nullptr || new_state == nullptr || !flat_ok(g) || !flat_ok(state) ||
+      !flat_ok(new_state) || !std::isfinite(scale))
+    return FAVOR_ERR_INVALID_ARG;
+  const int e = elem(dt);
+  const void* p[4] = {q, k, v, o};
+  const int64_t* strides[4] = {q_strides, k_strides, v_strides, o_strides};
+  View views[4];
+  for (int i = 0; i < 4; ++i) {
+    int64_t s3[3] = {(int64_t)H * d, d, 0};
+    if (strides[i] != nullptr) {
+      s3[0] = strides[i][0];
+      s3[1] = strides[i][1];
+    }
+    if (!favor::make_view(&views[i], p[i], s3, B, H, 1, d, e)) return FAVOR_ERR_INVALID_ARG;
+  }
+  const int64_t n = (int64_t)B * H * d * d;
+  const View vn = favor::flat_view(new_state, n, 4), vg = favor::flat_view(g, H, 4);
+  if (favor::self_overlap(views[3]) || clash(views[3], state, n) || favor::overlap(views[3], vn) ||
+      favor::overlap(views[3], vg) || favor::overlap(vn, vg) || clash(new_state, n, state, n, true))
+    return FAVOR_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (favor::overlap(views[3], views[i]) || favor::overlap(vn, views[i])) return FAVOR_ERR_INVALID_ARG;
+  favor::DecayStep a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  int64_t* to[4] = {a.qs, a.ks, a.vs, a.os};
+  for (int i = 0; i < 4; ++i) {
+    to[i][0] = views[i].s[0];
+    to[i][1] = views[i].s[1];
+  }
+  a.g = g;
+  a.state = state;
+  a.next = new_state;
+  a.scale = scale;
+  a.B = B;
+  a.H = H;
+  a.d = d;
+  a.vec = d % 4 == 0 && reinterpret_cast<uintptr_t>(state) % 16 == 0 && reinterpret_cast<uintptr_t>(new_state) % 16 == 0;
+  return done(favor::launch_decay_step(a, dt == FAVOR_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 """Binding of the sequence operators (``include/favor_ops.h``): layer norm and
-rotary positions of queries and keys, and the gated linear recurrence.
+rotary positions of queries and keys, both in one pass with a root-mean-square
+norm, and the gated linear recurrence.
 
 As in the package itself every function only marshals arguments; the rules
 are those of the header.  Tensors are [B, H, L, d] views with a unit stride
@@ -19,7 +20,8 @@ import torch
 from . import FavorError, _DT, _check, load
 
 __all__ = ["fwd_gated_scan", "bwd_gated_scan", "gated_scan_step", "new_gated_scan_state", "fwd_layer_norm",
-           "bwd_layer_norm", "bwd_layer_norm_workspace_bytes", "fwd_rotary", "bwd_rotary", "new_rotary_table"]
+           "bwd_layer_norm", "bwd_layer_norm_workspace_bytes", "fwd_rotary", "bwd_rotary", "new_rotary_table",
+           "fwd_qk_norm_rotary", "bwd_qk_norm_rotary", "bwd_qk_norm_rotary_workspace_bytes"]
 
 PAIRINGS = {"adjacent": 0, "halves": 1}              # favor_pairing
 MAX_AXES = 4
@@ -42,8 +44,13 @@ def declare(lib):
     lib.favor_bwd_layer_norm_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.favor_fwd_rotary.argtypes = [vp] * 8 + [i] * 5 + [vp, i, i, vp, vp, i, i, vp]
     lib.favor_bwd_rotary.argtypes = lib.favor_fwd_rotary.argtypes
+    turns = [vp, i, i, vp, vp, i, i]                  # positions to pairing, dtype
+    lib.favor_fwd_qk_norm_rotary.argtypes = [vp] * 8 + [vp, vp, f] + [i] * 5 + turns + [vp]
+    lib.favor_bwd_qk_norm_rotary.argtypes = [vp] * 12 + [vp] * 4 + [f] + [i] * 5 + turns + [vp, size, vp]
+    lib.favor_bwd_qk_norm_rotary_workspace_bytes.argtypes = [i] * 6
+    lib.favor_bwd_qk_norm_rotary_workspace_bytes.restype = size
     for name in ("fwd_gated_scan", "bwd_gated_scan", "gated_scan_step", "fwd_layer_norm", "bwd_layer_norm",
-                 "fwd_rotary", "bwd_rotary"):
+                 "fwd_rotary", "bwd_rotary", "fwd_qk_norm_rotary", "bwd_qk_norm_rotary"):
         getattr(lib, "favor_" + name).restype = i
     lib.favor_bwd_layer_norm_workspace_bytes.restype = size
     lib.favor_selftest_scan_timeout.argtypes = [vp] * 4 + [i] * 5 + [ctypes.c_int64, i, vp, vp]
@@ -354,10 +361,8 @@ def _sections(sections):
     return sections, (ctypes.c_int * len(sections))(*sections), sum(sections)
 
 
-def _rotary(Q, K, what, pos, table, sections, pairing, Qo, Ko, stream):
-    if stream is not None:
-        return _on(stream, _rotary, Q, K, what, pos, table, sections, pairing, Qo, Ko, None)
-    B, Hq, L, d, dt, dev = _sizes(what, "Q", Q, True)
+def _turns(what, B, L, dev, pos, table, sections, pairing):
+    """Positions, axes, sections, table and pairing of a call, as the entry points take them."""
     sections, c_sections, pairs = _sections(sections if type(sections) is tuple else tuple(sections))
     pairing = PAIRINGS.get(pairing)
     if pairing is None:
@@ -366,15 +371,30 @@ def _rotary(Q, K, what, pos, table, sections, pairing, Qo, Ko, stream):
     if (pos.dtype is not torch.int32 or pos.get_device() != dev or not pos.is_contiguous()
             or (pos.shape != (n, B, L) and pos.shape != (n, 1, L))):
         raise FavorError(f"{what}: positions must be contiguous int32 [{n}, {B} or 1, {L}] on cuda:{dev}")
+    return (pos.data_ptr(), pos.shape[1], n, c_sections,
+            *_flats(what, ("the table (new_rotary_table)",), (table,), (pairs,), dev, torch.int64), pairing)
+
+
+def _heads(what, K, B, L, d):
+    """Shape of the keys [B, Hk, L, d], any number of heads."""
+    Hk = K.shape[1] if K.dim() == 4 else 0
+    if Hk < 1 or Hk > _INT:
+        raise FavorError(f"{what}: K must be [B, Hk, L, d]")
+    return B, Hk, L, d
+
+
+def _rotary(Q, K, what, pos, table, sections, pairing, Qo, Ko, stream):
+    if stream is not None:
+        return _on(stream, _rotary, Q, K, what, pos, table, sections, pairing, Qo, Ko, None)
+    B, Hq, L, d, dt, dev = _sizes(what, "Q", Q, True)
+    turns = _turns(what, B, L, dev, pos, table, sections, pairing)
     if Qo is None:
         Qo = torch.empty_like(Q, memory_format=_PLAIN)
     views = _views(what, ("Q", "Q's output"), (Q, Qo), Q.shape, dt, dev)
     Hk = 0
     if K is not None:
-        Hk = K.shape[1] if K.dim() == 4 else 0
-        if Hk < 1 or Hk > _INT:
-            raise FavorError(f"{what}: K must be [B, Hk, L, d]")
-        shape = (B, Hk, L, d)
+        shape = _heads(what, K, B, L, d)
+        Hk = shape[1]
         if Ko is None:
             Ko = torch.empty_like(K, memory_format=_PLAIN)
         views += _views(what, ("K", "K's output"), (K, Ko), shape, dt, dev)
@@ -382,9 +402,7 @@ def _rotary(Q, K, what, pos, table, sections, pairing, Qo, Ko, stream):
         views += (None, None, None, None)
     else:
         raise FavorError(f"{what}: an output for keys without keys")
-    _call(what, dev,
-          (*views, B, Hq, Hk, L, d, pos.data_ptr(), pos.shape[1], n, c_sections,
-           *_flats(what, ("the table (new_rotary_table)",), (table,), (pairs,), dev, torch.int64), pairing, _DT[dt]))
+    _call(what, dev, (*views, B, Hq, Hk, L, d, *turns, _DT[dt]))
     return Qo, Ko
 
 
@@ -402,3 +420,99 @@ def bwd_rotary(dQo, dKo, pos, table, sections, pairing="adjacent", dQ=None, dK=N
     """Gradients (dQ, dK) of fwd_rotary's inputs for those of its outputs: the
     rotation by the opposite angles; arguments as there."""
     return _rotary(dQo, dKo, "favor_bwd_rotary", pos, table, sections, pairing, dQ, dK, stream)
+
+
+def fwd_qk_norm_rotary(Q, K, q_weight, k_weight, pos, table, sections, pairing="adjacent", eps=1e-5, Qo=None, Ko=None,
+                       stream=None):
+    """Root-mean-square norm of Q [B, H, L, d] and K [B, Hk, L, d] (or None) over
+    d, with the weights q_weight and k_weight (fp32 [d], None: 1), and their
+    rotation by the tokens' positions as in fwd_rotary, in one pass.  Returns
+    (Qo, Ko), contiguous where none is given; Qo may be Q, Ko may be K."""
+    if stream is not None:
+        return _on(stream, fwd_qk_norm_rotary, Q, K, q_weight, k_weight, pos, table, sections, pairing, eps, Qo, Ko)
+    what = "favor_fwd_qk_norm_rotary"
+    B, Hq, L, d, dt, dev = _sizes(what, "Q", Q, True)
+    turns = _turns(what, B, L, dev, pos, table, sections, pairing)
+    if Qo is None:
+        Qo = torch.empty_like(Q, memory_format=_PLAIN)
+    views = _views(what, ("Q", "Q's output"), (Q, Qo), Q.shape, dt, dev)
+    Hk = 0
+    if K is not None:
+        shape = _heads(what, K, B, L, d)
+        Hk = shape[1]
+        if Ko is None:
+            Ko = torch.empty_like(K, memory_format=_PLAIN)
+        views += _views(what, ("K", "K's output"), (K, Ko), shape, dt, dev)
+    elif Ko is None and k_weight is None:
+        views += (None, None, None, None)
+    else:
+        raise FavorError(f"{what}: an output or a weight for keys without keys")
+    _call(what, dev,
+          (*views, *_flats(what, ("q_weight", "k_weight"), (q_weight, k_weight), (d,), dev), eps, B, Hq, Hk, L, d,
+           *turns, _DT[dt]))
+    return Qo, Ko
+
+
+def bwd_qk_norm_rotary_workspace_bytes(B: int, Hq: int, Hk: int, L: int, d: int, dtype, device=None) -> int:
+    """Bytes of bwd_qk_norm_rotary's workspace on `device` (None: the current
+    one), whose number of SMs it depends on; Hk = 0: no keys."""
+    if device is not None and device != _current_device():
+        with torch.cuda.device(device):
+            return bwd_qk_norm_rotary_workspace_bytes(B, Hq, Hk, L, d, dtype)
+    n = 0
+    if min(B, Hq, L, d) > 0 <= Hk and max(B, Hq, Hk, L, d) <= _INT:
+        n = load().favor_bwd_qk_norm_rotary_workspace_bytes(B, Hq, Hk, L, d, _DT[dtype])
+    if n == 0:
+        raise FavorError("unsupported shape")
+    return n
+
+
+def bwd_qk_norm_rotary(Q, K, dQo, dKo, q_weight, k_weight, pos, table, sections, pairing="adjacent", eps=1e-5, dQ=None,
+                       dK=None, dq_weight=None, dk_weight=None, workspace=None, stream=None, weight_grads=True):
+    """Gradients (dQ, dK, dq_weight, dk_weight) of fwd_qk_norm_rotary for those
+    of its outputs, dQo and dKo; the other arguments as there (K and dKo None:
+    no keys, dK and dk_weight None).  The weights' gradients are fp32 [d], summed
+    over all rows; weight_grads=False leaves them out (None, None).  dQ may be
+    dQo or Q, dK may be dKo or K."""
+    if stream is not None:
+        return _on(stream, bwd_qk_norm_rotary, Q, K, dQo, dKo, q_weight, k_weight, pos, table, sections, pairing, eps,
+                   dQ, dK, dq_weight, dk_weight, workspace, None, weight_grads)
+    what = "favor_bwd_qk_norm_rotary"
+    B, Hq, L, d, dt, dev = _sizes(what, "Q", Q, True)
+    turns = _turns(what, B, L, dev, pos, table, sections, pairing)
+    if dQ is None:
+        dQ = torch.empty_like(Q, memory_format=_PLAIN)
+    views = _views(what, ("Q", "dQo", "dQ"), (Q, dQo, dQ), Q.shape, dt, dev)
+    Hk = 0
+    if K is not None:
+        shape = _heads(what, K, B, L, d)
+        Hk = shape[1]
+        if dKo is None:
+            raise FavorError(f"{what}: keys without dKo")
+        if dK is None:
+            dK = torch.empty_like(K, memory_format=_PLAIN)
+        views += _views(what, ("K", "dKo", "dK"), (K, dKo, dK), shape, dt, dev)
+    elif dKo is None and dK is None and k_weight is None and dk_weight is None:
+        views += (None,) * 6
+    else:
+        raise FavorError(f"{what}: a gradient or a weight for keys without keys")
+    if weight_grads:
+        if dq_weight is None:
+            dq_weight = torch.empty(d, dtype=torch.float32, device=Q.device)
+        if dk_weight is None and Hk > 0:
+            dk_weight = torch.empty(d, dtype=torch.float32, device=Q.device)
+        if workspace is None:
+            workspace = torch.empty(bwd_qk_norm_rotary_workspace_bytes(B, Hq, Hk, L, d, dt, dev), dtype=torch.uint8,
+                                    device=Q.device)
+    elif dq_weight is not None or dk_weight is not None:
+        raise FavorError(f"{what}: a weight's gradient given with weight_grads=False")
+    ws, nbytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise FavorError(f"{what}: the workspace must be contiguous on cuda:{dev}")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(what, dev,
+          (*views, *_flats(what, ("q_weight", "k_weight", "dq_weight", "dk_weight"),
+                           (q_weight, k_weight, dq_weight, dk_weight), (d,), dev), eps, B, Hq, Hk, L, d, *turns,
+           _DT[dt], ws, nbytes))
+    return dQ, dK, dq_weight, dk_weight

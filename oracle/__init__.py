@@ -8,4 +8,5 @@ never imports it, and it never imports the product path.
 """
 
 from .favor import *  # noqa: F401,F403
+from .decay import *  # noqa: F401,F403
 from .sequence import *  # noqa: F401,F403
