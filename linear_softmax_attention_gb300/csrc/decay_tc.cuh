@@ -1,0 +1,28 @@
+// Tensor-core path of the causal linear attention with a decay per head.
+#pragma once
+
+#include "decay.cuh"
+
+namespace favor {
+
+// bf16, whole 16-byte pieces, no broadcast axis
+bool decay_tc_takes(const View* const* views, int n, bool bf16, int d);
+void decay_tc_plan(DecayShape* s);
+// a view and whether it is read or written, encoded once per call
+struct DecayMap {
+  alignas(64) unsigned char bytes[128];
+};
+bool decay_tc_map(DecayMap* map, const View& v);
+
+struct DecayTcPass {
+  DecayPass p;
+  const DecayMap *a, *b, *c, *o;
+};
+struct DecayTcGain {
+  DecayGain p;
+  const DecayMap *b, *c;
+};
+cudaError_t decay_tc_pass(const DecayTcPass& p, const DecayShape& s, cudaStream_t stream);
+cudaError_t decay_tc_gains(const DecayTcGain* gains, int n, const DecayShape& s, cudaStream_t stream);
+
+}  // namespace favor

@@ -3,7 +3,7 @@
 #include <cmath>
 #include <initializer_list>
 
-#include "decay.cuh"
+#include "decay_tc.cuh"
 #include "favor_selftest.h"
 #include "ops.cuh"
 
@@ -449,9 +449,12 @@ struct Flat {
 };
 
 size_t decay_workspace(int B, int H, int L, int d, bool backward) {
+  // what either path may need, whatever the tensors' alignment
   favor::DecayShape s = decay_shape(nullptr, nullptr, nullptr, B, H, L, d);
   favor::decay_simt_plan(&s);
-  const int64_t states = s.segs > 1 ? decay_states(s) : 0;
+  int64_t states = s.segs > 1 ? decay_states(s) : 0;
+  favor::decay_tc_plan(&s);
+  if (s.segs > 1) states = std::max(states, decay_states(s));
   return (size_t)states * (backward ? 2 : 1) * sizeof(float);
 }
 
@@ -730,11 +733,18 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   const bool bf16 = dt == FAVOR_BF16;
   const int piece = common_piece({&vq, &vk, &vv});
   favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
-  favor::decay_simt_plan(&s);
+  const View* all[4] = {&vq, &vk, &vv, &vo};
+  favor::DecayMap maps[4];
+  bool tc = favor::decay_tc_takes(all, 4, bf16, d);
+  for (int i = 0; i < 4 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
+  if (tc) favor::decay_tc_plan(&s);
+  else favor::decay_simt_plan(&s);
   float* ws = s.segs > 1 ? static_cast<float*>(workspace) : nullptr;
   if (ws != nullptr) {
     const favor::DecayGain gain{k, v, vk.strides(), vv.strides(), ws, 1.f, false};
-    cudaError_t err = favor::decay_simt_gains(&gain, 1, s, bf16, piece, strm);
+    const favor::DecayTcGain tc_gain{gain, &maps[1], &maps[2]};
+    cudaError_t err = tc ? favor::decay_tc_gains(&tc_gain, 1, s, strm)
+                         : favor::decay_simt_gains(&gain, 1, s, bf16, piece, strm);
     const favor::DecayScan scan{ws, S0, ST, false};
     if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
     if (err != cudaSuccess) return FAVOR_ERR_CUDA;
@@ -752,6 +762,7 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   p.last = ws != nullptr ? nullptr : ST;
   p.s_w = p.s_r = scale;
   p.s_u = 1.f;
+  if (tc) return done(favor::decay_tc_pass({p, &maps[0], &maps[1], &maps[2], &maps[3]}, s, strm));
   return done(favor::decay_simt_pass(p, s, bf16, piece, strm));
 }
 
@@ -806,13 +817,20 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
   const bool bf16 = dt == FAVOR_BF16;
   const int piece = common_piece({&in[0], &in[1], &in[2], &in[3]});
   favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
-  favor::decay_simt_plan(&s);
+  const View* all[7] = {&in[0], &in[1], &in[2], &in[3], &out[0], &out[1], &out[2]};
+  favor::DecayMap maps[7];
+  bool tc = favor::decay_tc_takes(all, 7, bf16, d);
+  for (int i = 0; i < 7 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
+  if (tc) favor::decay_tc_plan(&s);
+  else favor::decay_simt_plan(&s);
   float* ws = s.segs > 1 ? static_cast<float*>(workspace) : nullptr;
   float* ws_r = ws != nullptr ? ws + decay_states(s) : nullptr;
   if (ws != nullptr) {
     const favor::DecayGain gains[2] = {{k, v, in[1].strides(), in[2].strides(), ws, 1.f, false},
                                        {q, d_o, in[0].strides(), in[3].strides(), ws_r, scale, true}};
-    cudaError_t err = favor::decay_simt_gains(gains, 2, s, bf16, piece, strm);
+    const favor::DecayTcGain tc_gains[2] = {{gains[0], &maps[1], &maps[2]}, {gains[1], &maps[0], &maps[3]}};
+    cudaError_t err = tc ? favor::decay_tc_gains(tc_gains, 2, s, strm)
+                         : favor::decay_simt_gains(gains, 2, s, bf16, piece, strm);
     const favor::DecayScan scans[2] = {{ws, S0, nullptr, false}, {ws_r, dST, dS0, true}};
     if (err == cudaSuccess) err = favor::decay_scan_states(scans, 2, s, strm);
     if (err != cudaSuccess) return FAVOR_ERR_CUDA;
@@ -838,7 +856,9 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     p.s_w = scale;
     p.s_r = i == 0 ? scale : 1.f;
     p.s_u = i == 0 ? 1.f : scale;
-    const cudaError_t err = favor::decay_simt_pass(p, s, bf16, piece, strm);
+    const cudaError_t err =
+        tc ? favor::decay_tc_pass({p, &maps[abc[i][0]], &maps[abc[i][1]], &maps[abc[i][2]], &maps[4 + i]}, s, strm)
+           : favor::decay_simt_pass(p, s, bf16, piece, strm);
     if (err != cudaSuccess) return FAVOR_ERR_CUDA;
   }
   return FAVOR_OK;
