@@ -7,22 +7,29 @@ namespace favor {
 
 // bf16, whole 16-byte pieces, no broadcast axis
 bool decay_tc_takes(const View* const* views, int n, bool bf16, int d);
-void decay_tc_plan(DecayShape* s);
+// segments for `passes` passes side by side
+void decay_tc_plan(DecayShape* s, int passes);
 // a view and whether it is read or written, encoded once per call
 struct DecayMap {
   alignas(64) unsigned char bytes[128];
 };
 bool decay_tc_map(DecayMap* map, const View& v);
 
+// p.start NULL: each segment takes `edge` (the state at the sequence's near end,
+// NULL: zeros) through the gains of the segments before it, and the last one
+// writes p.last; neither may then be written by the same launch.
 struct DecayTcPass {
   DecayPass p;
+  const float *edge, *gains;
+  bool after_gains;          // the launch before in the stream is decay_tc_gains'
   const DecayMap *a, *b, *c, *o;
 };
 struct DecayTcGain {
   DecayGain p;
   const DecayMap *b, *c;
 };
-cudaError_t decay_tc_pass(const DecayTcPass& p, const DecayShape& s, cudaStream_t stream);
+// up to three side by side
+cudaError_t decay_tc_passes(const DecayTcPass* passes, int n, const DecayShape& s, cudaStream_t stream);
 cudaError_t decay_tc_gains(const DecayTcGain* gains, int n, const DecayShape& s, cudaStream_t stream);
 
 }  // namespace favor

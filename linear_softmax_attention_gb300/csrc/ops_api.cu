@@ -448,15 +448,21 @@ struct Flat {
   }
 };
 
-size_t decay_workspace(int B, int H, int L, int d, bool backward) {
+size_t decay_workspace(int B, int H, int L, int d, favor_dtype dt, bool backward) {
   // what either path may need, whatever the tensors' alignment
   favor::DecayShape s = decay_shape(nullptr, nullptr, nullptr, B, H, L, d);
   favor::decay_simt_plan(&s);
   int64_t states = s.segs > 1 ? decay_states(s) : 0;
-  favor::decay_tc_plan(&s);
-  if (s.segs > 1) states = std::max(states, decay_states(s));
+  if (dt == FAVOR_BF16) {
+    favor::decay_tc_plan(&s, backward ? 3 : 1);
+    states = std::max(states, decay_states(s));
+  }
   return (size_t)states * (backward ? 2 : 1) * sizeof(float);
 }
+
+// Segments whose gains the passes themselves add up (each segment those before
+// it); above, a scan of its own: see decay_tc_passes for what it cost.
+constexpr int kDecayInPass = 16;
 
 favor_status workspace_ok(const void* ws, size_t have, size_t need) {
   if (need == 0) return FAVOR_OK;
@@ -695,7 +701,7 @@ size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, in
 
 size_t favor_decay_attention_workspace_bytes(int B, int H, int L, int d, favor_dtype dt, int backward) {
   if (decay_sizes(B, H, L, d, dt) != FAVOR_OK) return 0;
-  return decay_workspace(B, H, L, d, backward != 0);
+  return decay_workspace(B, H, L, d, dt, backward != 0);
 }
 
 favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
@@ -713,7 +719,7 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
       !favor::make_view(&vv, v, v_strides, B, H, L, d, e) || !favor::make_view(&vo, o, o_strides, B, H, L, d, e))
     return FAVOR_ERR_INVALID_ARG;
   const int64_t states = (int64_t)B * H * d * d;
-  const size_t need = decay_workspace(B, H, L, d, false);
+  const size_t need = decay_workspace(B, H, L, d, dt, false);
   st = workspace_ok(workspace, ws_bytes, need);
   if (st != FAVOR_OK) return st;
   Flat flat;
@@ -737,18 +743,6 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   favor::DecayMap maps[4];
   bool tc = favor::decay_tc_takes(all, 4, bf16, d);
   for (int i = 0; i < 4 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
-  if (tc) favor::decay_tc_plan(&s);
-  else favor::decay_simt_plan(&s);
-  float* ws = s.segs > 1 ? static_cast<float*>(workspace) : nullptr;
-  if (ws != nullptr) {
-    const favor::DecayGain gain{k, v, vk.strides(), vv.strides(), ws, 1.f, false};
-    const favor::DecayTcGain tc_gain{gain, &maps[1], &maps[2]};
-    cudaError_t err = tc ? favor::decay_tc_gains(&tc_gain, 1, s, strm)
-                         : favor::decay_simt_gains(&gain, 1, s, bf16, piece, strm);
-    const favor::DecayScan scan{ws, S0, ST, false};
-    if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
-    if (err != cudaSuccess) return FAVOR_ERR_CUDA;
-  }
   favor::DecayPass p{};
   p.a = q;
   p.b = k;
@@ -758,12 +752,38 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   p.bs = vk.strides();
   p.cs = vv.strides();
   p.os = vo.strides();
-  p.start = ws != nullptr ? ws : S0;
-  p.last = ws != nullptr ? nullptr : ST;
   p.s_w = p.s_r = scale;
   p.s_u = 1.f;
-  if (tc) return done(favor::decay_tc_pass({p, &maps[0], &maps[1], &maps[2], &maps[3]}, s, strm));
-  return done(favor::decay_simt_pass(p, s, bf16, piece, strm));
+  if (tc) favor::decay_tc_plan(&s, 1);
+  else favor::decay_simt_plan(&s);
+  float* ws = static_cast<float*>(workspace);
+  const favor::DecayGain gain{k, v, vk.strides(), vv.strides(), ws, 1.f, false};
+  const favor::DecayScan scan{ws, S0, ST, false};
+  cudaError_t err = cudaSuccess;
+  if (!tc) {
+    if (s.segs > 1) {
+      err = favor::decay_simt_gains(&gain, 1, s, bf16, piece, strm);
+      if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
+    }
+    p.start = s.segs > 1 ? ws : S0;
+    p.last = s.segs > 1 ? nullptr : ST;
+    if (err == cudaSuccess) err = favor::decay_simt_pass(p, s, bf16, piece, strm);
+    return done(err);
+  }
+  favor::DecayTcPass pass{p, S0, ws, false, &maps[0], &maps[1], &maps[2], &maps[3]};
+  if (s.segs > 1 || ST != nullptr) {
+    const favor::DecayTcGain tc_gain{gain, &maps[1], &maps[2]};
+    err = favor::decay_tc_gains(&tc_gain, 1, s, strm);
+    if (s.segs > kDecayInPass || (ST != nullptr && ST == S0)) {
+      if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
+      pass.p.start = ws;
+    } else {
+      pass.p.last = ST;
+      pass.after_gains = true;
+    }
+  }
+  if (err == cudaSuccess) err = favor::decay_tc_passes(&pass, 1, s, strm);
+  return done(err);
 }
 
 favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
@@ -789,7 +809,7 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     if (!favor::make_view(&out[i], outp[i], outs[i], B, H, L, d, e) || favor::self_overlap(out[i]))
       return FAVOR_ERR_INVALID_ARG;
   const int64_t states = (int64_t)B * H * d * d;
-  const size_t need = decay_workspace(B, H, L, d, true);
+  const size_t need = decay_workspace(B, H, L, d, dt, true);
   st = workspace_ok(workspace, ws_bytes, need);
   if (st != FAVOR_OK) return st;
   // all that an output may not meet: the flat operands, the inputs and the other outputs
@@ -821,26 +841,19 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
   favor::DecayMap maps[7];
   bool tc = favor::decay_tc_takes(all, 7, bf16, d);
   for (int i = 0; i < 7 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
-  if (tc) favor::decay_tc_plan(&s);
+  if (tc) favor::decay_tc_plan(&s, 3);
   else favor::decay_simt_plan(&s);
-  float* ws = s.segs > 1 ? static_cast<float*>(workspace) : nullptr;
-  float* ws_r = ws != nullptr ? ws + decay_states(s) : nullptr;
-  if (ws != nullptr) {
-    const favor::DecayGain gains[2] = {{k, v, in[1].strides(), in[2].strides(), ws, 1.f, false},
-                                       {q, d_o, in[0].strides(), in[3].strides(), ws_r, scale, true}};
-    const favor::DecayTcGain tc_gains[2] = {{gains[0], &maps[1], &maps[2]}, {gains[1], &maps[0], &maps[3]}};
-    cudaError_t err = tc ? favor::decay_tc_gains(tc_gains, 2, s, strm)
-                         : favor::decay_simt_gains(gains, 2, s, bf16, piece, strm);
-    const favor::DecayScan scans[2] = {{ws, S0, nullptr, false}, {ws_r, dST, dS0, true}};
-    if (err == cudaSuccess) err = favor::decay_scan_states(scans, 2, s, strm);
-    if (err != cudaSuccess) return FAVOR_ERR_CUDA;
-  }
-  // dq, dk, dv: rows a, b, c among q, k, v, do.  dv comes last: it leaves dS0,
-  // which may be the dST that dk reads
+  float *ws = static_cast<float*>(workspace), *ws_r = ws != nullptr ? ws + decay_states(s) : nullptr;
+  const favor::DecayGain gains[2] = {{k, v, in[1].strides(), in[2].strides(), ws, 1.f, false},
+                                     {q, d_o, in[0].strides(), in[3].strides(), ws_r, scale, true}};
+  const favor::DecayScan scans[2] = {{ws, S0, nullptr, false}, {ws_r, dST, dS0, true}};
+  // dq, dk, dv: rows a, b, c among q, k, v, do.  dv comes last: where one segment
+  // leaves dS0 itself, that may be the dST that dk reads
   const int abc[3][3] = {{3, 2, 1}, {2, 3, 0}, {1, 0, 3}};
+  favor::DecayTcPass passes[3] = {};
   for (int i = 0; i < 3; ++i) {
     const View &a = in[abc[i][0]], &b = in[abc[i][1]], &c = in[abc[i][2]];
-    favor::DecayPass p{};
+    favor::DecayPass& p = passes[i].p;
     p.a = a.p;
     p.b = b.p;
     p.c = c.p;
@@ -851,17 +864,44 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     p.os = out[i].strides();
     p.rev = i > 0;
     p.transposed = i < 2;
-    p.start = i == 0 ? (ws != nullptr ? ws : S0) : (ws != nullptr ? ws_r : dST);
-    p.last = i == 2 && ws == nullptr ? dS0 : nullptr;
     p.s_w = scale;
     p.s_r = i == 0 ? scale : 1.f;
     p.s_u = i == 0 ? 1.f : scale;
-    const cudaError_t err =
-        tc ? favor::decay_tc_pass({p, &maps[abc[i][0]], &maps[abc[i][1]], &maps[abc[i][2]], &maps[4 + i]}, s, strm)
-           : favor::decay_simt_pass(p, s, bf16, piece, strm);
-    if (err != cudaSuccess) return FAVOR_ERR_CUDA;
+    passes[i].edge = i == 0 ? S0 : dST;
+    passes[i].gains = i == 0 ? ws : ws_r;
+    passes[i].a = &maps[abc[i][0]];
+    passes[i].b = &maps[abc[i][1]];
+    passes[i].c = &maps[abc[i][2]];
+    passes[i].o = &maps[4 + i];
   }
-  return FAVOR_OK;
+  cudaError_t err = cudaSuccess;
+  if (!tc) {
+    if (s.segs > 1) {
+      err = favor::decay_simt_gains(gains, 2, s, bf16, piece, strm);
+      if (err == cudaSuccess) err = favor::decay_scan_states(scans, 2, s, strm);
+    }
+    for (int i = 0; i < 3 && err == cudaSuccess; ++i) {
+      favor::DecayPass& p = passes[i].p;
+      p.start = s.segs > 1 ? passes[i].gains : passes[i].edge;
+      p.last = i == 2 && s.segs == 1 ? dS0 : nullptr;
+      err = favor::decay_simt_pass(p, s, bf16, piece, strm);
+    }
+    return done(err);
+  }
+  if (s.segs > 1 || dS0 != nullptr) {
+    const favor::DecayTcGain tc_gains[2] = {{gains[0], &maps[1], &maps[2]}, {gains[1], &maps[0], &maps[3]}};
+    const int from = s.segs > 1 ? 0 : 1;                 // one segment: only what dS0 is made of
+    err = favor::decay_tc_gains(tc_gains + from, 2 - from, s, strm);
+    if (s.segs > kDecayInPass || (dS0 != nullptr && dS0 == dST)) {
+      if (err == cudaSuccess) err = favor::decay_scan_states(scans + from, 2 - from, s, strm);
+      for (int i = from; i < 3; ++i) passes[i].p.start = passes[i].gains;
+    } else {
+      passes[2].p.last = dS0;
+      for (auto& p : passes) p.after_gains = true;
+    }
+  }
+  if (err == cudaSuccess) err = favor::decay_tc_passes(passes, 3, s, strm);
+  return done(err);
 }
 
 favor_status favor_decay_attention_step(const void* q, const int64_t* q_strides, const void* k,
