@@ -319,7 +319,8 @@ __global__ void __launch_bounds__(kThreads) decay_scan_kernel(Scans scans, Decay
   if (e >= dd) return;
   const float g2 = s.g[h] * kLog2E;
   const int len = decay_length(s, b);
-  float* st = p.states + (int64_t)bh * s.segs * dd + e;
+  const int64_t step = (int64_t)dd * p.pieces;
+  float* st = p.states + (int64_t)bh * s.segs * step + e;
   float m = p.first == nullptr ? 0.f : p.first[(int64_t)bh * dd + e];
   constexpr int kAhead = 8;
   for (int i0 = 0; i0 < s.segs; i0 += kAhead) {
@@ -327,13 +328,14 @@ __global__ void __launch_bounds__(kThreads) decay_scan_kernel(Scans scans, Decay
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j, seg = p.rev ? s.segs - 1 - i : i;
-      gain[j] = i < s.segs ? st[(int64_t)seg * dd] : 0.f;
+      gain[j] = i < s.segs ? st[seg * step] : 0.f;
+      if (i < s.segs && p.pieces > 1) gain[j] += st[seg * step + dd];
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j, seg = p.rev ? s.segs - 1 - i : i;
       if (i >= s.segs) break;
-      st[(int64_t)seg * dd] = m;
+      st[seg * step] = m;
       const int n = min(max(len - seg * s.seg_tokens, 0), s.seg_tokens);
       if (n > 0) m = decay_power(g2, n) * m + gain[j];
     }

@@ -51,7 +51,7 @@ struct DecayShape {
   int32_t* status;
   int B, H, L, d;
   int segs, seg_tokens;
-  int BH() const { return B * H; }
+  __host__ __device__ int BH() const { return B * H; }
 };
 
 // tokens of sequence b
@@ -76,12 +76,14 @@ cudaError_t decay_simt_gains(const DecayGain* gains, int n, const DecayShape& s,
                              cudaStream_t stream);
 cudaError_t decay_simt_pass(const DecayPass& p, const DecayShape& s, bool bf16, int piece, cudaStream_t stream);
 // gains -> the states that the segments start from, in place; `first` [B H][d][d] (NULL: zeros) before the first
-// segment (behind the last one where rev), `last` what follows the others (NULL: not wanted)
+// segment (behind the last one where rev), `last` what follows the others (NULL: not wanted).  pieces: a segment's
+// gain is the sum of that many, side by side; its state takes the place of the first
 struct DecayScan {
   float* states;
   const float* first;
   float* last;
   bool rev;
+  int pieces;                // 1 or 2
 };
 cudaError_t decay_scan_states(const DecayScan* scans, int n, const DecayShape& s, cudaStream_t stream);
 

@@ -15,7 +15,7 @@
 // rounded once beside o itself: its weight within a chunk, its key across chunks.
 // The decays never appear as l^-j: every factor is a power l^n, n >= 0.
 //
-// A warp of its own issues copies and products; the others share the work on
+// One warp issues the products, one the copies; the others share the work on
 // registers, 32 columns of a quarter of the lanes each:
 //   weights (P -> P')       while the gain's and I's products run before it,
 //   b's faded rows          while O = P' C runs,
@@ -38,7 +38,7 @@ constexpr int kM = 128;              // tokens of a chunk
 template <int D> struct Cfg {
   static constexpr int kParts = D / 32;                    // warps of a quarter of the lanes, 32 columns each
   static constexpr int kEpi = 128 * kParts, kEpiWarps = 4 * kParts;
-  static constexpr int kThreads = kEpi + 32;
+  static constexpr int kThreads = kEpi + 64;
   static constexpr int kCtas = D == 64 ? 2 : 1;            // of an SM
   static constexpr int kAtoms = D / 64;                    // 128-byte columns of a tile
   static constexpr int kTile = kAtoms * kAtom;
@@ -47,20 +47,23 @@ template <int D> struct Cfg {
   static constexpr int kImg = kSlots * kTile;
   static constexpr int kImgAtom = 2 * D * 128;
   static constexpr int kBars = kImg + kAtoms * kImgAtom;
-  static constexpr int kFade = kBars + 160;                // l^0 .. l^128
-  static constexpr int kSmem = kFade + 132 * 4;
+  static constexpr int kPowers = kBars + 144;              // l^15 .. l^0 (walking back: l^0 .. l^15)
+  static constexpr int kDiag = kPowers + 64;               // factors of a diagonal group, see below
+  static constexpr int kFade = kDiag + 64 * 4;             // l^0 .. l^128
+  static constexpr int kSmem = kFade + 129 * 4;
   // tensor memory: P (P' over its first half), O, I, M
   static constexpr uint32_t kCols = D == 64 ? 256 : 512;
   static constexpr uint32_t kP = 0, kO = D == 64 ? 64 : 128, kI = D == 64 ? 128 : 256, kState = D == 64 ? 192 : 384;
-  // the gains: four tiles, and b's rows in three parts
-  static constexpr int kGainSlots = 4;
-  static constexpr int kParts3 = kGainSlots * kTile;
-  static constexpr int kGainBars = kParts3 + 3 * kTile;
+  // the gains (64 of b's columns a CTA): tiles of chunks to come, and b's rows in three parts, twice
+  static constexpr int kDepth = D == 64 ? 3 : 2;
+  static constexpr int kPair = kAtom + kTile;
+  static constexpr int kSplit = kDepth * kPair;
+  static constexpr int kGainBars = kSplit + 2 * 3 * kAtom;
   static constexpr int kGainSmem = kGainBars + 128;
 };
 // an SM's 228 KB, 1 KB of it reserved for each CTA
 static_assert(2 * (Cfg<64>::kSmem + 1024) <= 233472 && Cfg<128>::kSmem <= 232448, "shared memory");
-static_assert(2 * (Cfg<64>::kGainSmem + 1024) <= 233472 && Cfg<128>::kGainSmem <= 232448, "shared memory");
+static_assert(Cfg<64>::kGainSmem <= 232448 && Cfg<128>::kGainSmem <= 232448, "shared memory");
 
 // waits for a phase although other waits have run out: copies and products in
 // flight must end before their memory goes
@@ -85,6 +88,12 @@ __device__ __forceinline__ bool named_bar_or(int id, int count, bool v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+__device__ __forceinline__ float2 both(uint32_t w) { return make_float2(bf_lo(w), bf_hi(w)); }
+__device__ __forceinline__ uint32_t pack2(float2 v) { return pack_bf16(v.x, v.y); }
+template <int N> __device__ __forceinline__ float2 pair(const uint32_t (&x)[N], int e) {
+  return make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+}
+
 // 32 columns of row `row` of a tile times u, rounded to bf16, in their place; 0 where !in
 __device__ __forceinline__ void fade_rows(uint8_t* tile, int row, int part, float u, bool in) {
 #pragma unroll
@@ -93,57 +102,52 @@ __device__ __forceinline__ void fade_rows(uint8_t* tile, int row, int part, floa
     uint4* at = reinterpret_cast<uint4*>(tile + (col >> 6) * kAtom + row * 128 +
                                          ((((col & 63) >> 3) ^ (row & 7)) << 4));
     uint4 w = in ? *at : make_uint4(0, 0, 0, 0);
-    w.x = pack_bf16(bf_lo(w.x) * u, bf_hi(w.x) * u);
-    w.y = pack_bf16(bf_lo(w.y) * u, bf_hi(w.y) * u);
-    w.z = pack_bf16(bf_lo(w.z) * u, bf_hi(w.z) * u);
-    w.w = pack_bf16(bf_lo(w.w) * u, bf_hi(w.w) * u);
+    w.x = pack2(mul2(both(w.x), make_float2(u, u)));
+    w.y = pack2(mul2(both(w.y), make_float2(u, u)));
+    w.z = pack2(mul2(both(w.z), make_float2(u, u)));
+    w.w = pack2(mul2(both(w.w), make_float2(u, u)));
     *at = w;
   }
 }
 
-// the same as three bf16 parts whose sum has all of fp32's bits
-template <int TILE>
+// 32 columns of a row of a 64-column tile times u as three bf16 parts, whose sum has all of fp32's bits
 __device__ __forceinline__ void fade_rows3(const uint8_t* tile, uint8_t* parts, int row, int part, float u, bool in) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int col = part * 32 + c * 8;
-    const int off = (col >> 6) * kAtom + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+    const int off = row * 128 + (((part * 4 + c) ^ (row & 7)) << 4);
     const uint4 raw = in ? *reinterpret_cast<const uint4*>(tile + off) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t h[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float a = bf_lo(w[i]) * u, b = bf_hi(w[i]) * u;
+      float2 a = mul2(both(w[i]), make_float2(u, u));
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        h[k][i] = pack_bf16(a, b);
-        if (k < 2) {
-          a -= bf_lo(h[k][i]);
-          b -= bf_hi(h[k][i]);
-        }
+        h[k][i] = pack2(a);
+        if (k < 2) a = fma2(both(h[k][i]), make_float2(-1.f, -1.f), a);
       }
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      *reinterpret_cast<uint4*>(parts + k * TILE + off) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+      *reinterpret_cast<uint4*>(parts + k * kAtom + off) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
   }
 }
 
 // rows [n, 128) of a tile: 0 (what lies behind a sequence's end may be anything)
 template <int D>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int n, int tid) {
-  for (int e = tid; e < (kM - n) * 8 * Cfg<D>::kAtoms; e += Cfg<D>::kEpi) {
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int n, int tid, int threads) {
+  for (int e = tid; e < (kM - n) * 8 * Cfg<D>::kAtoms; e += threads) {
     const int a = e / ((kM - n) * 8), r = e - a * (kM - n) * 8;
     *reinterpret_cast<uint4*>(tile + a * kAtom + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
   }
 }
 
-// acc (+)= b^T c over a chunk's 128 tokens, b's columns in atoms `lbo` apart (0: at d <= 64
-// the upper half of the lanes repeats the lower one)
-template <int D>
-__device__ __forceinline__ void issue_gain(uint32_t acc, uint32_t b, uint32_t lbo, uint32_t c, bool add) {
-  constexpr uint32_t id = idesc_bf16(kM, D, true, true);
-  const uint64_t a0 = sdesc(b, lbo, 1024), b0 = sdesc(c, kAtom, 1024);
+// acc [128 lanes][N] (+)= a^T b over a chunk's 128 tokens; a's columns in atoms `lbo` apart (0: at
+// d <= 64 the upper half of the lanes repeats the lower one)
+template <int N>
+__device__ __forceinline__ void issue_gain(uint32_t acc, uint32_t a, uint32_t lbo, uint32_t b, bool add) {
+  constexpr uint32_t id = idesc_bf16(kM, N, true, true);
+  const uint64_t a0 = sdesc(a, lbo, 1024), b0 = sdesc(b, kAtom, 1024);
 #pragma unroll
   for (int k = 0; k < kM / 16; ++k) mma_bf16(acc, dadd(a0, kstep_mn(k)), dadd(b0, kstep_mn(k)), id, add || k > 0);
 }
@@ -153,12 +157,14 @@ __device__ __forceinline__ void issue_gain(uint32_t acc, uint32_t b, uint32_t lb
 // ---------------------------------------------------------------------------
 struct PassParams {
   DecayShape s;
-  // What a segment starts from: `start` [B H][segs][d][d] where it is set; else
-  // `edge` [B H][d][d] (NULL: zeros) taken through the gains of the segments
-  // before it, [B H][segs][d][d]; `last`: what the last segment leaves.
+  // What a segment starts from: `start` [B H][segs][2][d][d] (the first of each
+  // two) where it is set; else `edge` [B H][d][d] (NULL: zeros) taken through the
+  // gains of the segments before it, each the sum of two pieces, [B H][segs]
+  // [2][d][d]; `last`: what the last segment leaves.
   const float *start, *edge, *gains;
   float* last;
   bool transposed;                    // all of them hold M^T
+  bool rev;
   float s_w, s_r, s_u;
   const __nv_bfloat16* c;             // for rows with infinities or NaN
   __nv_bfloat16* o;                   // for rows behind a sequence's last chunk
@@ -170,7 +176,7 @@ __device__ __forceinline__ int seg_live(const DecayShape& s, int len, int i) {
   return min(max(len - i * s.seg_tokens, 0), s.seg_tokens);
 }
 
-template <int D, bool REV>
+template <int D>
 __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_c,
                                           const CUtensorMap& map_o, const PassParams& p, uint8_t* sm) {
   using C = Cfg<D>;
@@ -180,10 +186,13 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
   uint64_t* end_bar = full + 14;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* odd_rows = tmem_slot + 2;                                   // [4] rows of c with infinities or NaN
+  uint32_t* odd_rows = reinterpret_cast<uint32_t*>(full + 16);          // [4] rows of c with infinities or NaN
+  float* powers = reinterpret_cast<float*>(sm + C::kPowers);
+  float* diag = reinterpret_cast<float*>(sm + C::kDiag);
   float* fade = reinterpret_cast<float*>(sm + C::kFade);
 
   const DecayShape& s = p.s;
+  const bool rev = p.rev;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.x / s.segs, seg = blockIdx.x - bh * s.segs, b = bh / s.H, h = bh - b * s.H;
   const float g2 = s.g[h] * kLog2E;
@@ -192,7 +201,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
   const int live = stop > first ? (stop - first + kM - 1) / kM : 0;     // chunks with tokens
   const WaitCtx wctx{abort_flag, s.status};
   // the i-th chunk in the pass's order
-  auto token0 = [&](int i) { return first + (REV ? live - 1 - i : i) * kM; };
+  auto token0 = [&](int i) { return first + (rev ? live - 1 - i : i) * kM; };
   auto tokens = [&](int i) { return min(kM, stop - token0(i)); };
   // its tiles: kind 0: b, 1: a, 2: c
   auto slot = [&](int i, int kind) { return sm + ((3 * i + kind) % C::kSlots) * C::kTile; };
@@ -210,14 +219,73 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
   }
-  if (threadIdx.x <= kM) fade[threadIdx.x] = decay_power(g2, threadIdx.x);
+  // diag[31 - i + j]: the weight of column j for row i of a 32 x 32 group on the diagonal
+  for (int e = threadIdx.x; e < 129 + 16 + 63; e += C::kThreads) {
+    const int k = e < 129 ? e : e < 145 ? (rev ? e - 129 : 144 - e) : rev ? e - 145 - 31 : 31 - (e - 145);
+    const float f = k < 0 ? 0.f : decay_power(g2, k);
+    if (e < 129) fade[e] = f;
+    else if (e < 145) powers[e - 129] = f;
+    else diag[e - 145] = f * p.s_w;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == C::kEpiWarps) {
-    // ---- copies and products
+    // ---- products
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0; i < live; ++i) {
+        ok = mbar_wait(slot_full(i, 0), slot_phase(i, 0), wctx) && mbar_wait(slot_full(i, 1), slot_phase(i, 1), wctx);
+        if (!ok) break;
+        const uint64_t a0 = sdesc(smem_addr(slot(i, 1)), 16, 1024);
+        {
+          constexpr uint32_t id = idesc_bf16(kM, kM, false, false);
+          const uint64_t b0 = sdesc(smem_addr(slot(i, 0)), 16, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_bf16(tmem + C::kP, dadd(a0, kstep_k(k, kAtom)), dadd(b0, kstep_k(k, kAtom)), id, k > 0);
+          mma_commit(scores);
+        }
+        constexpr uint32_t id = idesc_bf16(kM, D, false, true);
+        ok = mbar_wait(copy_done, i & 1, wctx);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          const uint64_t m0 = sdesc(smem_addr(sm + C::kImg), C::kImgAtom, 1024);
+#pragma unroll
+          for (int k = 0; k < 2 * D / 16; ++k)
+            mma_bf16(tmem + C::kI, dadd(a0, kstep_k(k % (D / 16), kAtom)), dadd(m0, kstep_mn(k)), id, k > 0);
+        }
+        ok = mbar_wait(slot_full(i, 2), slot_phase(i, 2), wctx) && mbar_wait(weights_done, i & 1, wctx);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t c0 = sdesc(smem_addr(slot(i, 2)), kAtom, 1024);
+#pragma unroll
+        for (int k = 0; k < kM / 16; ++k)
+          mma_bf16_ts(tmem + C::kO, tmem + C::kP + k * 8, dadd(c0, kstep_mn(k)), id, k > 0);
+        mma_commit(out_bar);
+        if (i + 1 < live) {
+          ok = mbar_wait(faded_done, i & 1, wctx);
+          if (!ok) break;
+          tc_fence_after();
+          issue_gain<D>(tmem + C::kState, smem_addr(slot(i, 0)), D == 64 ? 0 : kAtom, smem_addr(slot(i, 2)), true);
+          mma_commit(gain_bar);
+        }
+        ok = mbar_wait(rows_done, i & 1, wctx);                  // P and O are read
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (!ok) {
+        // after a wait that ran out: what is in flight ends before its memory goes
+        mma_commit(end_bar);
+        drain(end_bar, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == C::kEpiWarps + 1) {
+    // ---- copies
     if (lane == 0) {
       uint32_t issued = 0, phases = 0;                           // of the slots
       auto load = [&](int i, int kind) {
@@ -238,75 +306,30 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       load(1, 1);
       if (C::kSlots == 6) load(1, 2);
       bool ok = true;
-      for (int i = 0; i < live && ok; ++i) {
-        const bool more = i + 1 < live;
-        ok = mbar_wait(slot_full(i, 0), slot_phase(i, 0), wctx) && mbar_wait(slot_full(i, 1), slot_phase(i, 1), wctx);
-        if (!ok) break;
-        const uint64_t a0 = sdesc(smem_addr(slot(i, 1)), 16, 1024);
-        {
-          constexpr uint32_t id = idesc_bf16(kM, kM, false, false);
-          const uint64_t b0 = sdesc(smem_addr(slot(i, 0)), 16, 1024);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_bf16(tmem + C::kP, dadd(a0, kstep_k(k, kAtom)), dadd(b0, kstep_k(k, kAtom)), id, k > 0);
-          mma_commit(scores);
-        }
-        if (i > 0) {
-          // the chunk before: b and c are read, and the rows leave from a's place
-          ok = mbar_wait(gain_bar, (i - 1) & 1, wctx);
-          if (!ok) break;
-          if constexpr (C::kSlots == 6) {
-            load(i + 1, 0);
-            load(i + 1, 2);
-          } else {
-            load(i, 2);
-            load(i + 1, 1);
-          }
-        }
-        constexpr uint32_t id = idesc_bf16(kM, D, false, true);
-        ok = mbar_wait(copy_done, i & 1, wctx);
-        if (!ok) break;
-        tc_fence_after();
-        {
-          const uint64_t m0 = sdesc(smem_addr(sm + C::kImg), C::kImgAtom, 1024);
-#pragma unroll
-          for (int k = 0; k < 2 * D / 16; ++k)
-            mma_bf16(tmem + C::kI, dadd(a0, kstep_k(k % (D / 16), kAtom)), dadd(m0, kstep_mn(k)), id, k > 0);
-        }
-        if (i > 0) {
-          bulk_wait_read0();
-          load(i + 1, C::kSlots == 6 ? 1 : 0);
-        }
-        ok = mbar_wait(slot_full(i, 2), slot_phase(i, 2), wctx) && mbar_wait(weights_done, i & 1, wctx);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t c0 = sdesc(smem_addr(slot(i, 2)), kAtom, 1024);
-#pragma unroll
-        for (int k = 0; k < kM / 16; ++k)
-          mma_bf16_ts(tmem + C::kO, tmem + C::kP + k * 8, dadd(c0, kstep_mn(k)), id, k > 0);
-        mma_commit(out_bar);
-        if (more) {
-          ok = mbar_wait(faded_done, i & 1, wctx);
-          if (!ok) break;
-          tc_fence_after();
-          issue_gain<D>(tmem + C::kState, smem_addr(slot(i, 0)), D == 64 ? 0 : kAtom, smem_addr(slot(i, 2)), true);
-          mma_commit(gain_bar);
-        }
+      for (int i = 0; i < live; ++i) {
         ok = mbar_wait(rows_done, i & 1, wctx);
         if (!ok) break;
-        tc_fence_after();
 #pragma unroll
         for (int a = 0; a < C::kAtoms; ++a) tma_store_4d(&map_o, a * 64, token0(i), h, b, slot(i, 1) + a * kAtom);
         bulk_commit();
+        if (i + 1 == live) break;
+        // b and c are read, and the rows leave from a's place
+        ok = mbar_wait(gain_bar, i & 1, wctx);
+        if (!ok) break;
+        if constexpr (C::kSlots == 6) {
+          load(i + 2, 0);
+          load(i + 2, 2);
+        } else {
+          load(i + 1, 2);
+          load(i + 2, 1);
+        }
+        bulk_wait_read0();
+        load(i + 2, C::kSlots == 6 ? 1 : 0);
       }
       bulk_wait0();
-      if (!ok) {
-        // after a wait that ran out: what is in flight ends before its memory goes
+      if (!ok)
         for (int x = 0; x < C::kSlots; ++x)
           if (issued >> x & 1) drain(full + x, phases >> x & 1);
-        mma_commit(end_bar);
-        drain(end_bar, 0);
-      }
     }
     __syncwarp();
   } else {
@@ -320,17 +343,21 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
     auto copy_state = [&](uint32_t (&m)[32], float all) {
       uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(m[2 * e]), __uint_as_float(m[2 * e + 1]));
+      for (int e = 0; e < 16; ++e) w[e] = pack2(pair(m, e));
       const uint32_t img = smem_addr(sm + C::kImg);
       if (D == 128 || t < 64) store_row<16>(img, C::kImgAtom, x, part * 32, w);
       if (D == 128 || t >= 64) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          w[e] = pack_bf16(__uint_as_float(m[2 * e]) - bf_lo(w[e]), __uint_as_float(m[2 * e + 1]) - bf_hi(w[e]));
+          w[e] = pack2(fma2(both(w[e]), make_float2(-1.f, -1.f), pair(m, e)));
         store_row<16>(img, C::kImgAtom, D + x, part * 32, w);
       }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) m[e] = __float_as_uint(__uint_as_float(m[e]) * all);
+      for (int e = 0; e < 16; ++e) {
+        const float2 v = mul2(pair(m, e), make_float2(all, all));
+        m[2 * e] = __float_as_uint(v.x);
+        m[2 * e + 1] = __float_as_uint(v.y);
+      }
       tmem_st32(tmem + C::kState + lane_off + part * 32, m);
       tmem_st_wait();
       fence_proxy_async_smem();
@@ -347,16 +374,16 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       float4* state = reinterpret_cast<float4*>(sm + C::kImg);
       griddep_wait();                                                    // the gains (or states) are written
       const float4* from = reinterpret_cast<const float4*>(
-          p.start != nullptr ? p.start + ((int64_t)bh * s.segs + seg) * dd : p.edge != nullptr ? p.edge + bh * dd : nullptr);
-      const bool lasts = p.last != nullptr && seg == (REV ? 0 : s.segs - 1);
-      const int before = p.start != nullptr ? 0 : REV ? s.segs - 1 - seg : seg;
-      const float4* gains = reinterpret_cast<const float4*>(p.gains + (int64_t)bh * s.segs * dd);
+          p.start != nullptr ? p.start + ((int64_t)bh * s.segs + seg) * 2 * dd : p.edge != nullptr ? p.edge + bh * dd : nullptr);
+      const bool lasts = p.last != nullptr && seg == (rev ? 0 : s.segs - 1);
+      const int before = p.start != nullptr ? 0 : rev ? s.segs - 1 - seg : seg;
+      const float4* gains = reinterpret_cast<const float4*>(p.gains + (int64_t)bh * s.segs * 2 * dd);
       const float whole = decay_power(g2, s.seg_tokens);
       if (d < D) {                                                       // channels behind the d are 0
         for (int e = threadIdx.x; e < D * D / 4; e += C::kEpi) state[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         named_bar(5, C::kEpi);
       }
-      constexpr int kPlaces = 4, kAhead = 4;                             // loads in flight: their product
+      constexpr int kPlaces = 2, kAhead = 4;                             // loads in flight: 2 kPlaces kAhead
 #pragma unroll 1
       for (int e0 = threadIdx.x; e0 < pieces; e0 += kPlaces * C::kEpi) {
         auto piece = [&](const float4* st, int k) {
@@ -366,26 +393,31 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
         auto then = [](float4 m, float all, float4 g) {
           return make_float4(fmaf(m.x, all, g.x), fmaf(m.y, all, g.y), fmaf(m.z, all, g.z), fmaf(m.w, all, g.w));
         };
+        auto sum = [](float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); };
         float4 m[kPlaces];
 #pragma unroll
         for (int k = 0; k < kPlaces; ++k) m[k] = from != nullptr ? piece(from, k) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (int j0 = 0; j0 < before; j0 += kAhead) {
-          float4 gain[kAhead][kPlaces];
+          float4 gain[kAhead][2][kPlaces];
 #pragma unroll
           for (int j = 0; j < kAhead; ++j)
-            if (j0 + j < before)
+            if (j0 + j < before) {
+              const float4* at = gains + (rev ? s.segs - 1 - j0 - j : j0 + j) * (dd / 2);
 #pragma unroll
-              for (int k = 0; k < kPlaces; ++k)
-                gain[j][k] = piece(gains + (REV ? s.segs - 1 - j0 - j : j0 + j) * (dd / 4), k);
+              for (int k = 0; k < kPlaces; ++k) {
+                gain[j][0][k] = piece(at, k);
+                gain[j][1][k] = piece(at + dd / 4, k);
+              }
+            }
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
             if (j0 + j >= before) break;
-            const int n = seg_live(s, len, REV ? s.segs - 1 - j0 - j : j0 + j);
+            const int n = seg_live(s, len, rev ? s.segs - 1 - j0 - j : j0 + j);
             if (n == 0) continue;
             const float all = n == s.seg_tokens ? whole : decay_power(g2, n);
 #pragma unroll
-            for (int k = 0; k < kPlaces; ++k) m[k] = then(m[k], all, gain[j][k]);
+            for (int k = 0; k < kPlaces; ++k) m[k] = then(m[k], all, sum(gain[j][0][k], gain[j][1][k]));
           }
         }
         const int n = seg_live(s, len, seg);
@@ -395,8 +427,10 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
           const int e = e0 + k * C::kEpi, row = e / d4, c = e - row * d4;
           if (e >= pieces) break;
           state[row * (D / 4) + (c ^ (row & 7))] = m[k];
-          if (lasts)
-            reinterpret_cast<float4*>(p.last + bh * dd)[e] = n > 0 ? then(m[k], all, gains[seg * (dd / 4) + e]) : m[k];
+          if (lasts) {
+            const float4* at = gains + seg * (dd / 2) + e;
+            reinterpret_cast<float4*>(p.last + bh * dd)[e] = n > 0 ? then(m[k], all, sum(at[0], at[dd / 4])) : m[k];
+          }
         }
       }
       if (live > 0) {
@@ -428,7 +462,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       // ---- the weights: faded, masked, rounded to bf16
       if (n < kM && token0(i) + n < s.L) {
         mbar_wait(slot_full(i, 2), slot_phase(i, 2), wctx);
-        clear_rows<D>(slot(i, 2), n, threadIdx.x);
+        clear_rows<D>(slot(i, 2), n, threadIdx.x, C::kEpi);
         fence_proxy_async_smem();
       }
       mbar_wait(scores, i & 1, wctx);
@@ -436,11 +470,18 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       tc_fence_after();
       {
         constexpr int G = 4 / C::kParts;                         // groups of 32 columns of a thread
+        float2 power[8];                                         // l^(15 - k), walking back l^k
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float4 v = *reinterpret_cast<const float4*>(powers + 2 * e);
+          power[e] = make_float2(v.x, v.y);
+          power[e + 1] = make_float2(v.z, v.w);
+        }
         uint32_t w[G][16];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const int grp = part * G + g, j0 = grp * 32;
-          if (REV ? grp < q : grp > q) {
+          if (rev ? grp < q : grp > q) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[g][e] = 0u;
             continue;
@@ -448,35 +489,29 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
           uint32_t sc[32];
           tmem_ld32(tmem + C::kP + lane_off + j0, sc);
           tmem_ld_wait();
-          if (grp != q && (!REV || n == kM)) {
-            // whole groups of 16: l^(i - j) = l^(i - j0 - 15) l^(15 - k)
-            float power[16];                                     // l^0 .. l^15
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(power + e) = *reinterpret_cast<const float4*>(fade + e);
+          if (grp != q) {
+            // 16 columns from jh on: l^(t - j) = l^(t - jh - 15) l^(15 - k), l^(j - t) = l^(jh - t) l^k
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const int jh = j0 + 16 * hf;
-              const float base = p.s_w * fade[REV ? jh - t : t - jh - 15];
+              const float base = p.s_w * fade[rev ? j0 + 16 * hf - t : t - j0 - 16 * hf - 15];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float f0 = base * power[REV ? 2 * e : 15 - 2 * e];
-                const float f1 = base * power[REV ? 2 * e + 1 : 14 - 2 * e];
-                w[g][8 * hf + e] = pack_bf16(__uint_as_float(sc[16 * hf + 2 * e]) * f0,
-                                             __uint_as_float(sc[16 * hf + 2 * e + 1]) * f1);
-              }
+              for (int e = 0; e < 8; ++e)
+                w[g][8 * hf + e] = pack2(mul2(pair(sc, 8 * hf + e), mul2(make_float2(base, base), power[e])));
+            }
+            if (rev && n < j0 + 32) {
+              // columns behind the last token (a sequence's last chunk)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w[g][e] &= (j0 + 2 * e < n ? 0xffffu : 0u) | (j0 + 2 * e + 1 < n ? 0xffff0000u : 0u);
             }
           } else {
+            const float* f = diag + 31 - lane;
+            uint32_t in = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+            if (n < j0 + 32) in &= n > j0 ? (1u << (n - j0)) - 1 : 0u;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float v[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int j = j0 + 2 * e + k, apart = REV ? j - t : t - j;
-                const bool in = apart >= 0 && j < n;
-                v[k] = in ? __uint_as_float(sc[2 * e + k]) * (p.s_w * fade[in ? apart : 0]) : 0.f;
-              }
-              w[g][e] = pack_bf16(v[0], v[1]);
+              const float v0 = __uint_as_float(sc[2 * e]) * f[2 * e], v1 = __uint_as_float(sc[2 * e + 1]) * f[2 * e + 1];
+              w[g][e] = pack_bf16(in >> (2 * e) & 1 ? v0 : 0.f, in >> (2 * e + 1) & 1 ? v1 : 0.f);
             }
           }
         }
@@ -494,7 +529,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       // ---- b's faded rows in b's place (P has read it)
       if (i + 1 < live) {
         const int row = threadIdx.x & 127;
-        fade_rows(slot(i, 0), row, threadIdx.x >> 7, row < n ? p.s_u * fade[REV ? row + 1 : n - 1 - row] : 0.f, row < n);
+        fade_rows(slot(i, 0), row, threadIdx.x >> 7, row < n ? p.s_u * fade[rev ? row + 1 : n - 1 - row] : 0.f, row < n);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(faded_done);
@@ -503,8 +538,8 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       mbar_wait(out_bar, i & 1, wctx);
       __syncwarp();
       tc_fence_after();
-      const float r = t < n ? p.s_r * fade[REV ? n - 1 - t : t + 1] : 0.f;
-      auto rows_out = [&](bool patch) {
+      const float r = t < n ? p.s_r * fade[rev ? n - 1 - t : t + 1] : 0.f;
+      for (bool patch = false;;) {
         uint32_t o[32], in[32];
         tmem_ld32(tmem + C::kO + lane_off + part * 32, o);
         tmem_ld32(tmem + C::kI + lane_off + part * 32, in);
@@ -517,7 +552,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
             const uint32_t pair = tmem_ld1(tmem + C::kP + lane_off + (j >> 1));
             tmem_ld_wait();
             const float w = j & 1 ? bf_hi(pair) : bf_lo(pair);
-            const bool sees = REV ? j >= t : j <= t;
+            const bool sees = rev ? j >= t : j <= t;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int y = part * 32 + e;
@@ -526,25 +561,23 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
             }
           }
         }
-        float bad = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) bad = fmaf(__uint_as_float(o[e]), 0.f, bad);
+        float2 bad = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float v0 = fmaf(__uint_as_float(in[2 * e]), r, __uint_as_float(o[2 * e]));
-          const float v1 = fmaf(__uint_as_float(in[2 * e + 1]), r, __uint_as_float(o[2 * e + 1]));
-          o[e] = t < n ? pack_bf16(v0, v1) : 0u;
+          const float2 v = pair(o, e);
+          bad = fma2(v, make_float2(0.f, 0.f), bad);
+          o[e] = t < n ? pack2(fma2(pair(in, e), make_float2(r, r), v)) : 0u;
         }
         store_row<16>(smem_addr(slot(i, 1)), kAtom, t, part * 32, o);
-        return t < n && bad != 0.f;
-      };
-      // rare: a product with zero weights has met infinities or NaN of rows that must not be seen
-      if (named_bar_or(5, C::kEpi, rows_out(false))) {
+        // rare: a product with zero weights has met infinities or NaN of rows that must not be seen
+        const bool odd = named_bar_or(5, C::kEpi, !patch && t < n && bad.x + bad.y != 0.f);
+        if (!odd) break;
         uint8_t* ct = slot(i, 2);
         if (threadIdx.x < 4) odd_rows[threadIdx.x] = 0;
         // the gain has read c
         if (i + 1 < live) mbar_wait(gain_bar, i & 1, wctx);
         named_bar(5, C::kEpi);
+#pragma unroll 1
         for (int e = threadIdx.x; e < C::kTile / 16; e += C::kEpi) {
           uint4 raw = *reinterpret_cast<const uint4*>(ct + e * 16);
           uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -573,7 +606,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
           tc_fence_after();
           constexpr uint32_t id = idesc_bf16(kM, D, false, true);
           const uint64_t c0 = sdesc(smem_addr(ct), kAtom, 1024);
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < kM / 16; ++k)
             mma_bf16_ts(tmem + C::kO, tmem + C::kP + k * 8, dadd(c0, kstep_mn(k)), id, k > 0);
           mma_commit(again_bar);
@@ -583,8 +616,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
         ++again;
         __syncwarp();
         tc_fence_after();
-        rows_out(true);
-        named_bar(5, C::kEpi);                                   // odd_rows is read
+        patch = true;
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -622,7 +654,6 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
 struct Passes {
   CUtensorMap a[3], b[3], c[3], o[3];
   PassParams p[3];
-  bool rev[3];
 };
 
 template <int D>
@@ -634,28 +665,81 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     if (threadIdx.x == 0) report_status(ps.p[k].s.status, FAVOR_ERR_CUDA);
     return;
   }
-  if (ps.rev[k]) pass_body<D, true>(ps.a[k], ps.b[k], ps.c[k], ps.o[k], ps.p[k], smem);
-  else pass_body<D, false>(ps.a[k], ps.b[k], ps.c[k], ps.o[k], ps.p[k], smem);
+  pass_body<D>(ps.a[k], ps.b[k], ps.c[k], ps.o[k], ps.p[k], smem);
 }
 
 // ---------------------------------------------------------------------------
 // The gains of the segments: sum_j u(j) b_j c_j^T, every factor reaching to the
-// segment's end (its front, walking back).
+// segment's end (its front, walking back).  A CTA takes 64 of b's columns: at
+// d <= 128 two neighbouring CTAs share c's tiles through L2.  The chunks of all
+// kinds, halves and heads are one list, of which every CTA takes an even share:
+// a segment may be cut in two pieces, [0] from its front and [1], which are kept
+// side by side (a share is never shorter than a segment).
+// Eight warps split b's rows in three parts while the tensor cores take the chunk
+// before, c^T [hi | middle | low] in one product, and four warps add the sums of
+// the one before that up in registers.
 // ---------------------------------------------------------------------------
 struct GainParams {
   DecayShape s;
-  float* out[2];
+  float* out[2];                      // [B H][segs][2][d][d]
   float s_u[2];
   bool rev[2];
+  int chunks, per, halves;            // of a sequence, of a segment; of b's columns
+  long long total;                    // entries of the list: [kind][head][half][chunk]
 };
 struct GainMaps {
   CUtensorMap b[2], c[2];
 };
-// chunks in one accumulator (at d <= 128 it takes all three parts' products)
-template <int D> constexpr int kGroup = D == 64 ? 2 : 1;
+constexpr int kSplitWarps = 8, kTakeWarps = 4, kGainThreads = 32 * (kSplitWarps + kTakeWarps + 2);
+
+// One CTA's share of the list as runs, each inside one segment.
+struct Runs {
+  const GainParams& p;
+  long long x, x1;
+  int kind, bh, b, h, half, seg, c0, c1, len;                    // the run's chunks [c0, c1) of its sequence
+  __device__ __forceinline__ Runs(const GainParams& prm, long long from, long long to) : p(prm), x(from), x1(to) {
+    const long long row = from / p.chunks;                       // [kind][b][h][half]
+    c1 = (int)(from - row * p.chunks);
+    half = (int)(row % p.halves);
+    const int r = (int)(row / p.halves);
+    kind = r >= p.s.BH();
+    bh = r - kind * p.s.BH();
+    b = bh / p.s.H;
+    h = bh - b * p.s.H;
+    seg = c1 / p.per;
+    len = x < x1 ? decay_length(p.s, b) : 0;
+  }
+  __device__ __forceinline__ bool next() {
+    if (x >= x1) return false;
+    if (c1 == p.chunks) {                                        // the next row's first segment
+      c1 = seg = 0;
+      if (++half == p.halves) {
+        half = 0;
+        ++bh;
+        if (++h == p.s.H) {
+          h = 0;
+          if (++b == p.s.B) b = bh = 0, ++kind;
+          len = decay_length(p.s, b);
+        }
+      }
+    } else if (c1 == (seg + 1) * p.per) {
+      ++seg;
+    }
+    c0 = c1;
+    c1 = (int)min((long long)min((seg + 1) * p.per, p.chunks), c0 + (x1 - x));
+    x += c1 - c0;
+    return true;
+  }
+  __device__ __forceinline__ int first() const { return seg * p.s.seg_tokens; }
+  __device__ __forceinline__ int stop() const { return min(min(first() + p.s.seg_tokens, p.s.L), len); }
+  // chunks of the run that have tokens
+  __device__ __forceinline__ int live() const {
+    return min(max((stop() - c0 * kM + kM - 1) / kM, 0), c1 - c0);
+  }
+};
 
 template <int D>
-__global__ void __launch_bounds__(Cfg<D>::kEpi, Cfg<D>::kCtas)
+__global__ void __launch_bounds__(kGainThreads, 1)
     decay_tc_gain_kernel(const __grid_constant__ GainMaps maps, const __grid_constant__ GainParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -666,33 +750,27 @@ __global__ void __launch_bounds__(Cfg<D>::kEpi, Cfg<D>::kCtas)
     if (threadIdx.x == 0) report_status(s.status, FAVOR_ERR_CUDA);
     return;
   }
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kGainBars);
-  uint64_t *full = bars, *done = bars + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 5);
+  uint64_t *b_full = reinterpret_cast<uint64_t*>(sm + C::kGainBars), *c_full = b_full + 3;   // [kDepth]
+  uint64_t *split = b_full + 6, *done = b_full + 8, *taken = b_full + 10, *end_bar = b_full + 12;   // [2] but the last
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 13);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int kind = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = warp & 3, part = warp >> 2, t = 32 * q + lane;
-  const uint32_t lane_off = static_cast<uint32_t>(32 * q) << 16;
-  const int bh = blockIdx.x / s.segs, seg = blockIdx.x - bh * s.segs, b = bh / s.H, h = bh - b * s.H;
-  const float g2 = s.g[h] * kLog2E;
-  const int first = seg * s.seg_tokens, stop = min(min(first + s.seg_tokens, s.L), decay_length(s, b));
-  const int live = stop > first ? (stop - first + kM - 1) / kM : 0;
   const WaitCtx wctx{abort_flag, s.status};
-  const CUtensorMap *map_b = &maps.b[kind], *map_c = &maps.c[kind];
-  const bool rev = p.rev[kind];
-  const float s_u = p.s_u[kind];
-  auto slot = [&](int i, int k) { return sm + ((2 * i + k) % C::kGainSlots) * C::kTile; };
-  auto slot_full = [&](int i, int k) { return full + (2 * i + k) % C::kGainSlots; };
-  auto slot_phase = [&](int i, int k) { return ((2 * i + k) / C::kGainSlots) & 1; };
-  constexpr uint32_t kCols = 128;                                // d <= 64: hi and middle parts' sums, the low parts'
+  const long long x0 = p.total * blockIdx.x / gridDim.x, x1 = p.total * (blockIdx.x + 1) / gridDim.x;
+  // lane = c's column; columns: b's 64 columns' three parts, twice
+  constexpr uint32_t kCols = 512, kAcc = 192, kAccStep = 256;
+  auto tile_b = [&](int j) { return sm + j % C::kDepth * C::kPair; };
+  auto tile_c = [&](int j) { return sm + j % C::kDepth * C::kPair + kAtom; };
+  auto parts = [&](int j) { return sm + C::kSplit + (j & 1) * 3 * kAtom; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 5; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 13; ++i)
+      mbar_init(b_full + i, i == 6 || i == 7 ? kSplitWarps : i == 10 || i == 11 ? kTakeWarps : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 0) {
+  constexpr int kProducts = kSplitWarps + kTakeWarps;
+  if (warp == kProducts) {
     tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
   }
@@ -700,116 +778,142 @@ __global__ void __launch_bounds__(Cfg<D>::kEpi, Cfg<D>::kCtas)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const bool loader = threadIdx.x == 32, issuer = threadIdx.x == 0;
-  int loads = 0, commits = 0;
-  auto load = [&](int i, int k) {
-    if (i >= live || *abort_flag) return;
-    ++loads;
-    uint64_t* bar = slot_full(i, k);
-    mbar_arrive_expect_tx(bar, C::kTile);
-#pragma unroll
-    for (int a = 0; a < C::kAtoms; ++a)
-      tma_load_4d(slot(i, k) + a * kAtom, k == 0 ? map_b : map_c, a * 64, first + i * kM, h, b, bar);
-  };
-  if (loader) {
-    load(0, 0);
-    load(0, 1);
-    load(1, 0);
-  }
-  const int row = threadIdx.x & 127;
-  float sum[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) sum[e] = 0.f;
-  auto take = [&] {
-    uint32_t x[32];
-    tmem_ld32(tmem + lane_off + part * 32, x);
-    tmem_ld_wait();
-#pragma unroll
-    for (int e = 0; e < 32; ++e) sum[e] += __uint_as_float(x[e]);
-    if constexpr (D == 64) {
-      if (t < 64) {                                              // whole warps
-        tmem_ld32(tmem + 64 + lane_off + part * 32, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) sum[e] += __uint_as_float(x[e]);
+
+  if (warp == kProducts) {
+    // ---- products
+    if (lane == 0) {
+      Runs run(p, x0, x1);
+      bool ok = true;
+      int j = 0;
+      while (ok && run.next()) {
+        const int live = run.live();
+        for (int i = 0; i < live; ++i, ++j) {
+          ok = mbar_wait(c_full + j % C::kDepth, j / C::kDepth & 1, wctx) &&
+               mbar_wait(split + (j & 1), j >> 1 & 1, wctx) &&
+               (j < 2 || mbar_wait(taken + (j & 1), (j - 2) >> 1 & 1, wctx));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_addr(parts(j)), c = smem_addr(tile_c(j));
+          issue_gain<kAcc>(tmem + (j & 1) * kAccStep, c, D == 64 ? 0 : kAtom, a, false);
+          mma_commit(done + (j & 1));
+        }
+      }
+      if (!ok) {
+        mma_commit(end_bar);
+        drain(end_bar, 0);
       }
     }
-    tc_fence_before();
-  };
-  for (int i = 0; i < live; ++i) {
-    const int t0 = first + i * kM, n = min(kM, stop - t0);
-    const float u = row < n ? s_u * decay_power(g2, rev ? t0 + row - first + 1 : stop - 1 - t0 - row) : 0.f;
-    mbar_wait(slot_full(i, 0), slot_phase(i, 0), wctx);
-    if (i > 0) {
-      mbar_wait(done, (i - 1) & 1, wctx);                        // the product before has read b's parts
-      if (i % kGroup<D> == 0) {
+    __syncwarp();
+  } else if (warp == kProducts + 1) {
+    // ---- copies, kDepth chunks ahead
+    if (lane == 0) {
+      Runs run(p, x0, x1);
+      bool ok = true;
+      int j = 0, jc = 0;
+      while (ok && run.next()) {
+        const int live = run.live();
+        for (int i = 0; i < live; ++i) {
+          const int t0 = (run.c0 + i) * kM, slot = j % C::kDepth, before = j - C::kDepth;
+          // b's place is free once its rows are split, c's once the products have ended
+          if (before >= 0 && !(ok = mbar_wait(split + (before & 1), before >> 1 & 1, wctx))) break;
+          mbar_arrive_expect_tx(b_full + slot, kAtom);
+          tma_load_4d(tile_b(j), &maps.b[run.kind], run.half * 64, t0, run.h, run.b, b_full + slot);
+          ++j;
+          if (before >= 0 && !(ok = mbar_wait(done + (before & 1), before >> 1 & 1, wctx))) break;
+          mbar_arrive_expect_tx(c_full + slot, C::kTile);
+#pragma unroll
+          for (int a = 0; a < C::kAtoms; ++a)
+            tma_load_4d(tile_c(jc) + a * kAtom, &maps.c[run.kind], a * 64, t0, run.h, run.b, c_full + slot);
+          ++jc;
+        }
+      }
+      if (!ok)
+        for (int k = 0; k < C::kDepth; ++k) {
+          if (k < j) drain(b_full + k, (j - 1 - k) / C::kDepth & 1);
+          if (k < jc) drain(c_full + k, (jc - 1 - k) / C::kDepth & 1);
+        }
+    }
+    __syncwarp();
+  } else if (warp < kSplitWarps) {
+    // ---- b's rows in three parts
+    const int row = threadIdx.x & 127;
+    Runs run(p, x0, x1);
+    int j = 0, h = -1;                                           // chunks so far
+    float g2 = 0.f;
+    while (run.next()) {
+      if (run.h != h) {
+        h = run.h;
+        g2 = s.g[h] * kLog2E;
+      }
+      const float s_u = p.s_u[run.kind];
+      const bool rev = p.rev[run.kind];
+      const int first = run.first(), stop = run.stop(), live = run.live();
+      for (int i = 0; i < live; ++i, ++j) {
+        const int t0 = (run.c0 + i) * kM, n = min(kM, stop - t0), at = t0 + row;
+        const float u = row < n ? s_u * decay_power(g2, rev ? at - first + 1 : stop - 1 - at) : 0.f;
+        mbar_wait(b_full + j % C::kDepth, j / C::kDepth & 1, wctx);
+        if (j >= 2) mbar_wait(done + (j & 1), (j - 2) >> 1 & 1, wctx);         // the parts' place is read
+        fade_rows3(tile_b(j), parts(j), row, threadIdx.x >> 7, u, row < n);
+        if (n < kM && t0 + n < s.L) {
+          mbar_wait(c_full + j % C::kDepth, j / C::kDepth & 1, wctx);
+          clear_rows<D>(tile_c(j), n, threadIdx.x, 32 * kSplitWarps);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(split + (j & 1));
+      }
+    }
+  } else {
+    // ---- the sums: lane = c's column y, N of b's columns from col on (at d <= 64 two lanes hold the same ones)
+    const int q = warp & 3, t = 32 * q + lane, y = t & (D - 1), d = s.d;
+    constexpr int N = D / 2;
+    const int col = t / D * N;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + col;
+    float sum[N];
+    Runs run(p, x0, x1);
+    int j = 0;
+    while (run.next()) {
+      const int live = run.live();
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] = 0.f;
+      for (int i = 0; i < live; ++i, ++j) {
+        mbar_wait(done + (j & 1), j >> 1 & 1, wctx);
         __syncwarp();
         tc_fence_after();
-        take();
-      }
-    }
-    fade_rows3<C::kTile>(slot(i, 0), sm + C::kParts3, row, threadIdx.x >> 7, u, row < n);
-    if (n < kM && t0 + n < s.L) {
-      mbar_wait(slot_full(i, 1), slot_phase(i, 1), wctx);
-      clear_rows<D>(slot(i, 1), n, threadIdx.x);
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (issuer) {
-      const bool in = mbar_wait(slot_full(i, 1), slot_phase(i, 1), wctx);
-      if (in && !*abort_flag) {
-        tc_fence_after();
-        const uint32_t parts = smem_addr(sm + C::kParts3), c = smem_addr(slot(i, 1));
-        const bool add = i % kGroup<D> > 0;
-        issue_gain<D>(tmem, parts, kAtom, c, add);
-        if constexpr (D == 64) {
-          issue_gain<D>(tmem + 64, parts + 2 * C::kTile, 0, c, add);
-        } else {
-          issue_gain<D>(tmem, parts + C::kTile, kAtom, c, true);
-          issue_gain<D>(tmem, parts + 2 * C::kTile, kAtom, c, true);
+#pragma unroll
+        for (int n = 0; n < N; n += 8) {
+          uint32_t v[3][8];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tmem_ld8(at + (j & 1) * kAccStep + k * 64 + n, v[k]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sum[n + e] += __uint_as_float(v[0][e]) + (__uint_as_float(v[1][e]) + __uint_as_float(v[2][e]));
         }
-        mma_commit(done);
-        ++commits;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(taken + (j & 1));
+      }
+      if (y < d) {
+        const int64_t dd = (int64_t)d * d;
+        const bool front = run.c0 == run.seg * p.per, whole = front && run.c1 == min((run.seg + 1) * p.per, p.chunks);
+        float* out = p.out[run.kind] + (((int64_t)run.bh * s.segs + run.seg) * 2 + (front ? 0 : 1)) * dd +
+                     (int64_t)(run.half * 64 + col) * d + y;
+        const int left = d - run.half * 64 - col;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if (e < left) {
+            out[e * d] = sum[e];
+            if (whole) out[dd + e * d] = 0.f;
+          }
+        }
       }
     }
-    if (loader) {
-      load(i + 1, 1);
-      load(i + 2, 0);
-    }
-    __syncwarp();
   }
-  if (live > 0) {
-    mbar_wait(done, (live - 1) & 1, wctx);
-    __syncwarp();
-    tc_fence_after();
-    take();
-  }
-  const int x = t & (D - 1);
-  if constexpr (D == 64) {
-    // the middle parts' sums join the others
-    float* buf = reinterpret_cast<float*>(sm + C::kParts3);
-    if (t >= 64)
-#pragma unroll
-      for (int e = 0; e < 32; ++e) buf[x * 65 + part * 32 + e] = sum[e];
-    __syncthreads();
-    if (t < 64)
-#pragma unroll
-      for (int e = 0; e < 32; ++e) sum[e] += buf[x * 65 + part * 32 + e];
-  }
-  if ((D == 128 || t < 64) && x < s.d) {
-    float* out = p.out[kind] + (int64_t)blockIdx.x * s.d * s.d + x * s.d;
-#pragma unroll
-    for (int e = 0; e < 32; e += 4)                              // d is a multiple of 8
-      if (part * 32 + e < s.d)
-        *reinterpret_cast<float4*>(out + part * 32 + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-  }
-  if (loader)
-    for (int k = max(0, loads - C::kGainSlots); k < loads; ++k) drain(full + k % C::kGainSlots, (k / C::kGainSlots) & 1);
-  if (issuer && commits > 0) drain(done, (commits - 1) & 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, kCols);
+  if (warp == kProducts) tmem_dealloc(tmem, kCols);
 }
 
 CUtensorMap map_of(const DecayMap& m) {
@@ -845,7 +949,7 @@ cudaError_t run_passes(const DecayTcPass* passes, int n, const DecayShape& s, cu
     p.o = static_cast<__nv_bfloat16*>(a.p.o);
     p.cs = a.p.cs;
     p.os = a.p.os;
-    ps.rev[i] = a.p.rev;
+    p.rev = a.p.rev;
   }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -875,7 +979,13 @@ cudaError_t run_gains(const DecayTcGain* gains, int n, const DecayShape& s, cuda
     p.s_u[i] = gains[i].p.s_u;
     p.rev[i] = gains[i].p.rev;
   }
-  kernel<<<dim3(s.segs * s.BH(), n), Cfg<D>::kEpi, Cfg<D>::kGainSmem, stream>>>(maps, p);
+  p.chunks = (s.L + kM - 1) / kM;
+  p.per = s.seg_tokens / kM;
+  p.halves = s.d > 64 ? 2 : 1;
+  p.total = (long long)n * s.BH() * p.halves * p.chunks;
+  // shares that are no shorter than a segment
+  const int ctas = (int)std::max<long long>(1, std::min<long long>(sm_count(), p.total / p.per));
+  kernel<<<ctas, kGainThreads, Cfg<D>::kGainSmem, stream>>>(maps, p);
   return cudaGetLastError();
 }
 

@@ -455,7 +455,7 @@ size_t decay_workspace(int B, int H, int L, int d, favor_dtype dt, bool backward
   int64_t states = s.segs > 1 ? decay_states(s) : 0;
   if (dt == FAVOR_BF16) {
     favor::decay_tc_plan(&s, backward ? 3 : 1);
-    states = std::max(states, decay_states(s));
+    states = std::max(states, 2 * decay_states(s));          // in two pieces
   }
   return (size_t)states * (backward ? 2 : 1) * sizeof(float);
 }
@@ -758,7 +758,7 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   else favor::decay_simt_plan(&s);
   float* ws = static_cast<float*>(workspace);
   const favor::DecayGain gain{k, v, vk.strides(), vv.strides(), ws, 1.f, false};
-  const favor::DecayScan scan{ws, S0, ST, false};
+  const favor::DecayScan scan{ws, S0, ST, false, tc ? 2 : 1};
   cudaError_t err = cudaSuccess;
   if (!tc) {
     if (s.segs > 1) {
@@ -843,10 +843,10 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
   for (int i = 0; i < 7 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
   if (tc) favor::decay_tc_plan(&s, 3);
   else favor::decay_simt_plan(&s);
-  float *ws = static_cast<float*>(workspace), *ws_r = ws != nullptr ? ws + decay_states(s) : nullptr;
+  float *ws = static_cast<float*>(workspace), *ws_r = ws != nullptr ? ws + (tc ? 2 : 1) * decay_states(s) : nullptr;
   const favor::DecayGain gains[2] = {{k, v, in[1].strides(), in[2].strides(), ws, 1.f, false},
                                      {q, d_o, in[0].strides(), in[3].strides(), ws_r, scale, true}};
-  const favor::DecayScan scans[2] = {{ws, S0, nullptr, false}, {ws_r, dST, dS0, true}};
+  const favor::DecayScan scans[2] = {{ws, S0, nullptr, false, tc ? 2 : 1}, {ws_r, dST, dS0, true, tc ? 2 : 1}};
   // dq, dk, dv: rows a, b, c among q, k, v, do.  dv comes last: where one segment
   // leaves dS0 itself, that may be the dST that dk reads
   const int abc[3][3] = {{3, 2, 1}, {2, 3, 0}, {1, 0, 3}};
