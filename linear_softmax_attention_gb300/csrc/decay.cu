@@ -15,7 +15,6 @@ constexpr int kPS = kC + 4;          // row of the weights tile
 // ---- tiles in shared memory -----------------------------------------------------
 template <int DP> struct Tile {
   static constexpr int S = DP + 4;   // row: 16-byte pieces of neighbouring rows fall on other banks
-  static constexpr int kBytes = kC * S * 4;
 };
 
 // Rows [t0, t0 + n) of one head into fp32 tile rows, zeros behind them and
@@ -310,37 +309,56 @@ struct Scans {
   DecayScan kind[2];
 };
 
-// One thread per element of a head's state, eight segments' loads in flight.
-__global__ void __launch_bounds__(kThreads) decay_scan_kernel(Scans scans, DecayShape s) {
+// A thread takes V neighbouring elements of a head's state through its segments,
+// AHEAD segments' gains in flight.
+template <int V, int AHEAD>
+__global__ void __launch_bounds__(kThreads) decay_scan_kernel(Scans scans, DecayShape s, int blocks) {
+  // the passes may take their places and wait
+  asm volatile("griddepcontrol.launch_dependents;");
   const DecayScan& p = scans.kind[blockIdx.z];
-  const int dd = s.d * s.d, blocks = (dd + kThreads - 1) / kThreads;
+  const int dd = s.d * s.d;
   const int bh = blockIdx.x / blocks, b = bh / s.H, h = bh - b * s.H;
-  const int e = (blockIdx.x - bh * blocks) * kThreads + threadIdx.x;
+  const int e = ((blockIdx.x - bh * blocks) * kThreads + threadIdx.x) * V;
   if (e >= dd) return;
-  const float g2 = s.g[h] * kLog2E;
-  const int len = decay_length(s, b);
   const int64_t step = (int64_t)dd * p.pieces;
   float* st = p.states + (int64_t)bh * s.segs * step + e;
-  float m = p.first == nullptr ? 0.f : p.first[(int64_t)bh * dd + e];
-  constexpr int kAhead = 8;
-  for (int i0 = 0; i0 < s.segs; i0 += kAhead) {
-    float gain[kAhead];
+  const float g2 = s.g[h] * kLog2E;
+  const int len = decay_length(s, b);
+  const float whole = decay_power(g2, s.seg_tokens);
+  tc::griddep_wait();
+  float m[V];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+  for (int v = 0; v < V; ++v) m[v] = 0.f;
+  if (p.first != nullptr) load_v<V>(m, p.first + (int64_t)bh * dd + e);
+  for (int i0 = 0; i0 < s.segs; i0 += AHEAD) {
+    float gain[AHEAD][2][V];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
       const int i = i0 + j, seg = p.rev ? s.segs - 1 - i : i;
-      gain[j] = i < s.segs ? st[seg * step] : 0.f;
-      if (i < s.segs && p.pieces > 1) gain[j] += st[seg * step + dd];
+      if (i < s.segs) {
+        load_v<V>(gain[j][0], st + seg * step);
+        if (p.pieces > 1) load_v<V>(gain[j][1], st + seg * step + dd);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       const int i = i0 + j, seg = p.rev ? s.segs - 1 - i : i;
       if (i >= s.segs) break;
-      st[seg * step] = m;
+      if constexpr (V == 4) *reinterpret_cast<float4*>(st + seg * step) = make_float4(m[0], m[1], m[2], m[3]);
+      else st[seg * step] = m[0];
       const int n = min(max(len - seg * s.seg_tokens, 0), s.seg_tokens);
-      if (n > 0) m = decay_power(g2, n) * m + gain[j];
+      if (n == 0) continue;
+      const float all = n == s.seg_tokens ? whole : decay_power(g2, n);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        m[v] = fmaf(all, m[v], p.pieces > 1 ? gain[j][0][v] + gain[j][1][v] : gain[j][0][v]);
     }
   }
-  if (p.last != nullptr) p.last[(int64_t)bh * dd + e] = m;
+  if (p.last != nullptr) {
+    float* last = p.last + (int64_t)bh * dd + e;
+#pragma unroll
+    for (int v = 0; v < V; ++v) last[v] = m[v];
+  }
 }
 
 // One token of one sequence and head.  Bound by memory: the state is read and
@@ -458,8 +476,21 @@ cudaError_t decay_simt_gains(const DecayGain* gains, int n, const DecayShape& s,
 cudaError_t decay_scan_states(const DecayScan* scans, int n, const DecayShape& s, cudaStream_t stream) {
   Scans g{};
   for (int i = 0; i < n; ++i) g.kind[i] = scans[i];
-  decay_scan_kernel<<<dim3((s.d * s.d + kThreads - 1) / kThreads * s.BH(), 1, n), kThreads, 0, stream>>>(g, s);
-  return cudaGetLastError();
+  // 16-byte pieces where there are threads enough, else single elements with twice the segments in flight
+  bool wide = (int64_t)s.BH() * n * s.d * s.d >= (int64_t)4 * kThreads * sm_count() && s.d % 2 == 0;
+  for (int i = 0; i < n; ++i) wide = wide && reinterpret_cast<uintptr_t>(scans[i].first) % 16 == 0;
+  const int per = kThreads * (wide ? 4 : 1), blocks = (s.d * s.d + per - 1) / per;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(blocks * s.BH()), 1, (unsigned)n);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return wide ? cudaLaunchKernelEx(&cfg, decay_scan_kernel<4, 8>, g, s, blocks)
+              : cudaLaunchKernelEx(&cfg, decay_scan_kernel<1, 16>, g, s, blocks);
 }
 
 cudaError_t launch_decay_step(const DecayStep& p, bool bf16, cudaStream_t stream) {

@@ -64,7 +64,8 @@ __device__ __forceinline__ float decay_power(float g2, int n) { return n == 0 ? 
 // Segments of a sequence, about `ctas` over all of them, of whole chunks
 inline void decay_segments(DecayShape* s, int chunk, int ctas) {
   const int chunks = (s->L + chunk - 1) / chunk;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(chunks, ctas / std::max(1, s->BH())));
+  // (no more than 128: a scan takes them one after another)
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min(chunks, 128), ctas / std::max(1, s->BH())));
   const int per = (int)((chunks + want - 1) / want);
   s->segs = (chunks + per - 1) / per;
   s->seg_tokens = per * chunk;

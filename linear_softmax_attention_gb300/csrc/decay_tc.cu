@@ -55,11 +55,11 @@ template <int D> struct Cfg {
   static constexpr uint32_t kCols = D == 64 ? 256 : 512;
   static constexpr uint32_t kP = 0, kO = D == 64 ? 64 : 128, kI = D == 64 ? 128 : 256, kState = D == 64 ? 192 : 384;
   // the gains (64 of b's columns a CTA): tiles of chunks to come, and b's rows in three parts, twice
-  static constexpr int kDepth = D == 64 ? 3 : 2;
-  static constexpr int kPair = kAtom + kTile;
-  static constexpr int kSplit = kDepth * kPair;
+  static constexpr int kDepthB = D == 64 ? 4 : 2, kDepthC = D == 64 ? 4 : 3;
+  static constexpr int kTilesC = kDepthB * kAtom;
+  static constexpr int kSplit = kTilesC + kDepthC * kTile;
   static constexpr int kGainBars = kSplit + 2 * 3 * kAtom;
-  static constexpr int kGainSmem = kGainBars + 128;
+  static constexpr int kGainSmem = kGainBars + 136;
 };
 // an SM's 228 KB, 1 KB of it reserved for each CTA
 static_assert(2 * (Cfg<64>::kSmem + 1024) <= 233472 && Cfg<128>::kSmem <= 232448, "shared memory");
@@ -157,24 +157,16 @@ __device__ __forceinline__ void issue_gain(uint32_t acc, uint32_t a, uint32_t lb
 // ---------------------------------------------------------------------------
 struct PassParams {
   DecayShape s;
-  // What a segment starts from: `start` [B H][segs][2][d][d] (the first of each
-  // two) where it is set; else `edge` [B H][d][d] (NULL: zeros) taken through the
-  // gains of the segments before it, each the sum of two pieces, [B H][segs]
-  // [2][d][d]; `last`: what the last segment leaves.
-  const float *start, *edge, *gains;
-  float* last;
-  bool transposed;                    // all of them hold M^T
+  // what each segment starts from, `step` elements apart, NULL: zeros
+  const float* start;
+  int64_t step;
+  bool transposed;                    // it holds M^T
   bool rev;
   float s_w, s_r, s_u;
   const __nv_bfloat16* c;             // for rows with infinities or NaN
   __nv_bfloat16* o;                   // for rows behind a sequence's last chunk
   Strides cs, os;
 };
-
-// tokens of segment i of a sequence of len
-__device__ __forceinline__ int seg_live(const DecayShape& s, int len, int i) {
-  return min(max(len - i * s.seg_tokens, 0), s.seg_tokens);
-}
 
 template <int D>
 __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_c,
@@ -366,71 +358,26 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       if (lane == 0) mbar_arrive(copy_done);
     };
 
-    // The state that the segment starts from, 16 bytes of it at a time with eight segments' gains in flight, through
-    // the copy's place in shared memory ([D][D] fp32, 16-byte pieces of row x moved by x mod 8).
+    // The state that the segment starts from, through the copy's place in shared memory ([D][D] fp32, 16-byte pieces of
+    // row x moved by x mod 8).
     {
-      const int d = s.d, d4 = d / 4, pieces = d * d4;
-      const int64_t dd = (int64_t)d * d;
+      const int d = s.d, d4 = d / 4;
       float4* state = reinterpret_cast<float4*>(sm + C::kImg);
-      griddep_wait();                                                    // the gains (or states) are written
-      const float4* from = reinterpret_cast<const float4*>(
-          p.start != nullptr ? p.start + ((int64_t)bh * s.segs + seg) * 2 * dd : p.edge != nullptr ? p.edge + bh * dd : nullptr);
-      const bool lasts = p.last != nullptr && seg == (rev ? 0 : s.segs - 1);
-      const int before = p.start != nullptr ? 0 : rev ? s.segs - 1 - seg : seg;
-      const float4* gains = reinterpret_cast<const float4*>(p.gains + (int64_t)bh * s.segs * 2 * dd);
-      const float whole = decay_power(g2, s.seg_tokens);
-      if (d < D) {                                                       // channels behind the d are 0
-        for (int e = threadIdx.x; e < D * D / 4; e += C::kEpi) state[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        named_bar(5, C::kEpi);
-      }
-      constexpr int kPlaces = 2, kAhead = 4;                             // loads in flight: 2 kPlaces kAhead
-#pragma unroll 1
-      for (int e0 = threadIdx.x; e0 < pieces; e0 += kPlaces * C::kEpi) {
-        auto piece = [&](const float4* st, int k) {
-          const int e = e0 + k * C::kEpi;
-          return e < pieces ? st[e] : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        auto then = [](float4 m, float all, float4 g) {
-          return make_float4(fmaf(m.x, all, g.x), fmaf(m.y, all, g.y), fmaf(m.z, all, g.z), fmaf(m.w, all, g.w));
-        };
-        auto sum = [](float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); };
+      griddep_wait();                                                    // the states are written
+      const float4* from = reinterpret_cast<const float4*>(p.start + ((int64_t)bh * s.segs + seg) * p.step);
+      constexpr int kPlaces = 4;
+#pragma unroll
+      for (int e0 = threadIdx.x; e0 < D * D / 4; e0 += kPlaces * C::kEpi) {
         float4 m[kPlaces];
 #pragma unroll
-        for (int k = 0; k < kPlaces; ++k) m[k] = from != nullptr ? piece(from, k) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int j0 = 0; j0 < before; j0 += kAhead) {
-          float4 gain[kAhead][2][kPlaces];
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j)
-            if (j0 + j < before) {
-              const float4* at = gains + (rev ? s.segs - 1 - j0 - j : j0 + j) * (dd / 2);
-#pragma unroll
-              for (int k = 0; k < kPlaces; ++k) {
-                gain[j][0][k] = piece(at, k);
-                gain[j][1][k] = piece(at + dd / 4, k);
-              }
-            }
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            if (j0 + j >= before) break;
-            const int n = seg_live(s, len, rev ? s.segs - 1 - j0 - j : j0 + j);
-            if (n == 0) continue;
-            const float all = n == s.seg_tokens ? whole : decay_power(g2, n);
-#pragma unroll
-            for (int k = 0; k < kPlaces; ++k) m[k] = then(m[k], all, sum(gain[j][0][k], gain[j][1][k]));
-          }
+        for (int k = 0; k < kPlaces; ++k) {
+          const int e = e0 + k * C::kEpi, row = e / (D / 4), c = e & (D / 4 - 1);
+          m[k] = p.start != nullptr && row < d && c < d4 ? from[row * d4 + c] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const int n = seg_live(s, len, seg);
-        const float all = decay_power(g2, n);
 #pragma unroll
         for (int k = 0; k < kPlaces; ++k) {
-          const int e = e0 + k * C::kEpi, row = e / d4, c = e - row * d4;
-          if (e >= pieces) break;
+          const int e = e0 + k * C::kEpi, row = e / (D / 4), c = e & (D / 4 - 1);
           state[row * (D / 4) + (c ^ (row & 7))] = m[k];
-          if (lasts) {
-            const float4* at = gains + seg * (dd / 2) + e;
-            reinterpret_cast<float4*>(p.last + bh * dd)[e] = n > 0 ? then(m[k], all, sum(at[0], at[dd / 4])) : m[k];
-          }
         }
       }
       if (live > 0) {
@@ -670,11 +617,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 
 // ---------------------------------------------------------------------------
 // The gains of the segments: sum_j u(j) b_j c_j^T, every factor reaching to the
-// segment's end (its front, walking back).  A CTA takes 64 of b's columns: at
-// d <= 128 two neighbouring CTAs share c's tiles through L2.  The chunks of all
-// kinds, halves and heads are one list, of which every CTA takes an even share:
-// a segment may be cut in two pieces, [0] from its front and [1], which are kept
-// side by side (a share is never shorter than a segment).
+// segment's end (its front, walking back).  The chunks of all kinds and heads are
+// one list, of which every CTA takes an even share: a segment may be cut in two
+// pieces, [0] from its front and [1], which are kept side by side (a share is
+// never shorter than a segment).  A CTA takes 64 of b's columns: at d <= 128 two
+// neighbours have one share and meet c's tiles in L2.
 // Eight warps split b's rows in three parts while the tensor cores take the chunk
 // before, c^T [hi | middle | low] in one product, and four warps add the sums of
 // the one before that up in registers.
@@ -684,8 +631,8 @@ struct GainParams {
   float* out[2];                      // [B H][segs][2][d][d]
   float s_u[2];
   bool rev[2];
-  int chunks, per, halves;            // of a sequence, of a segment; of b's columns
-  long long total;                    // entries of the list: [kind][head][half][chunk]
+  int chunks, per;                    // of a sequence, of a segment
+  long long total;                    // entries of the list: [kind][head][chunk]
 };
 struct GainMaps {
   CUtensorMap b[2], c[2];
@@ -696,14 +643,12 @@ constexpr int kSplitWarps = 8, kTakeWarps = 4, kGainThreads = 32 * (kSplitWarps 
 struct Runs {
   const GainParams& p;
   long long x, x1;
-  int kind, bh, b, h, half, seg, c0, c1, len;                    // the run's chunks [c0, c1) of its sequence
+  int kind, bh, b, h, seg, c0, c1, len;                    // the run's chunks [c0, c1) of its sequence
   __device__ __forceinline__ Runs(const GainParams& prm, long long from, long long to) : p(prm), x(from), x1(to) {
-    const long long row = from / p.chunks;                       // [kind][b][h][half]
-    c1 = (int)(from - row * p.chunks);
-    half = (int)(row % p.halves);
-    const int r = (int)(row / p.halves);
-    kind = r >= p.s.BH();
-    bh = r - kind * p.s.BH();
+    const int row = (int)(from / p.chunks);                      // [kind][b][h]
+    c1 = (int)(from - (long long)row * p.chunks);
+    kind = row >= p.s.BH();
+    bh = row - kind * p.s.BH();
     b = bh / p.s.H;
     h = bh - b * p.s.H;
     seg = c1 / p.per;
@@ -713,14 +658,11 @@ struct Runs {
     if (x >= x1) return false;
     if (c1 == p.chunks) {                                        // the next row's first segment
       c1 = seg = 0;
-      if (++half == p.halves) {
-        half = 0;
-        ++bh;
-        if (++h == p.s.H) {
-          h = 0;
-          if (++b == p.s.B) b = bh = 0, ++kind;
-          len = decay_length(p.s, b);
-        }
+      ++bh;
+      if (++h == p.s.H) {
+        h = 0;
+        if (++b == p.s.B) b = bh = 0, ++kind;
+        len = decay_length(p.s, b);
       }
     } else if (c1 == (seg + 1) * p.per) {
       ++seg;
@@ -750,22 +692,24 @@ __global__ void __launch_bounds__(kGainThreads, 1)
     if (threadIdx.x == 0) report_status(s.status, FAVOR_ERR_CUDA);
     return;
   }
-  uint64_t *b_full = reinterpret_cast<uint64_t*>(sm + C::kGainBars), *c_full = b_full + 3;   // [kDepth]
-  uint64_t *split = b_full + 6, *done = b_full + 8, *taken = b_full + 10, *end_bar = b_full + 12;   // [2] but the last
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 13);
+  uint64_t *b_full = reinterpret_cast<uint64_t*>(sm + C::kGainBars), *c_full = b_full + 4;
+  uint64_t *split = b_full + 8, *done = b_full + 10, *taken = b_full + 12, *end_bar = b_full + 14;   // [2] but the last
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wctx{abort_flag, s.status};
-  const long long x0 = p.total * blockIdx.x / gridDim.x, x1 = p.total * (blockIdx.x + 1) / gridDim.x;
+  const int half = D == 64 ? 0 : blockIdx.x & 1, share = D == 64 ? blockIdx.x : blockIdx.x >> 1;
+  const int shares = D == 64 ? gridDim.x : gridDim.x >> 1;
+  const long long x0 = p.total * share / shares, x1 = p.total * (share + 1) / shares;
   // lane = c's column; columns: b's 64 columns' three parts, twice
   constexpr uint32_t kCols = 512, kAcc = 192, kAccStep = 256;
-  auto tile_b = [&](int j) { return sm + j % C::kDepth * C::kPair; };
-  auto tile_c = [&](int j) { return sm + j % C::kDepth * C::kPair + kAtom; };
+  auto tile_b = [&](int j) { return sm + j % C::kDepthB * kAtom; };
+  auto tile_c = [&](int j) { return sm + C::kTilesC + j % C::kDepthC * C::kTile; };
   auto parts = [&](int j) { return sm + C::kSplit + (j & 1) * 3 * kAtom; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 13; ++i)
-      mbar_init(b_full + i, i == 6 || i == 7 ? kSplitWarps : i == 10 || i == 11 ? kTakeWarps : 1);
+    for (int i = 0; i < 15; ++i)
+      mbar_init(b_full + i, i == 8 || i == 9 ? kSplitWarps : i == 12 || i == 13 ? kTakeWarps : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -773,6 +717,11 @@ __global__ void __launch_bounds__(kGainThreads, 1)
   if (warp == kProducts) {
     tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
+  } else if (threadIdx.x == 32 * (kProducts + 1)) {
+    for (int k = 0; k < 2; ++k) {
+      prefetch_tmap(&maps.b[k]);
+      prefetch_tmap(&maps.c[k]);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -782,21 +731,31 @@ __global__ void __launch_bounds__(kGainThreads, 1)
   if (warp == kProducts) {
     // ---- products
     if (lane == 0) {
-      Runs run(p, x0, x1);
-      bool ok = true;
-      int j = 0;
-      while (ok && run.next()) {
-        const int live = run.live();
-        for (int i = 0; i < live; ++i, ++j) {
-          ok = mbar_wait(c_full + j % C::kDepth, j / C::kDepth & 1, wctx) &&
-               mbar_wait(split + (j & 1), j >> 1 & 1, wctx) &&
-               (j < 2 || mbar_wait(taken + (j & 1), (j - 2) >> 1 & 1, wctx));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = smem_addr(parts(j)), c = smem_addr(tile_c(j));
-          issue_gain<kAcc>(tmem + (j & 1) * kAccStep, c, D == 64 ? 0 : kAtom, a, false);
-          mma_commit(done + (j & 1));
+      int n = 0;                                                 // chunks of the share
+      for (Runs run(p, x0, x1); run.next();) n += run.live();
+      bool ok = true, ready = false;
+      constexpr uint32_t id = idesc_bf16(kM, kAcc, true, true);
+      for (int j = 0; j < n; ++j) {
+        uint64_t* const waits[3] = {c_full + j % C::kDepthC, split + (j & 1), taken + (j & 1)};
+        ok = ready || (mbar_wait(waits[0], j / C::kDepthC & 1, wctx) && mbar_wait(waits[1], j >> 1 & 1, wctx) &&
+                       (j < 2 || mbar_wait(waits[2], (j - 2) >> 1 & 1, wctx)));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a0 = sdesc(smem_addr(tile_c(j)), D == 64 ? 0 : kAtom, 1024);
+        const uint64_t b0 = sdesc(smem_addr(parts(j)), kAtom, 1024);
+        const uint32_t acc = tmem + (j & 1) * kAccStep;
+#pragma unroll
+        for (int k = 0; k < kM / 16; ++k) {
+          mma_bf16(acc, dadd(a0, kstep_mn(k)), dadd(b0, kstep_mn(k)), id, k > 0);
+          // what the next chunk waits for is looked at while products are queued
+          if (k == kM / 16 - 3 && j + 1 < n) {
+            const int x = j + 1;
+            ready = mbar_test_wait(smem_addr(c_full + x % C::kDepthC), x / C::kDepthC & 1) &&
+                    mbar_test_wait(smem_addr(split + (x & 1)), x >> 1 & 1) &&
+                    (x < 2 || mbar_test_wait(smem_addr(taken + (x & 1)), (x - 2) >> 1 & 1));
+          }
         }
+        mma_commit(done + (j & 1));
       }
       if (!ok) {
         mma_commit(end_bar);
@@ -813,25 +772,25 @@ __global__ void __launch_bounds__(kGainThreads, 1)
       while (ok && run.next()) {
         const int live = run.live();
         for (int i = 0; i < live; ++i) {
-          const int t0 = (run.c0 + i) * kM, slot = j % C::kDepth, before = j - C::kDepth;
+          const int t0 = (run.c0 + i) * kM;
           // b's place is free once its rows are split, c's once the products have ended
-          if (before >= 0 && !(ok = mbar_wait(split + (before & 1), before >> 1 & 1, wctx))) break;
-          mbar_arrive_expect_tx(b_full + slot, kAtom);
-          tma_load_4d(tile_b(j), &maps.b[run.kind], run.half * 64, t0, run.h, run.b, b_full + slot);
+          const int xb = j - C::kDepthB, xc = j - C::kDepthC;
+          if (xb >= 0 && !(ok = mbar_wait(split + (xb & 1), xb >> 1 & 1, wctx))) break;
+          mbar_arrive_expect_tx(b_full + j % C::kDepthB, kAtom);
+          tma_load_4d(tile_b(j), &maps.b[run.kind], half * 64, t0, run.h, run.b, b_full + j % C::kDepthB);
           ++j;
-          if (before >= 0 && !(ok = mbar_wait(done + (before & 1), before >> 1 & 1, wctx))) break;
-          mbar_arrive_expect_tx(c_full + slot, C::kTile);
+          if (xc >= 0 && !(ok = mbar_wait(done + (xc & 1), xc >> 1 & 1, wctx))) break;
+          mbar_arrive_expect_tx(c_full + jc % C::kDepthC, C::kTile);
 #pragma unroll
           for (int a = 0; a < C::kAtoms; ++a)
-            tma_load_4d(tile_c(jc) + a * kAtom, &maps.c[run.kind], a * 64, t0, run.h, run.b, c_full + slot);
+            tma_load_4d(tile_c(jc) + a * kAtom, &maps.c[run.kind], a * 64, t0, run.h, run.b, c_full + jc % C::kDepthC);
           ++jc;
         }
       }
-      if (!ok)
-        for (int k = 0; k < C::kDepth; ++k) {
-          if (k < j) drain(b_full + k, (j - 1 - k) / C::kDepth & 1);
-          if (k < jc) drain(c_full + k, (jc - 1 - k) / C::kDepth & 1);
-        }
+      if (!ok) {
+        for (int k = 0; k < C::kDepthB && k < j; ++k) drain(b_full + k, (j - 1 - k) / C::kDepthB & 1);
+        for (int k = 0; k < C::kDepthC && k < jc; ++k) drain(c_full + k, (jc - 1 - k) / C::kDepthC & 1);
+      }
     }
     __syncwarp();
   } else if (warp < kSplitWarps) {
@@ -851,11 +810,11 @@ __global__ void __launch_bounds__(kGainThreads, 1)
       for (int i = 0; i < live; ++i, ++j) {
         const int t0 = (run.c0 + i) * kM, n = min(kM, stop - t0), at = t0 + row;
         const float u = row < n ? s_u * decay_power(g2, rev ? at - first + 1 : stop - 1 - at) : 0.f;
-        mbar_wait(b_full + j % C::kDepth, j / C::kDepth & 1, wctx);
+        mbar_wait(b_full + j % C::kDepthB, j / C::kDepthB & 1, wctx);
         if (j >= 2) mbar_wait(done + (j & 1), (j - 2) >> 1 & 1, wctx);         // the parts' place is read
         fade_rows3(tile_b(j), parts(j), row, threadIdx.x >> 7, u, row < n);
         if (n < kM && t0 + n < s.L) {
-          mbar_wait(c_full + j % C::kDepth, j / C::kDepth & 1, wctx);
+          mbar_wait(c_full + j % C::kDepthC, j / C::kDepthC & 1, wctx);
           clear_rows<D>(tile_c(j), n, threadIdx.x, 32 * kSplitWarps);
         }
         fence_proxy_async_smem();
@@ -898,8 +857,8 @@ __global__ void __launch_bounds__(kGainThreads, 1)
         const int64_t dd = (int64_t)d * d;
         const bool front = run.c0 == run.seg * p.per, whole = front && run.c1 == min((run.seg + 1) * p.per, p.chunks);
         float* out = p.out[run.kind] + (((int64_t)run.bh * s.segs + run.seg) * 2 + (front ? 0 : 1)) * dd +
-                     (int64_t)(run.half * 64 + col) * d + y;
-        const int left = d - run.half * 64 - col;
+                     (int64_t)(half * 64 + col) * d + y;
+        const int left = d - half * 64 - col;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           if (e < left) {
@@ -938,9 +897,7 @@ cudaError_t run_passes(const DecayTcPass* passes, int n, const DecayShape& s, cu
     PassParams& p = ps.p[i];
     p.s = s;
     p.start = a.p.start;
-    p.edge = a.edge;
-    p.gains = a.gains;
-    p.last = a.p.last;
+    p.step = a.step;
     p.transposed = a.p.transposed;
     p.s_w = a.p.s_w;
     p.s_r = a.p.s_r;
@@ -960,7 +917,7 @@ cudaError_t run_passes(const DecayTcPass* passes, int n, const DecayShape& s, cu
   cfg.dynamicSmemBytes = Cfg<D>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = passes[0].after_gains ? 1 : 0;
+  cfg.numAttrs = passes[0].after_scan ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, ps);
 }
 
@@ -981,11 +938,11 @@ cudaError_t run_gains(const DecayTcGain* gains, int n, const DecayShape& s, cuda
   }
   p.chunks = (s.L + kM - 1) / kM;
   p.per = s.seg_tokens / kM;
-  p.halves = s.d > 64 ? 2 : 1;
-  p.total = (long long)n * s.BH() * p.halves * p.chunks;
+  p.total = (long long)n * s.BH() * p.chunks;
   // shares that are no shorter than a segment
-  const int ctas = (int)std::max<long long>(1, std::min<long long>(sm_count(), p.total / p.per));
-  kernel<<<ctas, kGainThreads, Cfg<D>::kGainSmem, stream>>>(maps, p);
+  constexpr int kHalves = D / 64;
+  const int shares = (int)std::max<long long>(1, std::min<long long>(sm_count() / kHalves, p.total / p.per));
+  kernel<<<shares * kHalves, kGainThreads, Cfg<D>::kGainSmem, stream>>>(maps, p);
   return cudaGetLastError();
 }
 

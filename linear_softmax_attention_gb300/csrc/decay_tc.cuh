@@ -15,13 +15,10 @@ struct DecayMap {
 };
 bool decay_tc_map(DecayMap* map, const View& v);
 
-// p.start NULL: each segment takes `edge` (the state at the sequence's near end,
-// NULL: zeros) through the gains of the segments before it, and the last one
-// writes p.last; neither may then be written by the same launch.
 struct DecayTcPass {
-  DecayPass p;
-  const float *edge, *gains;
-  bool after_gains;          // the launch before in the stream is decay_tc_gains'
+  DecayPass p;               // p.last is not written
+  int64_t step;              // elements between the segments' states
+  bool after_scan;           // the launch before in the stream is decay_scan_states'
   const DecayMap *a, *b, *c, *o;
 };
 struct DecayTcGain {

@@ -460,9 +460,7 @@ size_t decay_workspace(int B, int H, int L, int d, favor_dtype dt, bool backward
   return (size_t)states * (backward ? 2 : 1) * sizeof(float);
 }
 
-// Segments whose gains the passes themselves add up (each segment those before
-// it); above, a scan of its own: see decay_tc_passes for what it cost.
-constexpr int kDecayInPass = 16;
+bool by16(const float* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 favor_status workspace_ok(const void* ws, size_t have, size_t need) {
   if (need == 0) return FAVOR_OK;
@@ -741,7 +739,7 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
   const View* all[4] = {&vq, &vk, &vv, &vo};
   favor::DecayMap maps[4];
-  bool tc = favor::decay_tc_takes(all, 4, bf16, d);
+  bool tc = favor::decay_tc_takes(all, 4, bf16, d) && by16(S0);
   for (int i = 0; i < 4 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
   favor::DecayPass p{};
   p.a = q;
@@ -770,17 +768,16 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
     if (err == cudaSuccess) err = favor::decay_simt_pass(p, s, bf16, piece, strm);
     return done(err);
   }
-  favor::DecayTcPass pass{p, S0, ws, false, &maps[0], &maps[1], &maps[2], &maps[3]};
+  const int64_t dd = (int64_t)d * d;
+  favor::DecayTcPass pass{p, dd, false, &maps[0], &maps[1], &maps[2], &maps[3]};
+  pass.p.start = S0;
   if (s.segs > 1 || ST != nullptr) {
     const favor::DecayTcGain tc_gain{gain, &maps[1], &maps[2]};
     err = favor::decay_tc_gains(&tc_gain, 1, s, strm);
-    if (s.segs > kDecayInPass || (ST != nullptr && ST == S0)) {
-      if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
-      pass.p.start = ws;
-    } else {
-      pass.p.last = ST;
-      pass.after_gains = true;
-    }
+    if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
+    pass.p.start = ws;
+    pass.step = 2 * dd;
+    pass.after_scan = true;
   }
   if (err == cudaSuccess) err = favor::decay_tc_passes(&pass, 1, s, strm);
   return done(err);
@@ -839,7 +836,7 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
   favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
   const View* all[7] = {&in[0], &in[1], &in[2], &in[3], &out[0], &out[1], &out[2]};
   favor::DecayMap maps[7];
-  bool tc = favor::decay_tc_takes(all, 7, bf16, d);
+  bool tc = favor::decay_tc_takes(all, 7, bf16, d) && by16(S0) && by16(dST);
   for (int i = 0; i < 7 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
   if (tc) favor::decay_tc_plan(&s, 3);
   else favor::decay_simt_plan(&s);
@@ -867,8 +864,8 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     p.s_w = scale;
     p.s_r = i == 0 ? scale : 1.f;
     p.s_u = i == 0 ? 1.f : scale;
-    passes[i].edge = i == 0 ? S0 : dST;
-    passes[i].gains = i == 0 ? ws : ws_r;
+    p.start = i == 0 ? S0 : dST;
+    passes[i].step = (int64_t)d * d;
     passes[i].a = &maps[abc[i][0]];
     passes[i].b = &maps[abc[i][1]];
     passes[i].c = &maps[abc[i][2]];
@@ -882,7 +879,7 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     }
     for (int i = 0; i < 3 && err == cudaSuccess; ++i) {
       favor::DecayPass& p = passes[i].p;
-      p.start = s.segs > 1 ? passes[i].gains : passes[i].edge;
+      if (s.segs > 1) p.start = i == 0 ? ws : ws_r;
       p.last = i == 2 && s.segs == 1 ? dS0 : nullptr;
       err = favor::decay_simt_pass(p, s, bf16, piece, strm);
     }
@@ -892,13 +889,12 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     const favor::DecayTcGain tc_gains[2] = {{gains[0], &maps[1], &maps[2]}, {gains[1], &maps[0], &maps[3]}};
     const int from = s.segs > 1 ? 0 : 1;                 // one segment: only what dS0 is made of
     err = favor::decay_tc_gains(tc_gains + from, 2 - from, s, strm);
-    if (s.segs > kDecayInPass || (dS0 != nullptr && dS0 == dST)) {
-      if (err == cudaSuccess) err = favor::decay_scan_states(scans + from, 2 - from, s, strm);
-      for (int i = from; i < 3; ++i) passes[i].p.start = passes[i].gains;
-    } else {
-      passes[2].p.last = dS0;
-      for (auto& p : passes) p.after_gains = true;
+    if (err == cudaSuccess) err = favor::decay_scan_states(scans + from, 2 - from, s, strm);
+    for (int i = from; i < 3; ++i) {
+      passes[i].p.start = i == 0 ? ws : ws_r;
+      passes[i].step = 2 * (int64_t)d * d;
     }
+    for (auto& p : passes) p.after_scan = true;
   }
   if (err == cudaSuccess) err = favor::decay_tc_passes(passes, 3, s, strm);
   return done(err);
