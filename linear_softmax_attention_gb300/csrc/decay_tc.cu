@@ -47,7 +47,7 @@ template <int D> struct Cfg {
   static constexpr int kImg = kSlots * kTile;
   static constexpr int kImgAtom = 2 * D * 128;
   static constexpr int kBars = kImg + kAtoms * kImgAtom;
-  static constexpr int kPowers = kBars + 144;              // l^15 .. l^0 (walking back: l^0 .. l^15)
+  static constexpr int kPowers = kBars + 176;              // l^15 .. l^0 (walking back: l^0 .. l^15)
   static constexpr int kDiag = kPowers + 64;               // factors of a diagonal group, see below
   static constexpr int kFade = kDiag + 64 * 4;             // l^0 .. l^128
   static constexpr int kSmem = kFade + 129 * 4;
@@ -59,7 +59,7 @@ template <int D> struct Cfg {
   static constexpr int kTilesC = kDepthB * kAtom;
   static constexpr int kSplit = kTilesC + kDepthC * kTile;
   static constexpr int kGainBars = kSplit + 2 * 3 * kAtom;
-  static constexpr int kGainSmem = kGainBars + 136;
+  static constexpr int kGainSmem = kGainBars + 192;
 };
 // an SM's 228 KB, 1 KB of it reserved for each CTA
 static_assert(2 * (Cfg<64>::kSmem + 1024) <= 233472 && Cfg<128>::kSmem <= 232448, "shared memory");
@@ -176,9 +176,13 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
   uint64_t *scores = full + 6, *out_bar = full + 7, *gain_bar = full + 8, *again_bar = full + 9;
   uint64_t *weights_done = full + 10, *faded_done = full + 11, *rows_done = full + 12, *copy_done = full + 13;
   uint64_t* end_bar = full + 14;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + 15);
+  // What the copies' warp waits for, by the chunk's parity: nothing but its own copies keeps the others from running
+  // on, and a phase that is followed by another before it is looked at would never be seen (chunk i + 2 needs copies
+  // that are made after the waits for chunk i, so that no barrier runs two phases ahead).
+  uint64_t *rows_free = full + 15, *gain_free = full + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + 19);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* odd_rows = reinterpret_cast<uint32_t*>(full + 16);          // [4] rows of c with infinities or NaN
+  uint32_t* odd_rows = reinterpret_cast<uint32_t*>(full + 20);          // [4] rows of c with infinities or NaN
   float* powers = reinterpret_cast<float*>(sm + C::kPowers);
   float* diag = reinterpret_cast<float*>(sm + C::kDiag);
   float* fade = reinterpret_cast<float*>(sm + C::kFade);
@@ -204,6 +208,10 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
     for (int i = 0; i < 10; ++i) mbar_init(full + i, 1);
     for (int i = 10; i < 14; ++i) mbar_init(full + i, C::kEpiWarps);
     mbar_init(end_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(rows_free + i, C::kEpiWarps);
+      mbar_init(gain_free + i, 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -264,6 +272,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
           tc_fence_after();
           issue_gain<D>(tmem + C::kState, smem_addr(slot(i, 0)), D == 64 ? 0 : kAtom, smem_addr(slot(i, 2)), true);
           mma_commit(gain_bar);
+          mma_commit(gain_free + (i & 1));
         }
         ok = mbar_wait(rows_done, i & 1, wctx);                  // P and O are read
         if (!ok) break;
@@ -299,14 +308,14 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       if (C::kSlots == 6) load(1, 2);
       bool ok = true;
       for (int i = 0; i < live; ++i) {
-        ok = mbar_wait(rows_done, i & 1, wctx);
+        ok = mbar_wait(rows_free + (i & 1), i >> 1 & 1, wctx);
         if (!ok) break;
 #pragma unroll
         for (int a = 0; a < C::kAtoms; ++a) tma_store_4d(&map_o, a * 64, token0(i), h, b, slot(i, 1) + a * kAtom);
         bulk_commit();
         if (i + 1 == live) break;
         // b and c are read, and the rows leave from a's place
-        ok = mbar_wait(gain_bar, i & 1, wctx);
+        ok = mbar_wait(gain_free + (i & 1), i >> 1 & 1, wctx);
         if (!ok) break;
         if constexpr (C::kSlots == 6) {
           load(i + 2, 0);
@@ -568,7 +577,10 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(rows_done);
+      if (lane == 0) {
+        mbar_arrive(rows_done);
+        mbar_arrive(rows_free + (i & 1));
+      }
       // ---- the next chunk's copy of the state
       if (i + 1 < live) {
         mbar_wait(gain_bar, i & 1, wctx);
@@ -693,8 +705,9 @@ __global__ void __launch_bounds__(kGainThreads, 1)
     return;
   }
   uint64_t *b_full = reinterpret_cast<uint64_t*>(sm + C::kGainBars), *c_full = b_full + 4;
-  uint64_t *split = b_full + 8, *done = b_full + 10, *taken = b_full + 12, *end_bar = b_full + 14;   // [2] but the last
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 15);
+  uint64_t *b_free = b_full + 8, *c_free = b_full + 12;                                              // of the places
+  uint64_t *split = b_full + 16, *done = b_full + 18, *taken = b_full + 20, *end_bar = b_full + 22;  // [2] but the last
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 23);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wctx{abort_flag, s.status};
@@ -708,8 +721,10 @@ __global__ void __launch_bounds__(kGainThreads, 1)
   auto parts = [&](int j) { return sm + C::kSplit + (j & 1) * 3 * kAtom; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 15; ++i)
-      mbar_init(b_full + i, i == 8 || i == 9 ? kSplitWarps : i == 12 || i == 13 ? kTakeWarps : 1);
+    for (int i = 0; i < 23; ++i) {
+      const bool splits = (i >= 8 && i < 12) || i == 16 || i == 17;
+      mbar_init(b_full + i, splits ? kSplitWarps : i == 20 || i == 21 ? kTakeWarps : 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -756,6 +771,7 @@ __global__ void __launch_bounds__(kGainThreads, 1)
           }
         }
         mma_commit(done + (j & 1));
+        mma_commit(c_free + j % C::kDepthC);
       }
       if (!ok) {
         mma_commit(end_bar);
@@ -773,13 +789,14 @@ __global__ void __launch_bounds__(kGainThreads, 1)
         const int live = run.live();
         for (int i = 0; i < live; ++i) {
           const int t0 = (run.c0 + i) * kM;
-          // b's place is free once its rows are split, c's once the products have ended
-          const int xb = j - C::kDepthB, xc = j - C::kDepthC;
-          if (xb >= 0 && !(ok = mbar_wait(split + (xb & 1), xb >> 1 & 1, wctx))) break;
+          // b's place is free once its rows are split, c's once the products have ended (barriers of the places: those
+          // of the chunks' parity could run two phases ahead of this warp)
+          const int nb = j / C::kDepthB, nc = jc / C::kDepthC;
+          if (nb > 0 && !(ok = mbar_wait(b_free + j % C::kDepthB, (nb - 1) & 1, wctx))) break;
           mbar_arrive_expect_tx(b_full + j % C::kDepthB, kAtom);
           tma_load_4d(tile_b(j), &maps.b[run.kind], half * 64, t0, run.h, run.b, b_full + j % C::kDepthB);
           ++j;
-          if (xc >= 0 && !(ok = mbar_wait(done + (xc & 1), xc >> 1 & 1, wctx))) break;
+          if (nc > 0 && !(ok = mbar_wait(c_free + jc % C::kDepthC, (nc - 1) & 1, wctx))) break;
           mbar_arrive_expect_tx(c_full + jc % C::kDepthC, C::kTile);
 #pragma unroll
           for (int a = 0; a < C::kAtoms; ++a)
@@ -819,7 +836,10 @@ __global__ void __launch_bounds__(kGainThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(split + (j & 1));
+        if (lane == 0) {
+          mbar_arrive(split + (j & 1));
+          mbar_arrive(b_free + j % C::kDepthB);
+        }
       }
     }
   } else {

@@ -303,6 +303,28 @@ def test_graphs_streams_and_threads(cuda_lib):
         assert all(pool.map(work, range(2)))
 
 
+@pytest.mark.parametrize("shape", [(8, 8, 4096, 64), (2, 8, 6144, 128), (1, 1, 30000, 64)])
+def test_many_calls_end_in_time(cuda_lib, shape):
+    # one by one on an idle GPU, and one behind the other: no wait runs out, and the results are the first call's
+    B, H, L, d = shape
+    r = torch.Generator("cuda").manual_seed(5)
+    q, k, v, do = (torch.randn(shape, generator=r, device="cuda").to(BF16) for _ in range(4))
+    g = -torch.exp(torch.rand(H, generator=r, device="cuda") * 7 - 7)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        return (*cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, dev_status=status),
+                *cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.1, dev_status=status))
+
+    first = call()
+    for n in range(60):
+        got = call()
+        if n % 2 == 0:
+            torch.cuda.synchronize()
+            assert int(status.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_offsets_beyond_32_bits(cuda_lib, dtype):
     # tokens 2^26 elements apart: the last ones lie behind 2^31 elements
