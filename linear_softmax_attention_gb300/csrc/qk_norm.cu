@@ -6,8 +6,9 @@
 // takes both sums that it needs,
 //   sum x^2  and  sum (z w) x  with  z = R^T dy,
 // together.  A row belongs to 1 to 32 neighbouring lanes, about 16 channels each;
-// a group of lanes walks the heads of its token, so that sines, cosines and
-// weights stay in registers, with several heads' loads in flight.
+// a group of lanes walks the heads of its token, q's and k's, so that sines and
+// cosines are formed once, and each thread copies its pieces of the next rows
+// ahead into its own places in shared memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -17,8 +18,11 @@
 namespace favor {
 namespace {
 
-constexpr int kThreads = 256;
+// Small CTAs spread evenly over the SMs; the backward pass's leave sums behind
+// that are added up after.
+template <bool BWD> constexpr int kThreads = BWD ? 128 : 64;
 constexpr int kSumRows = 32;
+constexpr int kMostParts = 64;       // CTAs that a token's heads are shared out to, at most
 
 // E elements side by side <-> fp32
 template <typename T, int E> struct Vec {
@@ -80,7 +84,6 @@ struct Side {                         // q or k
   Strides xs, dys, os;
   const float* w;
   float* part;                        // backward: the CTAs' sums [CTA][d], or NULL
-  int heads, share, parts;            // heads of a CTA, CTAs of a token's heads
 };
 
 struct Work {
@@ -90,6 +93,7 @@ struct Work {
   int end[FAVOR_ROTARY_MAX_AXES];     // pairs of the axes up to and with each
   FastDiv l;                          // tokens of a row
   int tokens, L, d, P, pos_B;
+  int Hq, heads, share;               // heads of q, of q and k, of a CTA
   int lanes, items;                   // lanes of a row; pieces (pairs of pieces) of it
   bool halves;
   float eps;
@@ -104,7 +108,7 @@ template <typename T, int E, bool PAIRED, int NI> struct Row {
   using Raw = typename V::Raw;
   static constexpr int R = PAIRED ? 2 : 1;
   int c0[NI], c1[NI];                 // first channels of the pieces; -1: none
-  float cs[NI][N], sn[NI][N], w[NI][W];
+  float cs[NI][N], sn[NI][N];
 
   __device__ __forceinline__ void places(const Work& k, int lane) {
     const int turning = PAIRED ? k.P / E : 2 * k.P / E;
@@ -123,15 +127,6 @@ template <typename T, int E, bool PAIRED, int NI> struct Row {
         c1[j] = turns ? item * E + k.P : -1;
       }
     }
-  }
-  __device__ __forceinline__ void weights(const float* p) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const int c = i < E ? c0[j] : c1[j];
-        w[j][i] = c < 0 ? 0.f : p == nullptr ? 1.f : p[c + i % E];
-      }
   }
   // sines and cosines of token t of sequence b; channels without a position do not turn
   __device__ __forceinline__ void angles(const Work& k, int b, int t, int lane) {
@@ -156,20 +151,7 @@ template <typename T, int E, bool PAIRED, int NI> struct Row {
       }
     }
   }
-  __device__ __forceinline__ void load(Raw (&raw)[NI][R], const T* row) const {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      raw[j][0] = c0[j] >= 0 ? *reinterpret_cast<const Raw*>(row + c0[j]) : Raw{};
-      if constexpr (PAIRED) raw[j][1] = c1[j] >= 0 ? *reinterpret_cast<const Raw*>(row + c1[j]) : Raw{};
-    }
-  }
-  __device__ __forceinline__ void unpack(const Raw (&raw)[NI][R], float (&v)[NI][W]) const {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      V::unpack(raw[j][0], v[j]);
-      if constexpr (PAIRED) V::unpack(raw[j][1], v[j] + E);
-    }
-  }
+  // 1 / sqrt(mean x^2 + eps) is left to the caller
   __device__ __forceinline__ void store(T* row, const float (&v)[NI][W]) const {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
@@ -180,18 +162,105 @@ template <typename T, int E, bool PAIRED, int NI> struct Row {
   }
   // the pairs turned by their angles, or back
   template <bool BACK> __device__ __forceinline__ void turn(float (&v)[NI][W]) const {
+    if constexpr (PAIRED && E > 1) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const float2 u = make_float2(v[j][i], v[j][i + 1]), z = make_float2(v[j][E + i], v[j][E + i + 1]);
+          const float2 c = make_float2(cs[j][i], cs[j][i + 1]);
+          const float2 s = BACK ? make_float2(-sn[j][i], -sn[j][i + 1]) : make_float2(sn[j][i], sn[j][i + 1]);
+          const float2 a = fma2(u, c, mul2(make_float2(-z.x, -z.y), s)), b = fma2(u, s, mul2(z, c));
+          v[j][i] = a.x;
+          v[j][i + 1] = a.y;
+          v[j][E + i] = b.x;
+          v[j][E + i + 1] = b.y;
+        }
+    } else {
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float &u = v[j][PAIRED ? i : 2 * i], &z = v[j][PAIRED ? E + i : 2 * i + 1];
+        constexpr int kZ = PAIRED ? E : 1;
+        float &u = v[j][PAIRED ? i : 2 * i], &z = v[j][PAIRED ? i + kZ : 2 * i + kZ];
         const float c = cs[j][i], s = BACK ? -sn[j][i] : sn[j][i];
         const float a = u * c - z * s;
         z = u * s + z * c;
         u = a;
       }
+    }
   }
 };
+
+// The next rows of X tensors on their way: each thread's own places in shared
+// memory, S rows deep (elements of two bytes, which no asynchronous copy takes,
+// are stored there at once).
+template <typename T, int E, bool PAIRED, int NI, int X> struct Ring {
+  using Rw = Row<T, E, PAIRED, NI>;
+  using Raw = typename Rw::Raw;
+  static constexpr int kRow = X * NI * Rw::R * (int)sizeof(Raw);
+  static constexpr int S = kRow <= 16 ? 8 : kRow <= 32 ? 6 : kRow <= 64 ? 3 : 2;
+  static constexpr int kT = kThreads<X == 2>;
+  static constexpr size_t kBytes = (size_t)S * kRow * kT;
+  Raw* mine;
+  int in = 0, out = 0;
+  __device__ __forceinline__ explicit Ring(void* ring) : mine(static_cast<Raw*>(ring) + threadIdx.x) {}
+  __device__ __forceinline__ Raw* place(int stage, int x, int j, int r) const {
+    return mine + (((stage * X + x) * NI + j) * Rw::R + r) * kT;
+  }
+  __device__ __forceinline__ void copy(Raw* to, const T* from, bool here) {
+    if constexpr (sizeof(Raw) == 2) {
+      *to = here ? *reinterpret_cast<const Raw*>(from) : Raw{};
+    } else if constexpr (sizeof(Raw) == 16) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_addr(to)), "l"(from),
+                   "r"(here ? 16 : 0)
+                   : "memory");
+    } else {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(tc::smem_addr(to)), "l"(from),
+                   "n"(sizeof(Raw)), "r"(here ? (int)sizeof(Raw) : 0)
+                   : "memory");
+    }
+  }
+  // starts the copies of a row of tensor x; pieces that the row lacks become 0
+  __device__ __forceinline__ void fetch(const Rw& row, int x, const T* from, bool real) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const bool h0 = real && row.c0[j] >= 0;
+      copy(place(in, x, j, 0), h0 ? from + row.c0[j] : from, h0);
+      if constexpr (PAIRED) {
+        const bool h1 = real && row.c1[j] >= 0;
+        copy(place(in, x, j, 1), h1 ? from + row.c1[j] : from, h1);
+      }
+    }
+  }
+  __device__ __forceinline__ void fetched() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    in = in + 1 == S ? 0 : in + 1;
+  }
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory"); }
+  __device__ __forceinline__ void take(int x, float (&v)[NI][Rw::W]) const {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      Rw::V::unpack(*place(out, x, j, 0), v[j]);
+      if constexpr (PAIRED) Rw::V::unpack(*place(out, x, j, 1), v[j] + E);
+    }
+  }
+  __device__ __forceinline__ void taken() { out = out + 1 == S ? 0 : out + 1; }
+};
+
+// values two by two (W is even)
+template <int NI, int W, typename F> __device__ __forceinline__ void each(F&& f) {
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int e = 0; e < W; e += 2) f(j, e);
+}
+template <int W> __device__ __forceinline__ float2 get(const float (&x)[W], int e) { return make_float2(x[e], x[e + 1]); }
+template <int W> __device__ __forceinline__ void put(float (&x)[W], int e, float2 v) {
+  x[e] = v.x;
+  x[e + 1] = v.y;
+}
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -200,30 +269,80 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 // 1 / sqrt(x); NaN for infinity: a sum of squares that has left fp32 gives no zeros
 __device__ __forceinline__ float inverse_root(float x) { return fmaf(x, 0.f, rsqrtf(x)); }
 
-// heads of a thread whose loads are in flight together
-template <int NI, int R, int E, bool BWD>
-constexpr int kHeads = (E > 2 ? 8 : 4) / (NI * R * (BWD ? 2 : 1)) > 0 ? (E > 2 ? 8 : 4) / (NI * R * (BWD ? 2 : 1)) : 1;
+// A group's rows in their order: the heads [h0, h1) of its tokens, q's first.
+template <typename T> struct Walk {
+  const Work& k;
+  int64_t base, stride, token;        // the CTA's first token, the step, this group's
+  int group, h0, h1, h;
+  bool real;
+  const T *q, *kk, *dq, *dk;          // the token's rows of head 0
+  __device__ __forceinline__ Walk(const Work& w, int g, int groups, int from, int to)
+      : k(w), base((int64_t)blockIdx.x * groups), stride((int64_t)gridDim.x * groups), group(g), h0(from), h1(to), h(from) {
+    place();
+  }
+  __device__ __forceinline__ bool more() const { return base < k.tokens; }
+  __device__ __forceinline__ void place() {
+    token = base + group;
+    real = token < k.tokens;
+    const uint32_t tk = real ? (uint32_t)token : 0u;
+    const int b = (int)k.l.div(tk), t = (int)tk - b * k.L;
+    auto at = [&](const void* p, const Strides& s) { return static_cast<const T*>(p) + b * s.b + t * s.l; };
+    q = at(k.side[0].x, k.side[0].xs);
+    kk = at(k.side[1].x, k.side[1].xs);
+    dq = at(k.side[0].dy, k.side[0].dys);
+    dk = at(k.side[1].dy, k.side[1].dys);
+  }
+  __device__ __forceinline__ const T* x() const {
+    return h < k.Hq ? q + h * k.side[0].xs.h : kk + (h - k.Hq) * k.side[1].xs.h;
+  }
+  __device__ __forceinline__ const T* dy() const {
+    return h < k.Hq ? dq + h * k.side[0].dys.h : dk + (h - k.Hq) * k.side[1].dys.h;
+  }
+  __device__ __forceinline__ void next() {
+    if (++h < h1) return;
+    h = h0;
+    base += stride;
+    place();
+  }
+};
 
 template <typename T, int E, bool PAIRED, int NI, bool BWD>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant__ Work k) {
+__global__ void __launch_bounds__(kThreads<BWD>, NI * (PAIRED ? 2 * E : E) > 16 || E == 1 ? 1 : BWD ? 4 : 12)
+    qk_norm_kernel(const __grid_constant__ Work k) {
   using Rw = Row<T, E, PAIRED, NI>;
-  using Raw = typename Rw::Raw;
-  constexpr int W = Rw::W, HB = kHeads<NI, Rw::R, E, BWD>;
-  const int qparts = k.side[0].parts;
-  const bool keys = (int)blockIdx.y >= qparts;
-  const Side& s = k.side[keys];
-  const int part = blockIdx.y - (keys ? qparts : 0);
-  const int h0 = part * s.share, h1 = h0 + min(s.share, s.heads - h0);
-  const int lane = threadIdx.x & (k.lanes - 1), group = threadIdx.x / k.lanes, groups = kThreads / k.lanes;
+  using Rn = Ring<T, E, PAIRED, NI, BWD ? 2 : 1>;
+  constexpr int W = Rw::W, kT = kThreads<BWD>;
+  extern __shared__ __align__(16) float smem[];
+  float* weights = smem;                                         // [2][d], then the ring
+  const int lane = threadIdx.x & (k.lanes - 1), group = threadIdx.x / k.lanes, groups = kT / k.lanes;
+  const int h0 = blockIdx.y * k.share, h1 = h0 + min(k.share, k.heads - h0);
   const float inv_d = 1.f / k.d;
   Rw row;
   row.places(k, lane);
-  row.weights(s.w);
-  float dw[NI][W];
+  Rn ring(smem + (2 * k.d + 3) / 4 * 4);
+  Walk<T> ahead(k, group, groups, h0, h1);
+  auto fetch = [&] {
+    if (ahead.more()) {
+      ring.fetch(row, 0, ahead.x(), ahead.real);
+      if constexpr (BWD) ring.fetch(row, 1, ahead.dy(), ahead.real);
+      ahead.next();
+    }
+    ring.fetched();
+  };
 #pragma unroll
-  for (int j = 0; j < NI; ++j)
+  for (int i = 0; i < Rn::S - 1; ++i) fetch();
+  for (int c = threadIdx.x; c < 2 * k.d; c += kT) {
+    const float* w = k.side[c >= k.d].w;
+    weights[c] = w == nullptr ? 1.f : w[c >= k.d ? c - k.d : c];
+  }
+  __syncthreads();
+  float dw[BWD ? 2 : 1][NI][W];
+  if constexpr (BWD) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) dw[j][i] = 0.f;
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int e = 0; e < W; ++e) dw[0][j][e] = dw[1][j][e] = 0.f;
+  }
   // a CTA's groups walk together: every lane of a warp takes part in the sums
   for (int64_t base = (int64_t)blockIdx.x * groups; base < k.tokens; base += (int64_t)gridDim.x * groups) {
     const int64_t token = base + group;
@@ -231,77 +350,100 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant
     const uint32_t tk = real ? (uint32_t)token : 0u;
     const int b = (int)k.l.div(tk), t = (int)tk - b * k.L;
     row.angles(k, b, t, lane);
-    const T* x0 = static_cast<const T*>(s.x) + b * s.xs.b + t * s.xs.l;
-    const T* dy0 = BWD ? static_cast<const T*>(s.dy) + b * s.dys.b + t * s.dys.l : nullptr;
-    T* o0 = static_cast<T*>(s.out) + b * s.os.b + t * s.os.l;
-    for (int hb = h0; hb < h1; hb += HB) {
-      Raw rx[HB][NI][Rw::R], ry[BWD ? HB : 1][NI][Rw::R];
-#pragma unroll
-      for (int i = 0; i < HB; ++i) {
-        const int h = min(hb + i, h1 - 1);
-        row.load(rx[i], x0 + h * s.xs.h);
-        if constexpr (BWD) row.load(ry[i], dy0 + h * s.dys.h);
-      }
-#pragma unroll
-      for (int i = 0; i < HB; ++i) {
-        const bool here = real && hb + i < h1;
-        float x[NI][W];
-        row.unpack(rx[i], x);
-        float sq = 0.f;
+    auto heads = [&](const Side& s, const float* w0, int from, int to, float (&sums)[NI][W]) {
+      T* o = static_cast<T*>(s.out) + b * s.os.b + t * s.os.l + from * s.os.h;
+      for (int h = from; h < to; ++h, o += s.os.h) {
+        fetch();
+        ring.wait();
+        float x[NI][W], w[NI][W];
+        ring.take(0, x);
 #pragma unroll
         for (int j = 0; j < NI; ++j)
 #pragma unroll
-          for (int e = 0; e < W; ++e) sq = fmaf(x[j][e], x[j][e], sq);
+          for (int e = 0; e < W; e += E) {
+            const int c = e < E ? row.c0[j] : row.c1[j];
+            const float* at = w0 + max(c, 0);
+            if constexpr (E % 4 == 0) {
+#pragma unroll
+              for (int i = 0; i < E; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(at + i);
+                w[j][e + i] = v.x;
+                w[j][e + i + 1] = v.y;
+                w[j][e + i + 2] = v.z;
+                w[j][e + i + 3] = v.w;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < E; ++i) w[j][e + i] = at[i];
+            }
+          }
+        float2 sq2 = make_float2(0.f, 0.f);
+        each<NI, W>([&](int j, int e) {
+          const float2 v = get(x[j], e);
+          sq2 = fma2(v, v, sq2);
+        });
+        float sq = sq2.x + sq2.y;
         if constexpr (!BWD) {
+          ring.taken();
           const float r = inverse_root(fmaf(lanes_sum(sq, k.lanes), inv_d, k.eps));
-#pragma unroll
-          for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int e = 0; e < W; ++e) x[j][e] *= r * row.w[j][e];
+          each<NI, W>([&](int j, int e) { put(x[j], e, mul2(get(x[j], e), mul2(twice(r), get(w[j], e)))); });
           row.template turn<false>(x);
-          if (here) row.store(o0 + (hb + i) * s.os.h, x);
         } else {
           float z[NI][W];
-          row.unpack(ry[i], z);
+          ring.take(1, z);
+          ring.taken();
           row.template turn<true>(z);
-          float zx = 0.f;
-#pragma unroll
-          for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int e = 0; e < W; ++e) zx = fmaf(z[j][e] * row.w[j][e], x[j][e], zx);
-          sq = lanes_sum(sq, k.lanes);
-          zx = lanes_sum(zx, k.lanes);
+          float2 zx2 = make_float2(0.f, 0.f);
+          each<NI, W>([&](int j, int e) {
+            const float2 zw = mul2(get(z[j], e), get(w[j], e));
+            zx2 = fma2(zw, get(x[j], e), zx2);
+            put(w[j], e, zw);
+          });
+          float zx = zx2.x + zx2.y;
+          for (int m = k.lanes >> 1; m > 0; m >>= 1) {
+            sq += __shfl_xor_sync(0xffffffffu, sq, m);
+            zx += __shfl_xor_sync(0xffffffffu, zx, m);
+          }
           const float r = inverse_root(fmaf(sq, inv_d, k.eps));
-          const float along = r * r * (zx * inv_d);
-#pragma unroll
-          for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-              if (here) dw[j][e] = fmaf(z[j][e], x[j][e] * r, dw[j][e]);
-              x[j][e] = r * (z[j][e] * row.w[j][e] - x[j][e] * along);
-            }
-          if (here) row.store(o0 + (hb + i) * s.os.h, x);
+          const float2 along = twice(-(r * r * (zx * inv_d))), r2 = twice(r);
+          each<NI, W>([&](int j, int e) {
+            const float2 v = get(x[j], e);
+            if (real) put(sums[j], e, fma2(get(z[j], e), mul2(v, r2), get(sums[j], e)));
+            put(x[j], e, mul2(r2, fma2(v, along, get(w[j], e))));
+          });
         }
+        if (real) row.store(o, x);
       }
-    }
+    };
+    heads(k.side[0], weights, h0, min(h1, k.Hq), dw[0]);
+    heads(k.side[1], weights + k.d, max(h0 - k.Hq, 0), h1 - k.Hq, dw[BWD ? 1 : 0]);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");           // nothing is on its way any more
   if constexpr (BWD) {
-    if (s.part == nullptr) return;
-    // the groups' sums side by side, then column by column
-    extern __shared__ float sums[];
+    // the kernel that adds the CTAs' sums may take its place and wait
+    asm volatile("griddepcontrol.launch_dependents;");
+    // the groups' sums side by side in the ring's place, then column by column
+    float* sums = smem;
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
+    for (int side = 0; side < 2; ++side) {
+      float* part = k.side[side].part;
+      if (part == nullptr) continue;
+      __syncthreads();
 #pragma unroll
-      for (int e = 0; e < W; ++e) {
-        const int c = e < E ? row.c0[j] : row.c1[j];
-        if (c >= 0) sums[group * k.d + c + e % E] = dw[j][e];
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int c = e < E ? row.c0[j] : row.c1[j];
+          if (c >= 0) sums[group * k.d + c + e % E] = dw[side][j][e];
+        }
+      __syncthreads();
+      float* out = part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * k.d;
+      for (int c = threadIdx.x; c < k.d; c += kT) {
+        float v = sums[c];
+#pragma unroll 8
+        for (int g = 1; g < groups; ++g) v += sums[g * k.d + c];
+        out[c] = v;
       }
-    __syncthreads();
-    float* out = s.part + ((int64_t)part * gridDim.x + blockIdx.x) * k.d;
-    for (int c = threadIdx.x; c < k.d; c += kThreads) {
-      float v = sums[c];
-      for (int g = 1; g < groups; ++g) v += sums[g * k.d + c];
-      out[c] = v;
     }
   }
 }
@@ -333,8 +475,29 @@ __global__ void __launch_bounds__(32 * kSumRows) qk_norm_sum_kernel(Sums k, int 
 struct Plan {
   int E, NI, lanes, items;
   bool paired;
-  int ctas, share[2], parts[2];
+  int ctas, share, parts;             // CTAs beside one another; heads of one, CTAs of a token's heads
 };
+
+// CTAs of a launch: at most about four waves of those that are resident walk the
+// tokens, and a token's heads go to the number of CTAs that makes the fullest
+// SM's work (a row each, and about two rows' for the angles) the least.
+void share_out(Plan* p, int64_t tokens, int heads, bool backward) {
+  const int64_t sms = sm_count(), groups = (backward ? kThreads<true> : kThreads<false>) / p->lanes;
+  const int64_t units = std::min((tokens + groups - 1) / groups, (backward ? 16 : 48) * sms);
+  const int64_t at_once = backward ? 4 : 6;            // CTAs of an SM that cost each other little
+  int64_t best = 0;
+  for (int parts = 1; parts <= std::min(heads, kMostParts); ++parts) {
+    const int share = (heads + parts - 1) / parts;
+    const int64_t cost = std::max((units * parts + sms - 1) / sms, at_once) * (share + 2);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p->share = share;
+    }
+  }
+  p->share = std::max(p->share, heads / 32768 + 1);
+  p->parts = (heads + p->share - 1) / p->share;
+  p->ctas = (int)units;
+}
 
 Plan make_plan(const QkNormArgs& a, bool bf16, int piece, bool backward) {
   Plan p{};
@@ -354,34 +517,19 @@ Plan make_plan(const QkNormArgs& a, bool bf16, int piece, bool backward) {
   };
   if (lanes() > 32) p.NI *= 2;
   p.lanes = lanes();
-  const int64_t tokens = (int64_t)a.B * a.L, groups = kThreads / p.lanes;
-  const int64_t sms = sm_count(), wide = (tokens + groups - 1) / groups;
-  // backward: CTAs that walk, so that their sums of the weights' gradients stay few
-  p.ctas = (int)(backward ? std::min<int64_t>(wide, 4 * sms) : wide);
-  // enough CTAs for every SM: fewer heads each where tokens are few
-  const int64_t want = std::max<int64_t>(1, 8 * sms / std::max(1, p.ctas));
-  const int heads[2] = {a.Hq, a.Hk};
-  for (int i = 0; i < 2; ++i) {
-    if (heads[i] == 0) continue;
-    const int64_t parts = std::min<int64_t>(std::min(heads[i], 16384), want);
-    p.share[i] = (int)((heads[i] + parts - 1) / parts);
-    p.parts[i] = (heads[i] + p.share[i] - 1) / p.share[i];
-  }
+  share_out(&p, (int64_t)a.B * a.L, a.Hq + a.Hk, backward);
   return p;
 }
 
 template <typename T, int E, bool PAIRED, int NI>
 cudaError_t run(const Work& w, const Plan& p, bool backward, cudaStream_t stream) {
-  const dim3 grid(p.ctas, p.parts[0] + p.parts[1]);
-  if (!backward) {
-    qk_norm_kernel<T, E, PAIRED, NI, false><<<grid, kThreads, 0, stream>>>(w);
-    return cudaGetLastError();
-  }
-  const size_t smem = (size_t)(kThreads / p.lanes) * w.d * sizeof(float);
-  const auto kernel = qk_norm_kernel<T, E, PAIRED, NI, true>;
+  const auto kernel = backward ? qk_norm_kernel<T, E, PAIRED, NI, true> : qk_norm_kernel<T, E, PAIRED, NI, false>;
+  const size_t ring = backward ? Ring<T, E, PAIRED, NI, 2>::kBytes : Ring<T, E, PAIRED, NI, 1>::kBytes;
+  size_t smem = (2 * (size_t)w.d + 3) / 4 * 16 + ring;
+  if (backward) smem = std::max(smem, (size_t)(kThreads<true> / p.lanes) * w.d * sizeof(float));
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, smem, stream>>>(w);
+  kernel<<<dim3(p.ctas, p.parts), backward ? kThreads<true> : kThreads<false>, smem, stream>>>(w);
   return cudaGetLastError();
 }
 
@@ -404,11 +552,10 @@ size_t qk_norm_workspace_bytes(const QkNormArgs& a) {
   // what any kernel of the shape may write, whatever the tensors' alignment and the pairs
   size_t most = 0;
   for (int lanes = 1; lanes <= 32; lanes *= 2) {
-    const int64_t groups = kThreads / lanes, wide = ((int64_t)a.B * a.L + groups - 1) / groups;
-    const int64_t ctas = std::min<int64_t>(wide, 4 * sm_count()), want = std::max<int64_t>(1, 8 * sm_count() / ctas);
-    size_t n = 0;
-    for (const int heads : {a.Hq, a.Hk}) n += (size_t)ctas * std::min<int64_t>(heads, want);
-    most = std::max(most, n);
+    Plan p{};
+    p.lanes = lanes;
+    share_out(&p, (int64_t)a.B * a.L, a.Hq + a.Hk, true);
+    most = std::max(most, (size_t)p.ctas * p.parts * (a.Hk > 0 ? 2 : 1));
   }
   return most * a.d * sizeof(float);
 }
@@ -434,15 +581,12 @@ cudaError_t launch_qk_norm(const QkNormArgs& a, bool bf16, int piece, bool backw
     s.dys = dys[i];
     s.os = os[i];
     s.w = weight[i];
-    s.heads = heads[i];
-    s.share = p.share[i];
-    s.parts = p.parts[i];
     if (backward && dw[i] != nullptr && heads[i] > 0) {
       any = true;
       s.part = at;
       sums.part[i] = at;
       sums.out[i] = dw[i];
-      sums.n[i] = p.ctas * p.parts[i];
+      sums.n[i] = p.ctas * p.parts;
       at += (int64_t)sums.n[i] * a.d;
     }
   }
@@ -456,14 +600,25 @@ cudaError_t launch_qk_norm(const QkNormArgs& a, bool bf16, int piece, bool backw
   w.d = a.d;
   w.P = a.pairs;
   w.pos_B = a.pos_B;
+  w.Hq = a.Hq;
+  w.heads = a.Hq + a.Hk;
+  w.share = p.share;
   w.lanes = p.lanes;
   w.items = p.items;
   w.halves = a.halves;
   w.eps = a.eps;
   cudaError_t e = bf16 ? run_type<__nv_bfloat16>(w, p, backward, stream) : run_type<float>(w, p, backward, stream);
   if (e != cudaSuccess || !any) return e;
-  qk_norm_sum_kernel<<<dim3((a.d + 31) / 32, 2), 32 * kSumRows, 0, stream>>>(sums, a.d);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.d + 31) / 32, 2);
+  cfg.blockDim = dim3(32 * kSumRows);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_norm_sum_kernel, sums, a.d);
 }
 
 }  // namespace favor
