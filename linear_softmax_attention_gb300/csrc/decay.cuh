@@ -61,11 +61,12 @@ __device__ __forceinline__ int decay_length(const DecayShape& s, int b) {
 // l^n of l = 2^g2; l^0 = 1 whatever l is
 __device__ __forceinline__ float decay_power(float g2, int n) { return n == 0 ? 1.f : exp2f(g2 * n); }
 
-// Segments of a sequence, about `ctas` over all of them, of whole chunks
-inline void decay_segments(DecayShape* s, int chunk, int ctas) {
+// Segments of a sequence, about `ctas` over all of them, of whole chunks; one where there are no more than `one` chunks
+inline void decay_segments(DecayShape* s, int chunk, int ctas, int one) {
   const int chunks = (s->L + chunk - 1) / chunk;
   // (no more than 128: a scan takes them one after another)
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min(chunks, 128), ctas / std::max(1, s->BH())));
+  int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min(chunks, 128), ctas / std::max(1, s->BH())));
+  if (chunks <= one) want = 1;
   const int per = (int)((chunks + want - 1) / want);
   s->segs = (chunks + per - 1) / per;
   s->seg_tokens = per * chunk;

@@ -34,6 +34,7 @@ namespace {
 using namespace tc;
 
 constexpr int kM = 128;              // tokens of a chunk
+constexpr int kShort = 4;            // chunks of a sequence that is one segment, and whose gains run beside the passes
 
 template <int D> struct Cfg {
   static constexpr int kParts = D / 32;                    // warps of a quarter of the lanes, 32 columns each
@@ -620,6 +621,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     decay_tc_pass_kernel(const __grid_constant__ Passes ps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int k = blockIdx.y;
+  // what runs beside the passes may start (one segment: the gains; others wait for the passes' end)
+  asm volatile("griddepcontrol.launch_dependents;");
   if (smem_addr(smem) % 1024 != 0) {                             // tiles are read by 1024-byte swizzle blocks
     if (threadIdx.x == 0) report_status(ps.p[k].s.status, FAVOR_ERR_CUDA);
     return;
@@ -640,10 +643,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 // ---------------------------------------------------------------------------
 struct GainParams {
   DecayShape s;
-  float* out[2];                      // [B H][segs][2][d][d]
+  float* out[2];                      // [B H][segs][2][d][d]; `ends`: [B H][d][d]
+  const float* first[2];
+  bool ends;                          // one segment: what is left is the state behind it, from `first` (NULL: zeros)
   float s_u[2];
   bool rev[2];
-  int chunks, per;                    // of a sequence, of a segment
+  int chunks, per, unit;              // of a sequence, of a segment, of what a share is made of
   long long total;                    // entries of the list: [kind][head][chunk]
 };
 struct GainMaps {
@@ -713,7 +718,8 @@ __global__ void __launch_bounds__(kGainThreads, 1)
   const WaitCtx wctx{abort_flag, s.status};
   const int half = D == 64 ? 0 : blockIdx.x & 1, share = D == 64 ? blockIdx.x : blockIdx.x >> 1;
   const int shares = D == 64 ? gridDim.x : gridDim.x >> 1;
-  const long long x0 = p.total * share / shares, x1 = p.total * (share + 1) / shares;
+  const long long units = p.total / p.unit;
+  const long long x0 = units * share / shares * p.unit, x1 = units * (share + 1) / shares * p.unit;
   // lane = c's column; columns: b's 64 columns' three parts, twice
   constexpr uint32_t kCols = 512, kAcc = 192, kAccStep = 256;
   auto tile_b = [&](int j) { return sm + j % C::kDepthB * kAtom; };
@@ -873,8 +879,24 @@ __global__ void __launch_bounds__(kGainThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(taken + (j & 1));
       }
-      if (y < d) {
-        const int64_t dd = (int64_t)d * d;
+      const int64_t dd = (int64_t)d * d;
+      if (p.ends) {
+        // the pass beside may start from the state that this one takes the place of
+        griddep_wait();
+        const float all = decay_power(s.g[run.h] * kLog2E, min(run.stop(), run.len) - run.first());
+        const int64_t to = run.bh * dd + (int64_t)(half * 64 + col) * d + y;
+        const float* from = p.first[run.kind];
+        const int left = y < d ? d - half * 64 - col : 0;
+#pragma unroll
+        for (int n = 0; n < N; n += 16) {                        // (`from` may be what is written: loads together first)
+          float m[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) m[e] = from != nullptr && n + e < left ? from[to + (n + e) * d] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (n + e < left) p.out[run.kind][to + (n + e) * d] = live > 0 ? fmaf(all, m[e], sum[n + e]) : m[e];
+        }
+      } else if (y < d) {
         const bool front = run.c0 == run.seg * p.per, whole = front && run.c1 == min((run.seg + 1) * p.per, p.chunks);
         float* out = p.out[run.kind] + (((int64_t)run.bh * s.segs + run.seg) * 2 + (front ? 0 : 1)) * dd +
                      (int64_t)(half * 64 + col) * d + y;
@@ -955,15 +977,27 @@ cudaError_t run_gains(const DecayTcGain* gains, int n, const DecayShape& s, cuda
     p.out[i] = gains[i].p.out;
     p.s_u[i] = gains[i].p.s_u;
     p.rev[i] = gains[i].p.rev;
+    p.first[i] = gains[i].first;
   }
+  p.ends = gains[0].ends;
   p.chunks = (s.L + kM - 1) / kM;
   p.per = s.seg_tokens / kM;
   p.total = (long long)n * s.BH() * p.chunks;
+  p.unit = p.ends ? p.chunks : 1;
   // shares that are no shorter than a segment
   constexpr int kHalves = D / 64;
   const int shares = (int)std::max<long long>(1, std::min<long long>(sm_count() / kHalves, p.total / p.per));
-  kernel<<<shares * kHalves, kGainThreads, Cfg<D>::kGainSmem, stream>>>(maps, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(shares * kHalves));
+  cfg.blockDim = dim3(kGainThreads);
+  cfg.dynamicSmemBytes = Cfg<D>::kGainSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.ends ? 1 : 0;                                 // beside the passes
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
 }  // namespace
@@ -980,7 +1014,9 @@ bool decay_tc_takes(const View* const* views, int n, bool bf16, int d) {
   return true;
 }
 
-void decay_tc_plan(DecayShape* s, int passes) { decay_segments(s, kM, (s->d <= 64 ? 2 : 1) * sm_count() / passes); }
+void decay_tc_plan(DecayShape* s, int passes) {
+  decay_segments(s, kM, (s->d <= 64 ? 2 : 1) * sm_count() / passes, kShort);
+}
 
 // [B, H, L, d] as a map {d, L, H, B}; box {64, 128, 1, 1}; 128-byte swizzle; what lies outside reads as 0
 bool decay_tc_map(DecayMap* out, const View& v) {
@@ -997,6 +1033,8 @@ bool decay_tc_map(DecayMap* out, const View& v) {
   memcpy(out->bytes, &map, sizeof(map));
   return true;
 }
+
+bool decay_tc_ends_beside(const DecayShape& s) { return s.L <= kShort * kM; }
 
 cudaError_t decay_tc_passes(const DecayTcPass* passes, int n, const DecayShape& s, cudaStream_t stream) {
   return s.d <= 64 ? run_passes<64>(passes, n, s, stream) : run_passes<128>(passes, n, s, stream);

@@ -21,8 +21,15 @@ struct DecayTcPass {
   bool after_scan;           // the launch before in the stream is decay_scan_states'
   const DecayMap *a, *b, *c, *o;
 };
+// short sequences of one segment: no states are kept, and the gains run beside the passes
+bool decay_tc_ends_beside(const DecayShape& s);
+// ends: such sequences; p.out [B H][d][d] becomes the state behind it, from `first`
+// (NULL: zeros, may be p.out).  The launch before must then be that of the passes,
+// beside which it runs.
 struct DecayTcGain {
   DecayGain p;
+  const float* first;
+  bool ends;
   const DecayMap *b, *c;
 };
 // up to three side by side

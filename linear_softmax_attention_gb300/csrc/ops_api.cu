@@ -455,7 +455,7 @@ size_t decay_workspace(int B, int H, int L, int d, favor_dtype dt, bool backward
   int64_t states = s.segs > 1 ? decay_states(s) : 0;
   if (dt == FAVOR_BF16) {
     favor::decay_tc_plan(&s, backward ? 3 : 1);
-    states = std::max(states, 2 * decay_states(s));          // in two pieces
+    if (!favor::decay_tc_ends_beside(s)) states = std::max(states, 2 * decay_states(s));      // in two pieces
   }
   return (size_t)states * (backward ? 2 : 1) * sizeof(float);
 }
@@ -771,8 +771,9 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   const int64_t dd = (int64_t)d * d;
   favor::DecayTcPass pass{p, dd, false, &maps[0], &maps[1], &maps[2], &maps[3]};
   pass.p.start = S0;
-  if (s.segs > 1 || ST != nullptr) {
-    const favor::DecayTcGain tc_gain{gain, &maps[1], &maps[2]};
+  favor::DecayTcGain tc_gain{gain, nullptr, false, &maps[1], &maps[2]};
+  const bool beside = favor::decay_tc_ends_beside(s);
+  if (s.segs > 1 || (ST != nullptr && !beside)) {
     err = favor::decay_tc_gains(&tc_gain, 1, s, strm);
     if (err == cudaSuccess) err = favor::decay_scan_states(&scan, 1, s, strm);
     pass.p.start = ws;
@@ -780,6 +781,12 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
     pass.after_scan = true;
   }
   if (err == cudaSuccess) err = favor::decay_tc_passes(&pass, 1, s, strm);
+  if (err == cudaSuccess && beside && ST != nullptr) {
+    tc_gain.p.out = ST;
+    tc_gain.first = S0;
+    tc_gain.ends = true;
+    err = favor::decay_tc_gains(&tc_gain, 1, s, strm);
+  }
   return done(err);
 }
 
@@ -885,18 +892,26 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
     }
     return done(err);
   }
-  if (s.segs > 1 || dS0 != nullptr) {
-    const favor::DecayTcGain tc_gains[2] = {{gains[0], &maps[1], &maps[2]}, {gains[1], &maps[0], &maps[3]}};
+  favor::DecayTcGain tc_gains[2] = {{gains[0], nullptr, false, &maps[1], &maps[2]},
+                                    {gains[1], nullptr, false, &maps[0], &maps[3]}};
+  const bool beside = favor::decay_tc_ends_beside(s);
+  if (s.segs > 1 || (dS0 != nullptr && !beside)) {
     const int from = s.segs > 1 ? 0 : 1;                 // one segment: only what dS0 is made of
     err = favor::decay_tc_gains(tc_gains + from, 2 - from, s, strm);
     if (err == cudaSuccess) err = favor::decay_scan_states(scans + from, 2 - from, s, strm);
+    for (auto& p : passes) p.after_scan = true;
     for (int i = from; i < 3; ++i) {
       passes[i].p.start = i == 0 ? ws : ws_r;
       passes[i].step = 2 * (int64_t)d * d;
     }
-    for (auto& p : passes) p.after_scan = true;
   }
   if (err == cudaSuccess) err = favor::decay_tc_passes(passes, 3, s, strm);
+  if (err == cudaSuccess && beside && dS0 != nullptr) {
+    tc_gains[1].p.out = dS0;
+    tc_gains[1].first = dST;
+    tc_gains[1].ends = true;
+    err = favor::decay_tc_gains(tc_gains + 1, 1, s, strm);
+  }
   return done(err);
 }
 

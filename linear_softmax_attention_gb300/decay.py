@@ -12,6 +12,7 @@ device's current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -54,10 +55,14 @@ def decay_attention_workspace_bytes(B: int, H: int, L: int, d: int, dtype, backw
     return load().favor_decay_attention_workspace_bytes(B, H, L, d, _DT[dtype], int(backward))
 
 
+# a shape's size on a device never changes
+_workspace_bytes = functools.lru_cache(maxsize=1024)(decay_attention_workspace_bytes)
+
+
 def _workspace(what, workspace, B, H, L, d, dt, dev, backward):
     """(tensor to keep, pointer, bytes)"""
     if workspace is None:
-        n = decay_attention_workspace_bytes(B, H, L, d, dt, backward, dev)
+        n = _workspace_bytes(B, H, L, d, dt, backward, dev)
         if n == 0:
             return None, None, 0
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
@@ -81,7 +86,7 @@ def fwd_decay_attention(Q, K, V, g, scale=1.0, S0=None, lengths=None, O=None, ST
         O = torch.empty_like(Q, memory_format=_PLAIN)
     state = (B, H, d, d)
     if ST is None:
-        ST = torch.empty(state, dtype=torch.float32, device=Q.device)
+        ST = torch.empty(state, dtype=torch.float32, device=dev)
     workspace, ws, nbytes = _workspace(what, workspace, B, H, L, d, dt, dev, False)
     _call(what, dev,
           (*_views(what, ("Q", "K", "V", "O"), (Q, K, V, O), Q.shape, dt, dev), *_flats(what, ("g",), (g,), (H,), dev),
@@ -109,7 +114,7 @@ def bwd_decay_attention(Q, K, V, g, dO, scale=1.0, S0=None, dST=None, lengths=No
         dV = torch.empty_like(Q, memory_format=_PLAIN)
     state = (B, H, d, d)
     if dS0 is None:
-        dS0 = torch.empty(state, dtype=torch.float32, device=Q.device)
+        dS0 = torch.empty(state, dtype=torch.float32, device=dev)
     workspace, ws, nbytes = _workspace(what, workspace, B, H, L, d, dt, dev, True)
     _call(what, dev,
           (*_views(what, ("Q", "K", "V", "dO", "dQ", "dK", "dV"), (Q, K, V, dO, dQ, dK, dV), Q.shape, dt, dev),
@@ -133,13 +138,13 @@ def decay_attention_step(q, k, v, g, state, scale=1.0, o=None, new_state=None, s
     if B < 1 or H < 1 or d < 1 or B > _INT or H > _INT or d > _INT:
         raise FavorError(f"{what}: q has an empty or oversized axis: {list(shape)}")
     if o is None:
-        o = torch.empty_like(q, memory_format=_PLAIN)
+        o = torch.empty(shape, dtype=dt, device=dev)
     if new_state is None:
         new_state = state
     args = []
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+    for t in (q, k, v, o):
         if t.shape != shape or t.dtype is not dt or t.get_device() != dev:
-            raise FavorError(f"{what}: {name} must be a {dt} tensor {list(shape)} on cuda:{dev}, "
+            raise FavorError(f"{what}: {'qkvo'[len(args) // 2]} must be a {dt} tensor {list(shape)} on cuda:{dev}, "
                              f"not {t.dtype} {list(t.shape)} on {t.device}")
         args.append(t.data_ptr())
         if t.is_contiguous():
@@ -147,7 +152,7 @@ def decay_attention_step(q, k, v, g, state, scale=1.0, o=None, new_state=None, s
             continue
         st = t.stride()
         if st[2] != 1 and d > 1:
-            raise FavorError(f"{what}: {name} must have a unit stride along its last axis")
+            raise FavorError(f"{what}: {'qkvo'[len(args) // 2]} must have a unit stride along its last axis")
         args.append(_S2(st[0], st[1]))
     if state is None or new_state is None:
         raise FavorError(f"{what}: a state is needed (new_decay_state)")
