@@ -2,6 +2,7 @@
 // the shapes that the tensor-core path does not take; the scan over segments
 // and the one-token step.  decay.cuh has the form that every pass follows.
 #include <algorithm>
+#include <type_traits>
 
 #include "decay.cuh"
 
@@ -17,49 +18,77 @@ template <int DP> struct Tile {
   static constexpr int S = DP + 4;   // row: 16-byte pieces of neighbouring rows fall on other banks
 };
 
-// Rows [t0, t0 + n) of one head into fp32 tile rows, zeros behind them and
-// behind the d channels; returns whether this thread met infinities or NaN.
-template <typename T, int DP>
-__device__ __forceinline__ bool load_tile(float* tile, const T* p, int64_t ls, int n, int d, int piece) {
-  constexpr int S = Tile<DP>::S;
-  float odd = 0.f;
-  if (piece == 16) {
-    constexpr int E = 16 / sizeof(T);
-    const int per = DP / E > 0 ? DP / E : 1;
-    for (int e = threadIdx.x; e < kC * per; e += kThreads) {
-      const int r = e / per, c = (e - r * per) * E;
-      float f[E];
+// Rows [0, n) of a head from p on, on their way to a tile: every thread's loads are
+// issued together, then stored; zeros behind the rows and the d channels.
+// In 16-byte pieces (PIECE 16), else one by one.
+template <typename T, int DP, int PIECE> struct Fetch {
+  static constexpr int E = PIECE / (int)sizeof(T), kPer = (DP + E - 1) / E, N = (kC * kPer + kThreads - 1) / kThreads;
+  using Raw = typename std::conditional<PIECE == 16, uint4, T>::type;
+  Raw raw[N];
+  __device__ __forceinline__ void issue(const T* p, int64_t ls, int n, int d) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = 0.f;
-      if (r < n && c < d) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(p + r * ls + c);
-        const unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < E; i += 4)
-        *reinterpret_cast<float4*>(tile + r * S + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-#pragma unroll
-      for (int i = 0; i < E; ++i) odd = fmaf(f[i], 0.f, odd);
-    }
-  } else {
-    for (int e = threadIdx.x; e < kC * DP; e += kThreads) {
-      const int r = e / DP, c = e - r * DP;
-      const float f = r < n && c < d ? to_f32(p[r * ls + c]) : 0.f;
-      tile[r * S + c] = f;
-      odd = fmaf(f, 0.f, odd);
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * kThreads, r = e / kPer, c = (e - r * kPer) * E;
+      raw[i] = r < n && c < d ? *reinterpret_cast<const Raw*>(p + r * ls + c) : Raw{};
     }
   }
-  return odd != 0.f;                 // infinities and NaN make it NaN
+  // returns whether this thread met infinities or NaN
+  __device__ __forceinline__ bool store(float* tile) const {
+    constexpr int S = Tile<DP>::S;
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * kThreads, r = e / kPer, c = (e - r * kPer) * E;
+      if (kC * kPer % kThreads != 0 && r >= kC) break;
+      float f[E];
+      if constexpr (PIECE != 16) {
+        f[0] = to_f32(raw[i]);
+        tile[r * S + c] = f[0];
+      } else {
+        const unsigned w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(w[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = __uint_as_float(w[k] << 16);
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < E; k += 4)
+          *reinterpret_cast<float4*>(tile + r * S + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) odd = fmaf(f[k], 0.f, odd);
+    }
+    return odd != 0.f;               // infinities and NaN make it NaN
+  }
+};
+
+// X tiles side by side, their loads in flight together (one by one where single
+// elements would take too many registers); whether the last one has infinities or NaN
+template <typename T, int DP, int X>
+__device__ __forceinline__ bool load_tiles(float* tiles, const T* const (&p)[X], const int64_t (&ls)[X], int n, int d,
+                                           int piece) {
+  constexpr int kTile = kC * Tile<DP>::S;
+  bool odd = false;
+  if (piece == 16) {
+    Fetch<T, DP, 16> f[X];
+#pragma unroll
+    for (int x = 0; x < X; ++x) f[x].issue(p[x], ls[x], n, d);
+#pragma unroll
+    for (int x = 0; x < X; ++x) odd = f[x].store(tiles + x * kTile);
+  } else {
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      Fetch<T, DP, (int)sizeof(T)> f;
+      f.issue(p[x], ls[x], n, d);
+      odd = f.store(tiles + x * kTile);
+    }
+  }
+  return odd;
 }
 
 // The columns of a thread: V side by side, 16 V apart
@@ -84,10 +113,34 @@ template <int V> __device__ __forceinline__ void load_v(float* f, const float* p
   }
 }
 
-// acc[row][col] += sum_k X[row][k] Y[k][col] over k < K (a multiple of 4), rows
-// 16 apart; with GUARD only the terms of k that row may see
-template <int DP, bool GUARD>
-__device__ __forceinline__ void rows_times(float (&acc)[4][DP / 16], const float* X, int xs, const float* Y, int ys,
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+// columns two by two (one by one where a thread has a single one)
+template <int N> struct Acc {
+  float2 v[N > 1 ? N / 2 : 1];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < (N > 1 ? N / 2 : 1); ++j) v[j] = twice(0.f);
+  }
+  __device__ __forceinline__ void add(float x, const float (&y)[N]) {
+    if constexpr (N == 1) {
+      v[0].x = fmaf(x, y[0], v[0].x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) v[j] = fma2(twice(x), make_float2(y[2 * j], y[2 * j + 1]), v[j]);
+    }
+  }
+  __device__ __forceinline__ float operator[](int j) const { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+  __device__ __forceinline__ void scale(float x) {
+#pragma unroll
+    for (int j = 0; j < (N > 1 ? N / 2 : 1); ++j) v[j] = mul2(v[j], twice(x));
+  }
+};
+
+// acc[row][col] += sum_k X[row][k] Y[k][col], rows 16 apart, over k < K (a
+// multiple of 4; what lies between d and it is 0).  SEES: X are weights [64][64]: of
+// 16 x 16 blocks only those that the rows see; GUARD: of them only the terms.
+template <int DP, bool SEES, bool GUARD>
+__device__ __forceinline__ void rows_times(Acc<DP / 16> (&acc)[4], const float* X, int xs, const float* Y, int ys,
                                            int K, bool rev) {
   using C = Cols<DP>;
   const int r0 = threadIdx.x >> 4;
@@ -96,17 +149,18 @@ __device__ __forceinline__ void rows_times(float (&acc)[4][DP / 16], const float
     float x[4][4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) load_v<4>(x[r], X + (r0 + 16 * r) * xs + k);
+    float y[4][C::N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[C::N];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < C::N; j += C::V) load_v<C::V>(y + j, Y + (k + i) * ys + C::at(j));
+      for (int j = 0; j < C::N; j += C::V) load_v<C::V>(y[i] + j, Y + (k + i) * ys + C::at(j));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < 4; ++r) {
+      if (SEES && (rev ? k / 16 < r : k / 16 > r)) continue;     // the same for all threads
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         const bool sees = !GUARD || (rev ? k + i >= r0 + 16 * r : k + i <= r0 + 16 * r);
-        if (sees)
-#pragma unroll
-          for (int j = 0; j < C::N; ++j) acc[r][j] = fmaf(x[r][i], y[j], acc[r][j]);
+        if (sees) acc[r].add(x[r][i], y[i]);
       }
     }
   }
@@ -114,7 +168,7 @@ __device__ __forceinline__ void rows_times(float (&acc)[4][DP / 16], const float
 
 // m[i][j] += sum_t w[t] B[t][row i] C[t][col j] over t < n
 template <int DP>
-__device__ __forceinline__ void gain_times(float (&m)[DP / 16][DP / 16], const float* B, const float* Cc,
+__device__ __forceinline__ void gain_times(Acc<DP / 16> (&m)[DP / 16], const float* B, const float* Cc,
                                            const float* w, int n) {
   using C = Cols<DP>;
   constexpr int S = Tile<DP>::S;
@@ -128,58 +182,71 @@ __device__ __forceinline__ void gain_times(float (&m)[DP / 16][DP / 16], const f
       load_v<C::V>(c + j, Cc + t * S + C::at(j));
     }
 #pragma unroll
-    for (int i = 0; i < C::N; ++i) {
-      const float x = b[i] * u;
-#pragma unroll
-      for (int j = 0; j < C::N; ++j) m[i][j] = fmaf(x, c[j], m[i][j]);
-    }
+    for (int i = 0; i < C::N; ++i) m[i].add(b[i] * u, c);
   }
 }
 
+struct PassSet {
+  DecayPass pass[3];
+};
+
 // One segment of one head: chunk by chunk, the state M in shared memory.
+// blockIdx.y: which of the passes beside one another.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) decay_pass_kernel(DecayPass p, DecayShape s, int piece) {
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1)
+    decay_pass_kernel(const __grid_constant__ PassSet set, const __grid_constant__ DecayShape s, int piece) {
   using C = Cols<DP>;
   constexpr int S = Tile<DP>::S, MS = DP + 4;
   extern __shared__ __align__(16) float sm[];
   float *A = sm, *Bt = A + kC * S, *Ct = Bt + kC * S, *P = Ct + kC * S, *M = P + kC * kPS;
   __shared__ float fade[kC + 1], u[kC];      // l^0 .. l^64; the gains' weights
+  const DecayPass& p = set.pass[blockIdx.y];
   const int bh = blockIdx.x / s.segs, seg = blockIdx.x - bh * s.segs, b = bh / s.H, h = bh - b * s.H;
   const float g2 = s.g[h] * kLog2E;
   const int len = decay_length(s, b);
   const int first = seg * s.seg_tokens;
   const int end = min(first + s.seg_tokens, s.L), stop = min(end, len);     // rows to write, tokens
-  const int d = s.d;
+  const int d = s.d, K = (d + 3) / 4 * 4;
+  const bool rev = p.rev;
   const T* a0 = static_cast<const T*>(p.a) + b * p.as.b + h * p.as.h;
   const T* b0 = static_cast<const T*>(p.b) + b * p.bs.b + h * p.bs.h;
   const T* c0 = static_cast<const T*>(p.c) + b * p.cs.b + h * p.cs.h;
   T* o0 = static_cast<T*>(p.o) + b * p.os.b + h * p.os.h;
   const float* start = p.start == nullptr ? nullptr : p.start + ((int64_t)bh * s.segs + seg) * d * d;
-  for (int e = threadIdx.x; e < DP * DP; e += kThreads) {
-    const int x = e / DP, y = e - x * DP;
-    // consecutive threads read consecutive elements of either order
-    float v = 0.f;
-    if (start != nullptr && x < d && y < d) v = start[x * d + y];
-    M[p.transposed ? y * MS + x : x * MS + y] = v;
+  constexpr int kAhead = DP * DP / kThreads < 16 ? DP * DP / kThreads : 16;
+#pragma unroll 1
+  for (int e0 = threadIdx.x; e0 < DP * DP; e0 += kAhead * kThreads) {
+    float v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int e = e0 + i * kThreads, x = e / DP, y = e - x * DP;
+      v[i] = start != nullptr && x < d && y < d ? start[x * d + y] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int e = e0 + i * kThreads, x = e / DP, y = e - x * DP;
+      M[p.transposed ? y * MS + x : x * MS + y] = v[i];
+    }
   }
   if (threadIdx.x <= kC) fade[threadIdx.x] = decay_power(g2, threadIdx.x);
   const int chunks = stop > first ? (stop - first + kC - 1) / kC : 0;
   const int r0 = threadIdx.x >> 4;
+#pragma unroll 1
   for (int i = 0; i < chunks; ++i) {
-    const int t0 = first + (p.rev ? chunks - 1 - i : i) * kC;
+    const int t0 = first + (rev ? chunks - 1 - i : i) * kC;
     const int n = min(kC, stop - t0);
     __syncthreads();                          // the tiles of the chunk before are read
-    load_tile<T, DP>(A, a0 + (int64_t)t0 * p.as.l, p.as.l, n, d, piece);
-    load_tile<T, DP>(Bt, b0 + (int64_t)t0 * p.bs.l, p.bs.l, n, d, piece);
-    const bool odd = load_tile<T, DP>(Ct, c0 + (int64_t)t0 * p.cs.l, p.cs.l, n, d, piece);
-    if (threadIdx.x < kC) u[threadIdx.x] = threadIdx.x < n ? p.s_u * fade[p.rev ? threadIdx.x + 1 : n - 1 - threadIdx.x] : 0.f;
+    const T* const from[3] = {a0 + (int64_t)t0 * p.as.l, b0 + (int64_t)t0 * p.bs.l, c0 + (int64_t)t0 * p.cs.l};
+    const int64_t ls[3] = {p.as.l, p.bs.l, p.cs.l};
+    const bool odd = load_tiles<T, DP, 3>(A, from, ls, n, d, piece);
+    if (threadIdx.x < kC) u[threadIdx.x] = threadIdx.x < n ? p.s_u * fade[rev ? threadIdx.x + 1 : n - 1 - threadIdx.x] : 0.f;
     // infinities and NaN of rows that a token may not see would meet its zero weights
     const bool guard = __syncthreads_or(odd);
-    // weights
+    // weights, in the 16 x 16 blocks that rows see
     {
-      float acc[4][4] = {};
+      float2 acc[4][4] = {};
 #pragma unroll 2
-      for (int k = 0; k < DP; k += 4) {
+      for (int k = 0; k < K; k += 4) {
         float x[4][4], y[4][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -189,35 +256,33 @@ __global__ void __launch_bounds__(kThreads) decay_pass_kernel(DecayPass p, Decay
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[r][c] = fmaf(x[r][e], y[c][e], acc[r][c]);
+          for (int c = 0; c < 4; ++c) {
+            if (r != c && rev != (c > r)) continue;
+            acc[r][c] = fma2(make_float2(x[r][0], x[r][1]), make_float2(y[c][0], y[c][1]), acc[r][c]);
+            acc[r][c] = fma2(make_float2(x[r][2], x[r][3]), make_float2(y[c][2], y[c][3]), acc[r][c]);
+          }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int row = r0 + 16 * r, col = (threadIdx.x & 15) + 16 * c;
-          const int apart = p.rev ? col - row : row - col;
-          P[row * kPS + col] = apart >= 0 && col < n ? p.s_w * fade[apart] * acc[r][c] : 0.f;
+          const int apart = rev ? col - row : row - col;
+          P[row * kPS + col] = apart >= 0 && col < n ? p.s_w * fade[apart] * (acc[r][c].x + acc[r][c].y) : 0.f;
         }
     }
     __syncthreads();
-    float acc[4][C::N];
+    Acc<C::N> acc[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int j = 0; j < C::N; ++j) acc[r][j] = 0.f;
-    rows_times<DP, false>(acc, A, S, M, MS, DP, false);
+    for (int r = 0; r < 4; ++r) acc[r].clear();
+    rows_times<DP, false, false>(acc, A, S, M, MS, K, false);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = r0 + 16 * r;
-      const float w = row < n ? p.s_r * fade[p.rev ? n - 1 - row : row + 1] : 0.f;
-#pragma unroll
-      for (int j = 0; j < C::N; ++j) acc[r][j] *= w;
+      acc[r].scale(row < n ? p.s_r * fade[rev ? n - 1 - row : row + 1] : 0.f);
     }
-    if (guard) rows_times<DP, true>(acc, P, kPS, Ct, S, kC, p.rev);
-    else rows_times<DP, false>(acc, P, kPS, Ct, S, kC, p.rev);
+    if (guard) rows_times<DP, true, true>(acc, P, kPS, Ct, S, kC, rev);
+    else rows_times<DP, true, false>(acc, P, kPS, Ct, S, kC, rev);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = r0 + 16 * r;
@@ -229,16 +294,16 @@ __global__ void __launch_bounds__(kThreads) decay_pass_kernel(DecayPass p, Decay
     }
     if (i + 1 == chunks && p.last == nullptr) break;
     __syncthreads();                          // M is read
-    float m[C::N][C::N];
+    Acc<C::N> m[C::N];
     const float all = fade[n];
 #pragma unroll
-    for (int x = 0; x < C::N; ++x)
+    for (int x = 0; x < C::N; ++x) {
+      float v[C::N];
 #pragma unroll
-      for (int y = 0; y < C::N; y += C::V) {
-        load_v<C::V>(&m[x][y], M + C::row(x) * MS + C::at(y));
-#pragma unroll
-        for (int v = 0; v < C::V; ++v) m[x][y + v] *= all;
-      }
+      for (int y = 0; y < C::N; y += C::V) load_v<C::V>(v + y, M + C::row(x) * MS + C::at(y));
+      m[x].clear();
+      m[x].add(all, v);
+    }
     gain_times<DP>(m, Bt, Ct, u, n);
 #pragma unroll
     for (int x = 0; x < C::N; ++x)
@@ -280,16 +345,16 @@ __global__ void __launch_bounds__(kThreads) decay_gain_kernel(Gains gains, Decay
   const int first = seg * s.seg_tokens, stop = min(min(first + s.seg_tokens, s.L), decay_length(s, b));
   const T* b0 = static_cast<const T*>(p.b) + b * p.bs.b + h * p.bs.h;
   const T* c0 = static_cast<const T*>(p.c) + b * p.cs.b + h * p.cs.h;
-  float m[C::N][C::N];
+  Acc<C::N> m[C::N];
 #pragma unroll
-  for (int x = 0; x < C::N; ++x)
-#pragma unroll
-    for (int y = 0; y < C::N; ++y) m[x][y] = 0.f;
+  for (int x = 0; x < C::N; ++x) m[x].clear();
+#pragma unroll 1
   for (int t0 = first; t0 < stop; t0 += kC) {
     const int n = min(kC, stop - t0);
     __syncthreads();
-    load_tile<T, DP>(Bt, b0 + (int64_t)t0 * p.bs.l, p.bs.l, n, d, piece);
-    load_tile<T, DP>(Ct, c0 + (int64_t)t0 * p.cs.l, p.cs.l, n, d, piece);
+    const T* const from[2] = {b0 + (int64_t)t0 * p.bs.l, c0 + (int64_t)t0 * p.cs.l};
+    const int64_t ls[2] = {p.bs.l, p.cs.l};
+    load_tiles<T, DP, 2>(Bt, from, ls, n, d, piece);
     if (threadIdx.x < n) {
       const int t = t0 + threadIdx.x;
       u[threadIdx.x] = p.s_u * decay_power(g2, p.rev ? t - first + 1 : stop - 1 - t);
@@ -427,11 +492,11 @@ template <int DP> constexpr size_t pass_smem() { return (3 * (size_t)kC * (DP + 
 template <int DP> constexpr size_t gain_smem() { return 2 * (size_t)kC * (DP + 4) * 4; }
 
 template <typename T, int DP>
-cudaError_t run_pass(const DecayPass& p, const DecayShape& s, int piece, cudaStream_t stream) {
+cudaError_t run_pass(const PassSet& set, int n, const DecayShape& s, int piece, cudaStream_t stream) {
   const auto kernel = decay_pass_kernel<T, DP>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), pass_smem<DP>());
   if (e != cudaSuccess) return e;
-  kernel<<<s.segs * s.BH(), kThreads, pass_smem<DP>(), stream>>>(p, s, piece);
+  kernel<<<dim3(s.segs * s.BH(), n), kThreads, pass_smem<DP>(), stream>>>(set, s, piece);
   return cudaGetLastError();
 }
 template <typename T, int DP>
@@ -445,7 +510,7 @@ cudaError_t run_gains(const Gains& gains, int n, const DecayShape& s, int piece,
 
 }  // namespace
 
-void decay_simt_plan(DecayShape* s) { decay_segments(s, kC, (s->d <= 64 ? 2 : 1) * sm_count(), 1); }
+void decay_simt_plan(DecayShape* s, int passes) { decay_segments(s, kC, (s->d <= 64 ? 2 : 1) * sm_count() / passes, 1); }
 
 #define FAVOR_DECAY(call, T)              \
   if (s.d <= 16) return call<T, 16>;      \
@@ -453,12 +518,15 @@ void decay_simt_plan(DecayShape* s) { decay_segments(s, kC, (s->d <= 64 ? 2 : 1)
   if (s.d <= 64) return call<T, 64>;      \
   return call<T, 128>
 
-cudaError_t decay_simt_pass(const DecayPass& p, const DecayShape& s, bool bf16, int piece, cudaStream_t stream) {
-  auto pick = [&]() -> cudaError_t (*)(const DecayPass&, const DecayShape&, int, cudaStream_t) {
+cudaError_t decay_simt_passes(const DecayPass* passes, int n, const DecayShape& s, bool bf16, int piece,
+                              cudaStream_t stream) {
+  PassSet set{};
+  for (int i = 0; i < n; ++i) set.pass[i] = passes[i];
+  auto pick = [&]() -> cudaError_t (*)(const PassSet&, int, const DecayShape&, int, cudaStream_t) {
     if (bf16) { FAVOR_DECAY(run_pass, __nv_bfloat16); }
     FAVOR_DECAY(run_pass, float);
   };
-  return pick()(p, s, piece, stream);
+  return pick()(set, n, s, piece, stream);
 }
 
 cudaError_t decay_simt_gains(const DecayGain* gains, int n, const DecayShape& s, bool bf16, int piece,

@@ -73,10 +73,13 @@ inline void decay_segments(DecayShape* s, int chunk, int ctas, int one) {
 }
 
 // CUDA-core path: fp32 arithmetic, any d <= 128 and any strides
-void decay_simt_plan(DecayShape* s);
+// segments for `passes` passes side by side
+void decay_simt_plan(DecayShape* s, int passes);
 cudaError_t decay_simt_gains(const DecayGain* gains, int n, const DecayShape& s, bool bf16, int piece,
                              cudaStream_t stream);
-cudaError_t decay_simt_pass(const DecayPass& p, const DecayShape& s, bool bf16, int piece, cudaStream_t stream);
+// up to three side by side
+cudaError_t decay_simt_passes(const DecayPass* passes, int n, const DecayShape& s, bool bf16, int piece,
+                              cudaStream_t stream);
 // gains -> the states that the segments start from, in place; `first` [B H][d][d] (NULL: zeros) before the first
 // segment (behind the last one where rev), `last` what follows the others (NULL: not wanted).  pieces: a segment's
 // gain is the sum of that many, side by side; its state takes the place of the first

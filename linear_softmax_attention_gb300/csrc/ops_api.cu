@@ -451,7 +451,7 @@ struct Flat {
 size_t decay_workspace(int B, int H, int L, int d, favor_dtype dt, bool backward) {
   // what either path may need, whatever the tensors' alignment
   favor::DecayShape s = decay_shape(nullptr, nullptr, nullptr, B, H, L, d);
-  favor::decay_simt_plan(&s);
+  favor::decay_simt_plan(&s, backward ? 3 : 1);
   int64_t states = s.segs > 1 ? decay_states(s) : 0;
   if (dt == FAVOR_BF16) {
     favor::decay_tc_plan(&s, backward ? 3 : 1);
@@ -753,7 +753,7 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   p.s_w = p.s_r = scale;
   p.s_u = 1.f;
   if (tc) favor::decay_tc_plan(&s, 1);
-  else favor::decay_simt_plan(&s);
+  else favor::decay_simt_plan(&s, 1);
   float* ws = static_cast<float*>(workspace);
   const favor::DecayGain gain{k, v, vk.strides(), vv.strides(), ws, 1.f, false};
   const favor::DecayScan scan{ws, S0, ST, false, tc ? 2 : 1};
@@ -765,7 +765,7 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
     }
     p.start = s.segs > 1 ? ws : S0;
     p.last = s.segs > 1 ? nullptr : ST;
-    if (err == cudaSuccess) err = favor::decay_simt_pass(p, s, bf16, piece, strm);
+    if (err == cudaSuccess) err = favor::decay_simt_passes(&p, 1, s, bf16, piece, strm);
     return done(err);
   }
   const int64_t dd = (int64_t)d * d;
@@ -846,13 +846,12 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
   bool tc = favor::decay_tc_takes(all, 7, bf16, d) && by16(S0) && by16(dST);
   for (int i = 0; i < 7 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
   if (tc) favor::decay_tc_plan(&s, 3);
-  else favor::decay_simt_plan(&s);
+  else favor::decay_simt_plan(&s, 3);
   float *ws = static_cast<float*>(workspace), *ws_r = ws != nullptr ? ws + (tc ? 2 : 1) * decay_states(s) : nullptr;
   const favor::DecayGain gains[2] = {{k, v, in[1].strides(), in[2].strides(), ws, 1.f, false},
                                      {q, d_o, in[0].strides(), in[3].strides(), ws_r, scale, true}};
   const favor::DecayScan scans[2] = {{ws, S0, nullptr, false, tc ? 2 : 1}, {ws_r, dST, dS0, true, tc ? 2 : 1}};
-  // dq, dk, dv: rows a, b, c among q, k, v, do.  dv comes last: where one segment
-  // leaves dS0 itself, that may be the dST that dk reads
+  // dq, dk, dv: rows a, b, c among q, k, v, do
   const int abc[3][3] = {{3, 2, 1}, {2, 3, 0}, {1, 0, 3}};
   favor::DecayTcPass passes[3] = {};
   for (int i = 0; i < 3; ++i) {
@@ -884,12 +883,16 @@ favor_status favor_bwd_decay_attention(const void* q, const int64_t* q_strides, 
       err = favor::decay_simt_gains(gains, 2, s, bf16, piece, strm);
       if (err == cudaSuccess) err = favor::decay_scan_states(scans, 2, s, strm);
     }
-    for (int i = 0; i < 3 && err == cudaSuccess; ++i) {
-      favor::DecayPass& p = passes[i].p;
-      if (s.segs > 1) p.start = i == 0 ? ws : ws_r;
-      p.last = i == 2 && s.segs == 1 ? dS0 : nullptr;
-      err = favor::decay_simt_pass(p, s, bf16, piece, strm);
+    favor::DecayPass simt[3];
+    for (int i = 0; i < 3; ++i) {
+      simt[i] = passes[i].p;
+      if (s.segs > 1) simt[i].start = i == 0 ? ws : ws_r;
+      else if (i == 2) simt[i].last = dS0;
     }
+    // one segment leaves dS0 itself, which may be the dST that dk reads: dv follows
+    const bool apart = s.segs == 1 && dS0 != nullptr && dS0 == dST;
+    if (err == cudaSuccess) err = favor::decay_simt_passes(simt, apart ? 2 : 3, s, bf16, piece, strm);
+    if (err == cudaSuccess && apart) err = favor::decay_simt_passes(simt + 2, 1, s, bf16, piece, strm);
     return done(err);
   }
   favor::DecayTcGain tc_gains[2] = {{gains[0], nullptr, false, &maps[1], &maps[2]},
