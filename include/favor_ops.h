@@ -248,10 +248,12 @@ size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, in
  * Infinities and NaN in a token of k or v reach its own and later rows of its
  * head, in a token of q its own row.  No output may overlap an input (but ST
  * may be S0).
- * With fp32 tensors everything is fp32.  With bf16 tensors ST is accurate to
- * fp32's sums with factors of 2^-17, while o passes, beside its own rounding,
- * through weights and states rounded to bf16 (each term is off by at most 2^-8
- * or so of its size).
+ * States and sums are fp32, and with fp32 tensors everything else is, too.
+ * With bf16 tensors ST is formed from factors with all of
+ * fp32's bits, while a term of o is rounded to bf16 once beside o's own rounding:
+ * its weight where query and key are in one chunk of 128 tokens, its key where
+ * they are not (tensors whose rows are no whole 16-byte pieces, or with a
+ * stride of 0, are taken as fp32 ones).
  * Supported: d <= 128, B H < 2^20, L <= 2^30.
  */
 favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
@@ -291,8 +293,8 @@ size_t favor_decay_attention_workspace_bytes(int B, int H, int L, int d, favor_d
  * q, k, v, o: [B, H, d] with d fastest and, each, an int64_t[2] of the element
  * strides of B and H, or NULL for a contiguous tensor.  state, new_state: fp32
  * [B, H, d, d]; new_state may be state.  o may not overlap anything else.
- * Everything is fp32 but the rounding of o: row t of the forward call, given
- * the state of the tokens before it.
+ * Everything is fp32 but the rounding of o: row t of the forward call, given the
+ * state of the tokens before it, but for that call's roundings.
  * Supported: d <= 128, B H < 2^20.
  */
 favor_status favor_decay_attention_step(const void* q, const int64_t* q_strides, const void* k,
