@@ -510,7 +510,7 @@ cudaError_t run_gains(const Gains& gains, int n, const DecayShape& s, int piece,
 
 }  // namespace
 
-void decay_simt_plan(DecayShape* s, int passes) { decay_segments(s, kC, (s->d <= 64 ? 2 : 1) * sm_count() / passes, 1); }
+void decay_simt_plan(DecayShape* s, int passes) { decay_segments(s, kC, (s->d <= 64 ? 2 : 1) * sm_count(), passes, 1); }
 
 #define FAVOR_DECAY(call, T)              \
   if (s.d <= 16) return call<T, 16>;      \

@@ -61,15 +61,26 @@ __device__ __forceinline__ int decay_length(const DecayShape& s, int b) {
 // l^n of l = 2^g2; l^0 = 1 whatever l is
 __device__ __forceinline__ float decay_power(float g2, int n) { return n == 0 ? 1.f : exp2f(g2 * n); }
 
-// Segments of a sequence, about `ctas` over all of them, of whole chunks; one where there are no more than `one` chunks
-inline void decay_segments(DecayShape* s, int chunk, int ctas, int one) {
+// Segments of whole chunks for a sequence, one where there are no more than `one`
+// chunks: as many as make the waves of CTAs (`slots` of them are resident) the
+// cheapest, counting about two chunks' time for a CTA's start and a little for each
+// segment of the scan, which takes them one after another (128 at most).  Half, three
+// quarters, twice and three times that number of CTAs: 8 x 8 x 4096 x 64 bf16 74, 61,
+// 59 and 63 us against 54; 1 x 16 x 16384 x 128 158, 117, 117 and 130 against 108.
+inline void decay_segments(DecayShape* s, int chunk, int slots, int passes, int one) {
   const int chunks = (s->L + chunk - 1) / chunk;
-  // (no more than 128: a scan takes them one after another)
-  int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min(chunks, 128), ctas / std::max(1, s->BH())));
-  if (chunks <= one) want = 1;
-  const int per = (int)((chunks + want - 1) / want);
-  s->segs = (chunks + per - 1) / per;
-  s->seg_tokens = per * chunk;
+  const int most = chunks <= one ? 1 : std::min(chunks, 128);
+  double best = -1;
+  for (int want = 1; want <= most; ++want) {
+    const int per = (chunks + want - 1) / want, segs = (chunks + per - 1) / per;
+    const int64_t waves = ((int64_t)segs * s->BH() * passes + slots - 1) / slots;
+    const double cost = waves * (per + 2.0) + 0.05 * segs;
+    if (best < 0 || cost < best) {
+      best = cost;
+      s->segs = segs;
+      s->seg_tokens = per * chunk;
+    }
+  }
 }
 
 // CUDA-core path: fp32 arithmetic, any d <= 128 and any strides

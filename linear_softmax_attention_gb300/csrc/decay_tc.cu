@@ -1015,7 +1015,7 @@ bool decay_tc_takes(const View* const* views, int n, bool bf16, int d) {
 }
 
 void decay_tc_plan(DecayShape* s, int passes) {
-  decay_segments(s, kM, (s->d <= 64 ? 2 : 1) * sm_count() / passes, kShort);
+  decay_segments(s, kM, (s->d <= 64 ? 2 : 1) * sm_count(), passes, kShort);
 }
 
 // [B, H, L, d] as a map {d, L, H, B}; box {64, 128, 1, 1}; 128-byte swizzle; what lies outside reads as 0
