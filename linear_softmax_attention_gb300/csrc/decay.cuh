@@ -23,7 +23,6 @@
 namespace favor {
 
 constexpr int kDecayMaxD = 128;
-constexpr float kLog2E = 1.4426950408889634f;
 
 struct DecayPass {
   const void *a, *b, *c;

@@ -2,9 +2,9 @@
 // 128 in whole 16-byte pieces (decay.cuh has the form that every pass follows).
 //
 // The gains of the segments come first, exact to fp32's sums: b's faded rows are
-// kept as three bf16 parts (24 bits), c's rows as they are, and the products of
-// every two chunks of 128 tokens are added up in registers (the tensor cores cut
-// their sums off: 32 chunks in one accumulator were 4e-6 off, two are 1e-7).
+// kept as three bf16 parts (24 bits; two were 2.5e-6 off), c's rows as they are, and
+// each chunk's products are added up in registers (the tensor cores cut their sums
+// off: 32 chunks in one accumulator were 4e-6 off, single ones are 1e-7).
 // From them come the states that segments start from and the states returned.
 //
 // A pass then walks each segment's chunks.  P = A B^T; P is faded and masked on
@@ -21,6 +21,16 @@
 //   b's faded rows          while O = P' C runs,
 //   rows out (O, I -> o)    while the gain runs,
 //   the state's copy, faded while the next chunk's P runs.
+//
+// Bound by the chain of these steps: a chunk of d = 64 takes 5000 to 5600 cycles
+// with two CTAs on an SM (its bytes are 2850 of the SM's share of memory's rate),
+// and by what lies around them: the gains read b's and c's rows a second time
+// (1600 cycles a chunk), three launches, and each CTA's first chunk.  Measured (one GB300): 8
+// x 8 x 4096 x 64 54 us (gains 20, scan 5, pass 29; floor 20), 1 x 16 x 65536 x 128 350
+// us (161), backward of 2 x 8 x 12288 x 64 86 us (26) and of 8 x 8 x 4096 x 64 113 (35).
+// The tensor pipe is 20 to 27 % busy, DRAM 37 to 49 %.  On the CUDA cores the same
+// shapes took 363 us (8 x 8 x 4096 x 64), 916 (1 x 16 x 16384 x 128; here 108) and,
+// of 64 tokens in each of 32 heads, 13.5 (here 8.7).
 #include <string.h>
 
 #include <algorithm>
@@ -34,7 +44,10 @@ namespace {
 using namespace tc;
 
 constexpr int kM = 128;              // tokens of a chunk
-constexpr int kShort = 4;            // chunks of a sequence that is one segment, and whose gains run beside the passes
+// Chunks of a sequence that is one segment and whose gains run beside the passes:
+// 32 heads of 64 tokens 8.7 us (gains, scan and pass behind one another 13.0), of 333
+// 13.5 (15.5), of 512 16.1 (16.8), of 1024 24.4 (20.6); 256 heads of 512 35 (40).
+constexpr int kShort = 4;
 
 template <int D> struct Cfg {
   static constexpr int kParts = D / 32;                    // warps of a quarter of the lanes, 32 columns each
@@ -65,6 +78,8 @@ template <int D> struct Cfg {
 // an SM's 228 KB, 1 KB of it reserved for each CTA
 static_assert(2 * (Cfg<64>::kSmem + 1024) <= 233472 && Cfg<128>::kSmem <= 232448, "shared memory");
 static_assert(Cfg<64>::kGainSmem <= 232448 && Cfg<128>::kGainSmem <= 232448, "shared memory");
+// gains that wait for the passes beside them are never on an SM with one of those, which could want their tensor memory
+static_assert(Cfg<64>::kSmem + Cfg<64>::kGainSmem > 233472 && Cfg<128>::kSmem + Cfg<128>::kGainSmem > 233472, "apart");
 
 // waits for a phase although other waits have run out: copies and products in
 // flight must end before their memory goes
@@ -192,7 +207,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
   const bool rev = p.rev;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.x / s.segs, seg = blockIdx.x - bh * s.segs, b = bh / s.H, h = bh - b * s.H;
-  const float g2 = s.g[h] * kLog2E;
+  const float g2 = s.g[h] * kLog2e;
   const int len = decay_length(s, b), first = seg * s.seg_tokens, end = min(first + s.seg_tokens, s.L);
   const int stop = min(end, len);
   const int live = stop > first ? (stop - first + kM - 1) / kM : 0;     // chunks with tokens
@@ -825,7 +840,7 @@ __global__ void __launch_bounds__(kGainThreads, 1)
     while (run.next()) {
       if (run.h != h) {
         h = run.h;
-        g2 = s.g[h] * kLog2E;
+        g2 = s.g[h] * kLog2e;
       }
       const float s_u = p.s_u[run.kind];
       const bool rev = p.rev[run.kind];
@@ -883,7 +898,7 @@ __global__ void __launch_bounds__(kGainThreads, 1)
       if (p.ends) {
         // the pass beside may start from the state that this one takes the place of
         griddep_wait();
-        const float all = decay_power(s.g[run.h] * kLog2E, min(run.stop(), run.len) - run.first());
+        const float all = decay_power(s.g[run.h] * kLog2e, min(run.stop(), run.len) - run.first());
         const int64_t to = run.bh * dd + (int64_t)(half * 64 + col) * d + y;
         const float* from = p.first[run.kind];
         const int left = y < d ? d - half * 64 - col : 0;

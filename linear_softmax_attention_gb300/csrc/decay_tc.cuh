@@ -5,11 +5,13 @@
 
 namespace favor {
 
-// bf16, whole 16-byte pieces, no broadcast axis
+// bf16, d <= 128, whole 16-byte pieces, no broadcast axis: whatever the sizes (32 heads
+// of 64 tokens of 64 took 8.7 us against 13.5 on the CUDA cores, 64 of 4096 54 against
+// 363, 16 of 16384 of 128 108 against 916)
 bool decay_tc_takes(const View* const* views, int n, bool bf16, int d);
 // segments for `passes` passes side by side
 void decay_tc_plan(DecayShape* s, int passes);
-// a view and whether it is read or written, encoded once per call
+// a view, encoded once per call
 struct DecayMap {
   alignas(64) unsigned char bytes[128];
 };

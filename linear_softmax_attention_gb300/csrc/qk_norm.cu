@@ -9,6 +9,12 @@
 // a group of lanes walks the heads of its token, q's and k's, so that sines and
 // cosines are formed once, and each thread copies its pieces of the next rows
 // ahead into its own places in shared memory.
+//
+// Measured (one GB300; copy rate 6682 GB/s): 65536 tokens x (16 + 16) heads of 128
+// bf16 out of a joint [B, L, 3, H, d] buffer 167 us, 6.4 TB/s; backward of (16 + 4)
+// heads 168 us, 6.0 TB/s; 2 x 12288 x (8 + 8) heads of 64 fp32 38.5 and 62 us, bf16
+// 21.9 and 39 us (floors 30, 45, 15 and 23): there the waves' ends and, backward,
+// the second kernel show.  256 tokens of (8 + 8) heads of 64: 3.6 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -18,8 +24,9 @@
 namespace favor {
 namespace {
 
-// Small CTAs spread evenly over the SMs; the backward pass's leave sums behind
-// that are added up after.
+// Small CTAs spread evenly over the SMs (2 x 12288 x (8 + 8) heads of 64 bf16
+// forward: 21.9 us, 25.1 with 128 threads, 27.5 with 256); the backward pass's leave
+// sums behind that are added up after (39 us, 51 with 256).
 template <bool BWD> constexpr int kThreads = BWD ? 128 : 64;
 constexpr int kSumRows = 32;
 constexpr int kMostParts = 64;       // CTAs that a token's heads are shared out to, at most
@@ -151,7 +158,7 @@ template <typename T, int E, bool PAIRED, int NI> struct Row {
       }
     }
   }
-  // 1 / sqrt(mean x^2 + eps) is left to the caller
+  // rounded once, to the nearest
   __device__ __forceinline__ void store(T* row, const float (&v)[NI][W]) const {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
@@ -178,16 +185,16 @@ template <typename T, int E, bool PAIRED, int NI> struct Row {
         }
     } else {
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
+      for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        constexpr int kZ = PAIRED ? E : 1;
-        float &u = v[j][PAIRED ? i : 2 * i], &z = v[j][PAIRED ? i + kZ : 2 * i + kZ];
-        const float c = cs[j][i], s = BACK ? -sn[j][i] : sn[j][i];
-        const float a = u * c - z * s;
-        z = u * s + z * c;
-        u = a;
-      }
+        for (int i = 0; i < N; ++i) {
+          constexpr int kZ = PAIRED ? E : 1;
+          float &u = v[j][PAIRED ? i : 2 * i], &z = v[j][PAIRED ? i + kZ : 2 * i + kZ];
+          const float c = cs[j][i], s = BACK ? -sn[j][i] : sn[j][i];
+          const float a = u * c - z * s;
+          z = u * s + z * c;
+          u = a;
+        }
     }
   }
 };
@@ -480,7 +487,9 @@ struct Plan {
 
 // CTAs of a launch: at most about four waves of those that are resident walk the
 // tokens, and a token's heads go to the number of CTAs that makes the fullest
-// SM's work (a row each, and about two rows' for the angles) the least.
+// SM's work (a row each, and about two rows' for the angles) the least; up to
+// `at_once` CTAs of an SM cost each other little.  64 x 16 tokens x (8 + 8) heads
+// of 90 bf16: 5.8 us, with CTAs counted as if one followed the other 10.1.
 void share_out(Plan* p, int64_t tokens, int heads, bool backward) {
   const int64_t sms = sm_count(), groups = (backward ? kThreads<true> : kThreads<false>) / p->lanes;
   const int64_t units = std::min((tokens + groups - 1) / groups, (backward ? 16 : 48) * sms);
@@ -499,6 +508,10 @@ void share_out(Plan* p, int64_t tokens, int heads, bool backward) {
   p->ctas = (int)units;
 }
 
+// Pieces of 16 bytes, else of two elements, where the rows and each half of the
+// pairs are made of whole ones, else pair by pair: 16384 x (16 + 16) heads of 128
+// bf16 forward 65, 82 and 165 us for halves, 65, 75 and 173 for adjacent pairs;
+// backward 80, 114 and 256, and 80, 111 and 265.
 Plan make_plan(const QkNormArgs& a, bool bf16, int piece, bool backward) {
   Plan p{};
   const int e = bf16 ? 2 : 4;

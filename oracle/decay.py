@@ -15,8 +15,8 @@ bf16 tensors may be taken through tensor cores: ``half`` = 2^-8 is the most that
 one rounding to bf16 moves a value by.  A score (with its decay) is rounded
 once; of the state, which other tokens of the row meet, the factors of its
 outer products are rounded once and it itself once, so that a term of o is off
-by 2 half of its size.  What is returned in fp32 keeps two bf16 parts of a factor:
-half^2.
+by 2 half of its size.  What is returned in fp32 keeps three bf16 parts of a
+factor: half^3.
 """
 
 from __future__ import annotations
@@ -119,7 +119,7 @@ def _form_bound(a, b, c, g, scale_u, scale_r, first, lengths, half, reverse=Fals
         if reverse:
             err = np.where(live, lam * (err + rate * mag), err)
             mag = np.where(live, lam * mag, mag)
-    return _zero_behind(out, lengths), err + (base + half * half) * mag
+    return _zero_behind(out, lengths), err + (base + half ** 3) * mag
 
 
 def decay_attention_bound(q, k, v, g, scale=1.0, S0=None, lengths=None, half=0.0):

@@ -80,7 +80,8 @@ def test_matches_oracle(cuda_lib, dtype, shape):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape,lengths", [((4, 2, 300, 64), [300, 0, 129, 1]), ((3, 1, 200, 24), [128, 64, 199]),
                                            ((2, 2, 520, 128), [511, 7]), ((2, 1, 130, 64), [0, 0]),
-                                           ((3, 2, 65, 33), [-5, 70, 64])])
+                                           ((3, 2, 65, 33), [-5, 70, 64]), ((2, 1, 2600, 64), [2593, 3]),
+                                           ((3, 1, 1500, 128), [0, 1500, 700])])
 def test_lengths_and_what_lies_behind_them(cuda_lib, dtype, shape, lengths):
     t = inputs(shape, dtype, 11)
     for b, n in enumerate(lengths):
@@ -105,6 +106,7 @@ def test_decays_of_every_size(cuda_lib, dtype, d):
     # none, slow, one half a token, strong, and a memory of nothing
     g = [0.0, -1e-4, -0.6931, -20.0, -INF, -1e30]
     both(cuda_lib, inputs((1, 6, 270, d), dtype, 3, g), 0.1)
+    both(cuda_lib, inputs((1, 6, 1400, d), dtype, 4, g), 0.1)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -218,6 +220,100 @@ def test_infinities_and_nan_reach_no_earlier_row(cuda_lib, dtype, d):
         assert torch.equal(a[0, 2, at + 1:], b[0, 2, at + 1:]) and torch.equal(a[:, [0, 1, 3]], b[:, [0, 1, 3]])
     keep = [i for i in range(300) if i != at]
     assert torch.equal(dq[0, 2, keep], grads[0][0, 2, keep])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(2, 2, 50, 64), (2, 2, 200, 64), (1, 2, 2500, 64), (1, 1, 2100, 128), (2, 2, 300, 128),
+                                   (1, 3, 900, 24)])
+def test_states_in_place(cuda_lib, dtype, shape):
+    t = inputs(shape, dtype, 45)
+    q, k, v, do, g, S0, dST = (x.cuda() for x in t)
+    for lengths in (None, torch.tensor([shape[2] - 30, 0][:shape[0]], dtype=torch.int32, device="cuda")):
+        o, ST = cuda_lib.fwd_decay_attention(q, k, v, g, 0.2, S0, lengths)
+        grads = cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.2, S0, dST, lengths)
+        state, grad = S0.clone(), dST.clone()
+        got = (*cuda_lib.fwd_decay_attention(q, k, v, g, 0.2, state, lengths, ST=state),
+               *cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.2, S0, grad, lengths, dS0=grad))
+        assert got[1] is state and got[5] is grad
+        assert all(torch.equal(a, b) for a, b in zip(got, (o, ST, *grads)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 2, 200, 64), (1, 2, 1500, 64), (1, 1, 700, 128)])
+def test_states_off_16_bytes(cuda_lib, dtype, shape):
+    B, H, L, d = shape
+    t = inputs(shape, dtype, 47)
+    q, k, v, do, g = (x.cuda() for x in t[:5])
+    n = B * H * d * d
+    buf = torch.full((4, n + 4), NAN, device="cuda")
+    S0, dST, ST, dS0 = (buf[i, 1 + i % 3:][:n].view(B, H, d, d) for i in range(4))
+    S0.copy_(t[5])
+    dST.copy_(t[6])
+    args = [to_np(x) for x in (t[0], t[1], t[2], t[4])]
+    D, S, E = (to_np(t[i]) for i in (3, 5, 6))
+    for first, grad in ((S0, dST), (t[5].cuda(), t[6].cuda())):
+        fwd = cuda_lib.fwd_decay_attention(q, k, v, g, 0.2, first, ST=ST)
+        check(cuda_lib, "fwd", fwd, orc.decay_attention(*args, 0.2, S),
+              orc.decay_attention_bound(*args, 0.2, S, None, half(dtype)), ("o", "ST"))
+        bwd = cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.2, first, grad, dS0=dS0)
+        check(cuda_lib, "bwd", bwd, orc.decay_attention_grad(*args, D, 0.2, S, E),
+              orc.decay_attention_grad_bound(*args, D, 0.2, S, E, None, half(dtype)), ("dq", "dk", "dv", "dS0"))
+    assert int(torch.isnan(buf).sum()) == 4 * 4                     # nothing beside them is written
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_states_beyond_32_bits(cuda_lib, dtype):
+    # 131080 heads of 128 x 128: the last ones' states lie behind 2^31 elements
+    B, H, L, d = 16385, 8, 2, 128
+    r = torch.Generator("cuda").manual_seed(9)
+    q, k, v, do = (torch.randn((B, H, L, d), generator=r, device="cuda").to(dtype) for _ in range(4))
+    g = torch.linspace(-0.5, -0.01, H, device="cuda")
+    S0 = torch.empty((B, H, d, d), device="cuda")
+    S0.normal_(generator=r)
+    last = slice(B - 2, B)
+    small = [x[last].clone() for x in (q, k, v, do, S0)]
+    want = cuda_lib.fwd_decay_attention(*small[:3], g, 0.1, small[4])
+    o, ST = cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, S0)
+    assert torch.equal(o[last], want[0]) and torch.equal(ST[last], want[1])
+    step = cuda_lib.decay_attention_step(q[last, :, 0], k[last, :, 0], v[last, :, 0], g, want[1], 0.1)
+    ot, _ = cuda_lib.decay_attention_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g, ST, 0.1)
+    assert torch.equal(ot[last], step[0]) and torch.equal(ST[last], step[1])
+    want = cuda_lib.bwd_decay_attention(*small[:3], g, small[3], 0.1, small[4], small[4])
+    got = cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.1, S0, S0, dS0=ST)
+    assert all(torch.equal(a[last], b) for a, b in zip(got, want))
+
+
+def test_short_sequences_in_graphs_and_on_streams(cuda_lib):
+    # the states that run beside the passes: what follows waits for both
+    t = inputs((4, 8, 333, 64), BF16, 73)
+    q, k, v, do, g, S0, dST = (x.cuda() for x in t)
+    want = (*cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, S0),
+            *cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.1, S0, dST))
+    two = cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, want[1])
+    outs, state = [torch.empty_like(x) for x in want], torch.empty_like(S0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        state.copy_(S0)
+        cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, state, O=outs[0], ST=state)
+        outs[1].copy_(state)
+        o2, _ = cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, state, ST=state)
+        cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.1, S0, dST, dQ=outs[2], dK=outs[3], dV=outs[4], dS0=outs[5])
+    for _ in range(20):
+        for x in outs:
+            x.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*outs, o2, state), (*want, *two)))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for stream in streams:
+        stream.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for stream in streams:
+            got.append((stream, *cuda_lib.fwd_decay_attention(q, k, v, g, 0.1, S0, stream=stream),
+                        *cuda_lib.bwd_decay_attention(q, k, v, g, do, 0.1, S0, dST, stream=stream)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for _, *x in got for a, b in zip(x, want))
 
 
 def test_gradients_against_differences(cuda_lib):
