@@ -2,13 +2,15 @@
 // shapes that the tensor-core path does not take; the scan over segments and the
 // one-token step.  decay.cuh has the form that every pass follows.
 //
-// Bound by shared memory's reads: a thread holds 4 x 4 (4 x 8) of a product, eight
-// 16-byte reads for 64 multiplies and adds, and 67 % of the reads' rate is in use
-// at 40 % of the multiplies'.  Of the causal halves only the 16 x 16 blocks that
-// rows see are formed.  Measured (one GB300): 8 x 8 x 4096 x 64 fp32 344 us, 13
-// TFLOP/s; 1 x 16 x 8192 x 128 450 us; 3 x 5 x 1777 x 40 41 us; backward 2 x 4 x 2048
-// x 64 69 us.  (mma.sync on two tf32 parts of every factor took 299, 469, 37 and 60
-// us, but its sums are cut off: errors of 1.1e-6 of the outputs against 3e-7.)
+// Bound by the latencies of a pass's steps (loads, weights, rows, state, a barrier
+// after each) with two CTAs on an SM: 65 % of shared memory's rate and 40 % of the
+// multiplies' are in use.  Of the causal halves only the 16 x 16 blocks that rows see
+// are formed.  (8 x 4 of a product in a thread, with the terms split among groups of
+// warps, needs a quarter fewer reads, but another barrier: 355 us instead of 337.)
+// Measured (one GB300): 8 x 8 x 4096 x 64 fp32 337 us; 1 x 16 x 8192 x 128 441 us; 3 x 5
+// x 1777 x 40 42 us; backward 2 x 4 x 2048 x 64 68 us.  (mma.sync on two tf32 parts of
+// every factor took 299, 469, 37 and 60 us, but its sums are cut off: errors of
+// 1.1e-6 of the outputs against 3e-7.)
 #include <algorithm>
 #include <type_traits>
 
@@ -156,7 +158,8 @@ __device__ __forceinline__ void rows_times(Acc<DP / 16> (&acc)[4], const float* 
   for (int k = 0; k < K; k += 4) {
     float x[4][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) load_v<4>(x[r], X + (r0 + 16 * r) * xs + k);
+    for (int r = 0; r < 4; ++r)
+      if (!SEES || (rev ? k / 16 >= r : k / 16 <= r)) load_v<4>(x[r], X + (r0 + 16 * r) * xs + k);
     float y[4][C::N];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -339,11 +342,20 @@ struct Gains {
   DecayGain kind[2];
 };
 
-// The gain of one segment, in registers; block (segment, head, kind)
+// The gain of one segment, in registers; block (segment, head, kind).  Shared memory
+// returns 128 bytes a cycle, whatever lanes share: a thread holds 8 x 8 of the product
+// where there are so many, and groups of threads take the chunk's tokens in turn; their
+// sums are added at the end, in order.  3 x 5 x 1777 x 40, under the profiler: 13 us,
+// with 4 x 4 of all tokens 20.
+template <int DP> struct GainTile {
+  static constexpr int N = DP >= 64 ? 8 : DP / 8, V = N < 4 ? N : 4;
+  static constexpr int kSide = DP / N, kGroup = kSide * kSide, kGroups = kThreads / kGroup;
+  static __device__ __forceinline__ int at(int place, int j) { return place * V + (j / V) * kSide * V + j % V; }
+};
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) decay_gain_kernel(Gains gains, DecayShape s, int piece) {
-  using C = Cols<DP>;
-  constexpr int S = Tile<DP>::S;
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) decay_gain_kernel(Gains gains, DecayShape s, int piece) {
+  using G = GainTile<DP>;
+  constexpr int S = Tile<DP>::S, N = G::N;
   extern __shared__ __align__(16) float sm[];
   float *Bt = sm, *Ct = Bt + kC * S;
   __shared__ float u[kC];
@@ -353,9 +365,10 @@ __global__ void __launch_bounds__(kThreads) decay_gain_kernel(Gains gains, Decay
   const int first = seg * s.seg_tokens, stop = min(min(first + s.seg_tokens, s.L), decay_length(s, b));
   const T* b0 = static_cast<const T*>(p.b) + b * p.bs.b + h * p.bs.h;
   const T* c0 = static_cast<const T*>(p.c) + b * p.cs.b + h * p.cs.h;
-  Acc<C::N> m[C::N];
+  const int group = threadIdx.x / G::kGroup, ty = threadIdx.x % G::kGroup / G::kSide, tx = threadIdx.x % G::kSide;
+  Acc<N> m[N];
 #pragma unroll
-  for (int x = 0; x < C::N; ++x) m[x].clear();
+  for (int x = 0; x < N; ++x) m[x].clear();
 #pragma unroll 1
   for (int t0 = first; t0 < stop; t0 += kC) {
     const int n = min(kC, stop - t0);
@@ -368,14 +381,45 @@ __global__ void __launch_bounds__(kThreads) decay_gain_kernel(Gains gains, Decay
       u[threadIdx.x] = p.s_u * decay_power(g2, p.rev ? t - first + 1 : stop - 1 - t);
     }
     __syncthreads();
-    gain_times<DP>(m, Bt, Ct, u, n);
+#pragma unroll 2
+    for (int t = group; t < n; t += G::kGroups) {
+      float bv[N], cv[N];
+      const float w = u[t];
+#pragma unroll
+      for (int j = 0; j < N; j += G::V) {
+        load_v<G::V>(bv + j, Bt + t * S + G::at(ty, j));
+        load_v<G::V>(cv + j, Ct + t * S + G::at(tx, j));
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i].add(bv[i] * w, cv);
+    }
   }
   float* out = p.out + ((int64_t)bh * s.segs + seg) * d * d;
+  // the groups' sums one after another, in the tiles' place
+#pragma unroll 1
+  for (int k = 1; k < G::kGroups; ++k) {
+    __syncthreads();
+    if (group == k)
 #pragma unroll
-  for (int x = 0; x < C::N; ++x)
+      for (int x = 0; x < N; ++x)
 #pragma unroll
-    for (int y = 0; y < C::N; ++y)
-      if (C::row(x) < d && C::at(y) < d) out[C::row(x) * d + C::at(y)] = m[x][y];
+        for (int y = 0; y < N; ++y) sm[(x * N + y) * G::kGroup + threadIdx.x % G::kGroup] = m[x][y];
+    __syncthreads();
+    if (group == 0)
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        float v[N];
+#pragma unroll
+        for (int y = 0; y < N; ++y) v[y] = sm[(x * N + y) * G::kGroup + threadIdx.x];
+        m[x].add(1.f, v);
+      }
+  }
+  if (group == 0)
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+#pragma unroll
+      for (int y = 0; y < N; ++y)
+        if (G::at(ty, x) < d && G::at(tx, y) < d) out[G::at(ty, x) * d + G::at(tx, y)] = m[x][y];
 }
 
 struct Scans {

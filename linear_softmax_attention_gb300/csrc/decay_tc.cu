@@ -22,10 +22,11 @@
 //   rows out (O, I -> o)    while the gain runs,
 //   the state's copy, faded while the next chunk's P runs.
 //
-// Bound by the chain of these steps: a chunk of d = 64 takes 5000 to 5600 cycles
-// with two CTAs on an SM (its bytes are 2850 of the SM's share of memory's rate),
-// and by what lies around them: the gains read b's and c's rows a second time
-// (1600 cycles a chunk), three launches, and each CTA's first chunk.  Measured (one GB300): 8
+// Two CTAs on an SM take 5000 to 5600 cycles for a chunk of d = 64 each, whose bytes
+// are 5700 of the SM's share of memory's rate (b and c may still be in the L2 cache):
+// what is left lies around them.  The gains read b's and c's rows a first time (1600
+// cycles a chunk, 1420 by the bytes), there are three launches, each CTA's first chunk
+// waits for everything, and CTAs do not come out even (256 on 304 places).  Measured (one GB300): 8
 // x 8 x 4096 x 64 54 us (gains 20, scan 5, pass 29; floor 20), 1 x 16 x 65536 x 128 350
 // us (161), backward of 2 x 8 x 12288 x 64 86 us (26) and of 8 x 8 x 4096 x 64 113 (35).
 // The tensor pipe is 20 to 27 % busy, DRAM 37 to 49 %.  On the CUDA cores the same
