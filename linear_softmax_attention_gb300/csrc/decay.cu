@@ -123,6 +123,11 @@ template <int V> __device__ __forceinline__ void load_v(float* f, const float* p
   }
 }
 
+template <int V> __device__ __forceinline__ void store_v(float* p, const float (&f)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else *p = f[0];
+}
+
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 // columns two by two (one by one where a thread has a single one)
 template <int N> struct Acc {
@@ -541,6 +546,126 @@ __global__ void __launch_bounds__(kThreads) decay_step_kernel(DecayStep p) {
   }
 }
 
+// A few tokens of one sequence and head, each state read and written once, as by the
+// step; the tokens meet one another through weights (o's form over one chunk).  A
+// thread keeps its elements of the state, NR rows of V columns, in registers: one read
+// of q and k in shared memory goes to V of them.  Bound by memory for a token or two
+// (1024 heads of 128: 34 us, floor 20), then by the tokens: about 0.5 us each with two
+// CTAs on an SM.
+template <typename T, int V, int NR>
+__global__ void __launch_bounds__(kThreads, V * NR <= 16 ? 4 : 2)
+    decay_few_kernel(const __grid_constant__ DecayPass p, const __grid_constant__ DecayShape s) {
+  constexpr int kRow = kDecayMaxD + 4, kAtOnce = 4, W = NR < 4 ? NR : 4;
+  static_assert(kDecayMaxD % NR == 0, "rows of the last thread");
+  __shared__ __align__(16) float rows[3][kDecayFew][kRow];       // q, k, v; zeros to the threads' last row
+  __shared__ float part[kAtOnce][kThreads * V], w[kDecayFew][kDecayFew], fade[kDecayFew + 1];
+  const int bh = blockIdx.x, b = bh / s.H, h = bh - b * s.H, d = s.d, n = decay_length(s, b);
+  const float g2 = s.g[h] * kLog2e;
+  const int per = d / V, groups = (d + NR - 1) / NR;
+  const int r0 = threadIdx.x / per, c = (threadIdx.x - r0 * per) * V, x0 = r0 * NR;
+  const int here = r0 < groups ? min(NR, d - x0) : 0;            // rows of this thread
+  const int64_t at = (int64_t)bh * d * d + (int64_t)x0 * d + c;
+  float m[NR][V];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) m[j][i] = 0.f;
+    if (p.start != nullptr && j < here) load_v<V>(m[j], p.start + at + j * d);
+  }
+  const T* const from[3] = {static_cast<const T*>(p.a) + b * p.as.b + h * p.as.h,
+                            static_cast<const T*>(p.b) + b * p.bs.b + h * p.bs.h,
+                            static_cast<const T*>(p.c) + b * p.cs.b + h * p.cs.h};
+  const int64_t ls[3] = {p.as.l, p.bs.l, p.cs.l};
+  const int dp = max((d + 3) / 4 * 4, groups * NR);
+#pragma unroll
+  for (int x = 0; x < 3; ++x)
+#pragma unroll 4
+    for (int e = threadIdx.x; e < n * dp; e += kThreads) {
+      const int t = e / dp, y = e - t * dp;
+      rows[x][t][y] = y < d ? to_f32(from[x][t * ls[x] + y]) : 0.f;
+    }
+  if (threadIdx.x <= kDecayFew) fade[threadIdx.x] = decay_power(g2, threadIdx.x);
+  __syncthreads();
+  {
+    static_assert(kDecayFew * kDecayFew == kThreads, "a weight a thread");
+    const int t = threadIdx.x / kDecayFew, j = threadIdx.x % kDecayFew;
+    if (t < n && j <= t) {
+      float sum[4] = {};
+#pragma unroll 4
+      for (int y = 0; y < d; y += 4) {
+        float a[4], k[4];
+        load_v<4>(a, &rows[0][t][y]);
+        load_v<4>(k, &rows[1][j][y]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = fmaf(a[i], k[i], sum[i]);
+      }
+      w[t][j] = fade[t - j] * ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    }
+  }
+  T* out = static_cast<T*>(p.o) + b * p.os.b + h * p.os.h;
+  for (int t0 = 0; t0 < n; t0 += kAtOnce) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (t0 + i >= n || here == 0) break;
+      float o[V] = {};
+#pragma unroll
+      for (int j = 0; j < NR; j += W) {
+        float q[W];
+        load_v<W>(q, &rows[0][t0 + i][x0 + j]);
+#pragma unroll
+        for (int x = 0; x < W; ++x)
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = fmaf(q[x], m[j + x][e], o[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) part[i][r0 * d + c + e] = o[e];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kAtOnce * d; e += kThreads) {
+      const int i = e / d, y = e - i * d, t = t0 + i;
+      if (t >= n) break;
+      float old = 0.f, sum = 0.f;
+#pragma unroll 8
+      for (int g = 0; g < groups; ++g) old += part[i][g * d + y];
+#pragma unroll 4
+      for (int j = 0; j <= t; ++j) sum = fmaf(w[t][j], rows[2][j][y], sum);
+      out[t * p.os.l + y] = from_f32<T>(p.s_w * fmaf(fade[t + 1], old, sum));
+    }
+    __syncthreads();
+  }
+  // rows behind the sequence's end
+  for (int e = threadIdx.x; e < (s.L - n) * d; e += kThreads) {
+    const int t = e / d;
+    out[(n + t) * p.os.l + e - t * d] = from_f32<T>(0.f);
+  }
+  if (p.last == nullptr || here == 0) return;
+  const float all = fade[n];
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[j][e] *= all;
+#pragma unroll 1
+  for (int t = 0; t < n; ++t) {
+    float v[V];
+    load_v<V>(v, &rows[2][t][c]);
+    const float u = fade[n - 1 - t];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] *= u;
+#pragma unroll
+    for (int j = 0; j < NR; j += W) {
+      float k[W];
+      load_v<W>(k, &rows[1][t][x0 + j]);
+#pragma unroll
+      for (int x = 0; x < W; ++x)
+#pragma unroll
+        for (int e = 0; e < V; ++e) m[j + x][e] = fmaf(k[x], v[e], m[j + x][e]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+    if (j < here) store_v<V>(p.last + at + j * d, m[j]);
+}
+
 template <int DP> constexpr size_t pass_smem() { return (3 * (size_t)kC * (DP + 4) + kC * kPS + DP * (DP + 4)) * 4; }
 template <int DP> constexpr size_t gain_smem() { return 2 * (size_t)kC * (DP + 4) * 4; }
 
@@ -613,6 +738,22 @@ cudaError_t decay_scan_states(const DecayScan* scans, int n, const DecayShape& s
   cfg.numAttrs = 1;
   return wide ? cudaLaunchKernelEx(&cfg, decay_scan_kernel<4, 8>, g, s, blocks)
               : cudaLaunchKernelEx(&cfg, decay_scan_kernel<1, 16>, g, s, blocks);
+}
+
+template <typename T>
+cudaError_t run_few(const DecayPass& p, const DecayShape& s, bool vec, cudaStream_t stream) {
+  const int most = kThreads / (vec ? s.d / 4 : s.d), nr = (s.d + most - 1) / most;       // rows of a thread
+  const auto kernel = vec ? nr <= 1   ? decay_few_kernel<T, 4, 1>
+                            : nr <= 4 ? decay_few_kernel<T, 4, 4>
+                            : nr <= 8 ? decay_few_kernel<T, 4, 8>
+                                      : decay_few_kernel<T, 4, 16>
+                          : nr <= 4 ? decay_few_kernel<T, 1, 4> : nr <= 16 ? decay_few_kernel<T, 1, 16> : decay_few_kernel<T, 1, 64>;
+  kernel<<<s.BH(), kThreads, 0, stream>>>(p, s);
+  return cudaGetLastError();
+}
+cudaError_t decay_few(const DecayPass& p, const DecayShape& s, bool bf16, cudaStream_t stream) {
+  const bool vec = s.d % 4 == 0 && (reinterpret_cast<uintptr_t>(p.start) | reinterpret_cast<uintptr_t>(p.last)) % 16 == 0;
+  return bf16 ? run_few<__nv_bfloat16>(p, s, vec, stream) : run_few<float>(p, s, vec, stream);
 }
 
 cudaError_t launch_decay_step(const DecayStep& p, bool bf16, cudaStream_t stream) {

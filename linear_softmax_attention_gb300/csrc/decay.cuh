@@ -102,6 +102,14 @@ struct DecayScan {
 };
 cudaError_t decay_scan_states(const DecayScan* scans, int n, const DecayShape& s, cudaStream_t stream);
 
+// whole sequences of at most kDecayFew tokens, forward, any d <= 128 and any strides: o, and M
+// behind them at p.last (NULL: not wanted; may be p.start).  1, 4 and 16 tokens of 1024 heads
+// of 128 bf16: 34, 45 and 79 us (as a chunk on the tensor cores 158, 159 and 163, on the CUDA
+// cores 165 to 177), of 64: 12, 15 and 30 (46), of two heads of 128: 6.2, 7.7 and 13.8 (13.8),
+// of 64: 4.8, 4.9 and 8.9 (9.0); 17 tokens take the other paths
+constexpr int kDecayFew = 16;
+cudaError_t decay_few(const DecayPass& p, const DecayShape& s, bool bf16, cudaStream_t stream);
+
 struct DecayStep {
   const void *q, *k, *v;
   void* o;

@@ -737,10 +737,6 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   const bool bf16 = dt == FAVOR_BF16;
   const int piece = common_piece({&vq, &vk, &vv});
   favor::DecayShape s = decay_shape(g, lengths, dev_status, B, H, L, d);
-  const View* all[4] = {&vq, &vk, &vv, &vo};
-  favor::DecayMap maps[4];
-  bool tc = favor::decay_tc_takes(all, 4, bf16, d) && by16(S0);
-  for (int i = 0; i < 4 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
   favor::DecayPass p{};
   p.a = q;
   p.b = k;
@@ -752,6 +748,15 @@ favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, 
   p.os = vo.strides();
   p.s_w = p.s_r = scale;
   p.s_u = 1.f;
+  if (L <= favor::kDecayFew) {
+    p.start = S0;
+    p.last = ST;
+    return done(favor::decay_few(p, s, bf16, strm));
+  }
+  const View* all[4] = {&vq, &vk, &vv, &vo};
+  favor::DecayMap maps[4];
+  bool tc = favor::decay_tc_takes(all, 4, bf16, d) && by16(S0);
+  for (int i = 0; i < 4 && tc; ++i) tc = favor::decay_tc_map(&maps[i], *all[i]);
   if (tc) favor::decay_tc_plan(&s, 1);
   else favor::decay_simt_plan(&s, 1);
   float* ws = static_cast<float*>(workspace);

@@ -223,6 +223,58 @@ def test_infinities_and_nan_reach_no_earlier_row(cuda_lib, dtype, d):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [1, 4, 16, 31, 32, 40, 44, 64, 65, 72, 96, 100, 127, 128])
+def test_few_tokens(cuda_lib, dtype, d):
+    # fp32 arithmetic, whatever the tensors' type; neighbours of the states stay as they are
+    for L in (1, 3, 4, 5, 16, 17):
+        B, H = 3, 2
+        t = inputs((B, H, L, d), dtype, 300 + L)
+        n = [L, 0, L // 2]
+        for b in range(B):
+            for x in t[:3]:
+                x[b, :, n[b]:] = NAN
+        args = [to_np(x) for x in (t[0], t[1], t[2], t[4])]
+        want, last = orc.decay_attention(*args, 0.3, to_np(t[5]), n)
+        bo, bs = orc.decay_attention_bound(*args, 0.3, to_np(t[5]), n, half(dtype) if L > 16 else 0.0)
+        lengths = torch.tensor(n, dtype=torch.int32, device="cuda")
+        for layout in LAYOUTS:
+            for off in (0, 1):
+                buf = torch.full((B * H * d * d + 2,), NAN, device="cuda")
+                state = buf[off:off + B * H * d * d].view(B, H, d, d)
+                state.copy_(t[5])
+                o, ST = cuda_lib.fwd_decay_attention(*(view(x, layout) for x in t[:3]), t[4].cuda(), 0.3, state, lengths,
+                                                     O=view(torch.zeros_like(t[0]), layout), ST=state)
+                assert ST is state
+                close(o, want, bo, (L, layout, off, "o"))
+                close(ST, last, bs, (L, layout, off, "ST"))
+                assert torch.equal(ST[1], t[5][1].cuda()) and int(torch.isnan(buf).sum()) == 2
+                assert all((o[b, :, n[b]:] == 0).all() for b in range(B))
+        none = cuda_lib.fwd_decay_attention(*(x.cuda() for x in t[:3]), t[4].cuda(), 0.3, None, lengths)
+        zero = cuda_lib.fwd_decay_attention(*(x.cuda() for x in t[:3]), t[4].cuda(), 0.3, torch.zeros_like(ST), lengths)
+        assert all(torch.equal(a, b) for a, b in zip(none, zero))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [33, 64])
+def test_few_tokens_with_infinities(cuda_lib, dtype, d):
+    t = inputs((1, 3, 12, d), dtype, 91)
+    q, k, v = (x.cuda() for x in t[:3])
+    g, S0 = t[4].cuda(), t[5].cuda()
+    clean, last = cuda_lib.fwd_decay_attention(q, k, v, g, 0.2, S0)
+    for i, value in ((0, NAN), (1, INF), (2, NAN), (2, -INF)):
+        ins = [q.clone(), k.clone(), v.clone()]
+        ins[i][0, 1, 7, d // 2] = value
+        o, ST = cuda_lib.fwd_decay_attention(*ins, g, 0.2, S0)
+        assert torch.equal(o[:, :, :7], clean[:, :, :7]) and torch.equal(o[:, ::2], clean[:, ::2])
+        assert torch.equal(ST[:, ::2], last[:, ::2]) and not torch.isfinite(o[0, 1, 7]).all()
+        if i == 0:
+            assert torch.equal(o[0, 1, 8:], clean[0, 1, 8:]) and torch.equal(ST, last)
+        elif i == 2:                                                   # only its column
+            keep = [j for j in range(d) if j != d // 2]
+            assert torch.equal(o[..., keep], clean[..., keep]) and torch.equal(ST[..., keep], last[..., keep])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape", [(2, 2, 50, 64), (2, 2, 200, 64), (1, 2, 2500, 64), (1, 1, 2100, 128), (2, 2, 300, 128),
                                    (1, 3, 900, 24)])
 def test_states_in_place(cuda_lib, dtype, shape):
@@ -262,9 +314,10 @@ def test_states_off_16_bytes(cuda_lib, dtype, shape):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_states_beyond_32_bits(cuda_lib, dtype):
+@pytest.mark.parametrize("L", [2, 17])
+def test_states_beyond_32_bits(cuda_lib, dtype, L):
     # 131080 heads of 128 x 128: the last ones' states lie behind 2^31 elements
-    B, H, L, d = 16385, 8, 2, 128
+    B, H, d = 16385, 8, 128
     r = torch.Generator("cuda").manual_seed(9)
     q, k, v, do = (torch.randn((B, H, L, d), generator=r, device="cuda").to(dtype) for _ in range(4))
     g = torch.linspace(-0.5, -0.01, H, device="cuda")
