@@ -253,7 +253,7 @@ size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, in
  * fp32's bits, while a term of o is rounded to bf16 once beside o's own rounding:
  * its weight where query and key are in one chunk of 128 tokens, its key where
  * they are not (tensors whose rows are no whole 16-byte pieces, or with a
- * stride of 0, are taken as fp32 ones).
+ * stride of 0, and forward calls of L <= 16 are taken as fp32 ones).
  * Supported: d <= 128, B H < 2^20, L <= 2^30.
  */
 favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,
