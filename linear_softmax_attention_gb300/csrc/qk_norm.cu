@@ -12,8 +12,8 @@
 //
 // Measured (one GB300; copy rate 6682 GB/s): 65536 tokens x (16 + 16) heads of 128
 // bf16 out of a joint [B, L, 3, H, d] buffer 167 us, 6.4 TB/s; backward of (16 + 4)
-// heads 168 us, 6.0 TB/s; 2 x 12288 x (8 + 8) heads of 64 fp32 38.5 and 62 us, bf16
-// 21.9 and 39 us (floors 30, 45, 15 and 23): there the waves' ends and, backward,
+// heads 168 us, 6.0 TB/s; 2 x 12288 x (8 + 8) heads of 64 fp32 35 and 62 us, bf16
+// 21.4 and 39 us (floors 30, 45, 15 and 23): there the waves' ends and, backward,
 // the second kernel show.  256 tokens of (8 + 8) heads of 64: 3.6 us.
 #include <algorithm>
 #include <type_traits>
@@ -486,19 +486,27 @@ struct Plan {
 };
 
 // CTAs of a launch: at most about four waves of those that are resident walk the
-// tokens, and a token's heads go to the number of CTAs that makes the fullest
-// SM's work (a row each, and about two rows' for the angles) the least; up to
-// `at_once` CTAs of an SM cost each other little.  64 x 16 tokens x (8 + 8) heads
-// of 90 bf16: 5.8 us, with CTAs counted as if one followed the other 10.1.
-void share_out(Plan* p, int64_t tokens, int heads, bool backward) {
+// tokens, and a token's heads go to the number of CTAs with the least work for the
+// fullest SM, in rows: a CTA's own and `extra` for its angles (and, backward, the sums it
+// leaves) times the CTAs, of which 12 (4) run at once and fewer than 6 cost as 6, and
+// one for the start and end.  A token's heads in 1, 2, 4 and 8 CTAs forward:
+// 16384 x 32 heads of 128 bf16 54.1, 47.2, 49.3, 59.0 us (taken: 2), 2 x 12288 x 16 of 64
+// fp32 37.8, 35.5, 34.3, 40.3 (2), bf16 22.0, 22.6, 25.3, 33.5 (1), 4 x 2048 x 32 of 96
+// fp32 36.7, 38.6, 35.5, 37.2 (1), 256 x 16 of 64 bf16 9.7, 6.9, 5.5, 5.0 (16: 4.6).
+// Backward: 75, 81, 97, 141 (1); 62, 61, 69, 95 (1); 40, 41, 55, 85 (1); 54, 58, 63, 74
+// (2); 13, 9.7, 8.2, 7.6 (8).
+void share_out(Plan* p, int64_t tokens, int heads, bool bf16, bool backward) {
   const int64_t sms = sm_count(), groups = (backward ? kThreads<true> : kThreads<false>) / p->lanes;
   const int64_t units = std::min((tokens + groups - 1) / groups, (backward ? 16 : 48) * sms);
-  const int64_t at_once = backward ? 4 : 6;            // CTAs of an SM that cost each other little
-  int64_t best = 0;
+  const double extra = backward ? 4 : bf16 ? 2.8 : 1.25;
+  double best = -1;
   for (int parts = 1; parts <= std::min(heads, kMostParts); ++parts) {
     const int share = (heads + parts - 1) / parts;
-    const int64_t cost = std::max((units * parts + sms - 1) / sms, at_once) * (share + 2);
-    if (best == 0 || cost < best) {
+    const int64_t ctas = (units * parts + sms - 1) / sms;        // of the fullest SM
+    const double rounds = backward ? (double)units * parts / sms + 1.5
+                                   : ctas / 12 * 12 + (ctas % 12 > 0 ? std::max<int64_t>(ctas % 12, 6) : 0) + 1;
+    const double cost = rounds * (share + extra);
+    if (best < 0 || cost < best) {
       best = cost;
       p->share = share;
     }
@@ -530,7 +538,7 @@ Plan make_plan(const QkNormArgs& a, bool bf16, int piece, bool backward) {
   };
   if (lanes() > 32) p.NI *= 2;
   p.lanes = lanes();
-  share_out(&p, (int64_t)a.B * a.L, a.Hq + a.Hk, backward);
+  share_out(&p, (int64_t)a.B * a.L, a.Hq + a.Hk, bf16, backward);
   return p;
 }
 
@@ -567,7 +575,7 @@ size_t qk_norm_workspace_bytes(const QkNormArgs& a) {
   for (int lanes = 1; lanes <= 32; lanes *= 2) {
     Plan p{};
     p.lanes = lanes;
-    share_out(&p, (int64_t)a.B * a.L, a.Hq + a.Hk, true);
+    share_out(&p, (int64_t)a.B * a.L, a.Hq + a.Hk, true, true);
     most = std::max(most, (size_t)p.ctas * p.parts * (a.Hk > 0 ? 2 : 1));
   }
   return most * a.d * sizeof(float);
