@@ -76,7 +76,7 @@ def fwd_decay_attention(Q, K, V, g, scale=1.0, S0=None, lengths=None, O=None, ST
     """O_t = scale S_t^T Q_t of S_t = exp(g) S_{t-1} + K_t V_t^T over the tokens
     of Q, K, V [B, H, L, d], from the state S0 (None: zeros).  g: the logarithms
     of the heads' decays, fp32 [H], <= 0.  lengths: int32 [B], tokens of each
-    sequence (None: L); rows behind them are not read, and 0 in O.  Returns
+    sequence (None: L); rows behind them are not used, and 0 in O.  Returns
     (O, ST), ST the state behind each sequence's last token; ST may be S0."""
     if stream is not None:
         return _on(stream, fwd_decay_attention, Q, K, V, g, scale, S0, lengths, O, ST, workspace, dev_status)
