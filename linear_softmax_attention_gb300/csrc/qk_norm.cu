@@ -501,7 +501,7 @@ void share_out(Plan* p, int64_t tokens, int heads, bool bf16, bool backward) {
   const double extra = backward ? 4 : bf16 ? 2.8 : 1.25;
   double best = -1;
   for (int parts = 1; parts <= std::min(heads, kMostParts); ++parts) {
-    const int share = (heads + parts - 1) / parts;
+    const int share = (int)(((int64_t)heads + parts - 1) / parts);
     const int64_t ctas = (units * parts + sms - 1) / sms;        // of the fullest SM
     const double rounds = backward ? (double)units * parts / sms + 1.5
                                    : ctas / 12 * 12 + (ctas % 12 > 0 ? std::max<int64_t>(ctas % 12, 6) : 0) + 1;
@@ -512,7 +512,7 @@ void share_out(Plan* p, int64_t tokens, int heads, bool bf16, bool backward) {
     }
   }
   p->share = std::max(p->share, heads / 32768 + 1);
-  p->parts = (heads + p->share - 1) / p->share;
+  p->parts = (int)(((int64_t)heads + p->share - 1) / p->share);
   p->ctas = (int)units;
 }
 
