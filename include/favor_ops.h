@@ -181,7 +181,8 @@ favor_status favor_bwd_rotary(const void* dq_out, const int64_t* dq_out_strides,
  *   y = R(pos) (x w / sqrt(mean x^2 + eps))
  * with w = q_weight for q and k_weight for k (fp32 [d], NULL for 1) and the
  * rotation R of favor_fwd_rotary, whose arguments (pos, sections, table,
- * pairing) and limits these are.  eps > 0 and finite.  The normed row is kept
+ * pairing) and limits these are.  eps > 0 and finite (an eps, squares and means
+ * below fp32's normal numbers, 2^-126, have fewer bits).  The normed row is kept
  * in fp32 and rounded once, after the rotation.  q_out may be q, k_out may be k.
  * A row whose sum of squares leaves fp32 (values beyond about 2^60) is NaN, as
  * one with infinities or NaN is; rows do not touch one another.

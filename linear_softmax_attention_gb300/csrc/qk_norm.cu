@@ -15,6 +15,8 @@
 // heads 168 us, 6.0 TB/s; 2 x 12288 x (8 + 8) heads of 64 fp32 35 and 62 us, bf16
 // 21.4 and 39 us (floors 30, 45, 15 and 23): there the waves' ends and, backward,
 // the second kernel show.  256 tokens of (8 + 8) heads of 64: 3.6 us.
+#include <float.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -412,7 +414,9 @@ __global__ void __launch_bounds__(kThreads<BWD>, NI * (PAIRED ? 2 * E : E) > 16 
             zx += __shfl_xor_sync(0xffffffffu, zx, m);
           }
           const float r = inverse_root(fmaf(sq, inv_d, k.eps));
-          const float2 along = twice(-(r * r * (zx * inv_d))), r2 = twice(r);
+          // r^2 leaves fp32 where the mean square and eps are below 2^-128; its product with the mean need not
+          const float m = zx * inv_d, rr = r * r;
+          const float2 along = twice(-(rr <= FLT_MAX ? rr * m : r * (r * m))), r2 = twice(r);
           each<NI, W>([&](int j, int e) {
             const float2 v = get(x[j], e);
             if (real) put(sums[j], e, fma2(get(z[j], e), mul2(v, r2), get(sums[j], e)));
