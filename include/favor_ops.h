@@ -231,9 +231,11 @@ size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, in
  * by the layer (favor_fwd_layer_norm).
  *  - g: device fp32 [H], the logarithms of the decays, <= 0 (not checked).  0 is
  *    plain causal linear attention; with minus infinity a token sees itself
- *    alone.  (A positive g gives the formula's values while l^128 and the
- *    states stay finite in fp32.)  The decays are constants of the heads and
- *    have no gradient.
+ *    alone.  (Positive g: tokens, zeros too, are weighted by powers of l that
+ *    reach over a run of tokens, at most the sequence.  The values are the
+ *    formula's while l^L, its products with what the tensors hold and the states
+ *    stay finite in fp32.)  The decays are constants of the heads and have no
+ *    gradient.
  *  - lengths: device int32 [B], the tokens of each sequence, or NULL for L
  *    each; values are clamped to [0, L].  Rows of q, k and v at and behind a
  *    sequence's end are not used, whatever they hold, and its rows of o there
