@@ -72,20 +72,25 @@ def _workspace(what, workspace, B, H, L, d, dt, dev, backward):
 
 
 def fwd_decay_attention(Q, K, V, g, scale=1.0, S0=None, lengths=None, O=None, ST=None, workspace=None,
-                        dev_status=None, stream=None):
+                        dev_status=None, stream=None, last_state=True):
     """O_t = scale S_t^T Q_t of S_t = exp(g) S_{t-1} + K_t V_t^T over the tokens
     of Q, K, V [B, H, L, d], from the state S0 (None: zeros).  g: the logarithms
     of the heads' decays, fp32 [H], <= 0.  lengths: int32 [B], tokens of each
     sequence (None: L); rows behind them are not used, and 0 in O.  Returns
-    (O, ST), ST the state behind each sequence's last token; ST may be S0."""
+    (O, ST), ST the state behind each sequence's last token; ST may be S0.
+    last_state=False leaves it out (None)."""
     if stream is not None:
-        return _on(stream, fwd_decay_attention, Q, K, V, g, scale, S0, lengths, O, ST, workspace, dev_status)
+        return _on(stream, fwd_decay_attention, Q, K, V, g, scale, S0, lengths, O, ST, workspace, dev_status, None,
+                   last_state)
     what = "favor_fwd_decay_attention"
     B, H, L, d, dt, dev = _sizes(what, "Q", Q, True)
     if O is None:
         O = torch.empty_like(Q, memory_format=_PLAIN)
     state = (B, H, d, d)
-    if ST is None:
+    if not last_state:
+        if ST is not None:
+            raise FavorError(f"{what}: ST given with last_state=False")
+    elif ST is None:
         ST = torch.empty(state, dtype=torch.float32, device=dev)
     workspace, ws, nbytes = _workspace(what, workspace, B, H, L, d, dt, dev, False)
     _call(what, dev,
@@ -97,13 +102,14 @@ def fwd_decay_attention(Q, K, V, g, scale=1.0, S0=None, lengths=None, O=None, ST
 
 
 def bwd_decay_attention(Q, K, V, g, dO, scale=1.0, S0=None, dST=None, lengths=None, dQ=None, dK=None, dV=None,
-                        dS0=None, workspace=None, dev_status=None, stream=None):
+                        dS0=None, workspace=None, dev_status=None, stream=None, first_state_grad=True):
     """Gradients (dQ, dK, dV, dS0) of fwd_decay_attention for those of its
     outputs, dO and dST (None: zeros); the other arguments as there.  dS0 may
-    be dST.  The decays are constants and have none."""
+    be dST; first_state_grad=False leaves it out (None).  The decays are
+    constants and have none."""
     if stream is not None:
         return _on(stream, bwd_decay_attention, Q, K, V, g, dO, scale, S0, dST, lengths, dQ, dK, dV, dS0, workspace,
-                   dev_status)
+                   dev_status, None, first_state_grad)
     what = "favor_bwd_decay_attention"
     B, H, L, d, dt, dev = _sizes(what, "Q", Q, True)
     if dQ is None:
@@ -113,7 +119,10 @@ def bwd_decay_attention(Q, K, V, g, dO, scale=1.0, S0=None, dST=None, lengths=No
     if dV is None:
         dV = torch.empty_like(Q, memory_format=_PLAIN)
     state = (B, H, d, d)
-    if dS0 is None:
+    if not first_state_grad:
+        if dS0 is not None:
+            raise FavorError(f"{what}: dS0 given with first_state_grad=False")
+    elif dS0 is None:
         dS0 = torch.empty(state, dtype=torch.float32, device=dev)
     workspace, ws, nbytes = _workspace(what, workspace, B, H, L, d, dt, dev, True)
     _call(what, dev,
