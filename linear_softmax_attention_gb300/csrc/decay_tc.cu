@@ -295,8 +295,9 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
         if (!ok) break;
         tc_fence_after();
       }
-      if (!ok) {
-        // after a wait that ran out: what is in flight ends before its memory goes
+      // after a wait that ran out (the others may then arrive without having waited): what is in flight ends before its
+      // memory goes
+      if (!ok || *abort_flag) {
         mma_commit(end_bar);
         drain(end_bar, 0);
       }
@@ -345,7 +346,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
         load(i + 2, C::kSlots == 6 ? 1 : 0);
       }
       bulk_wait0();
-      if (!ok)
+      if (!ok || *abort_flag)
         for (int x = 0; x < C::kSlots; ++x)
           if (issued >> x & 1) drain(full + x, phases >> x & 1);
     }
@@ -575,7 +576,8 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
         fence_proxy_async_smem();
         tc_fence_before();
         named_bar(5, C::kEpi);
-        if (threadIdx.x == 0 && !*abort_flag) {
+        const bool made = threadIdx.x == 0 && !*abort_flag;
+        if (made) {
           tc_fence_after();
           constexpr uint32_t id = idesc_bf16(kM, D, false, true);
           const uint64_t c0 = sdesc(smem_addr(ct), kAtom, 1024);
@@ -585,7 +587,7 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
           mma_commit(again_bar);
         }
         __syncwarp();
-        mbar_wait(again_bar, again & 1, wctx);
+        if (!mbar_wait(again_bar, again & 1, wctx) && made) drain(again_bar, again & 1);
         ++again;
         __syncwarp();
         tc_fence_after();
@@ -609,7 +611,6 @@ __device__ __forceinline__ void pass_body(const CUtensorMap& map_a, const CUtens
         copy_state(m, fade[tokens(i + 1)]);
       }
     }
-    if (*abort_flag && threadIdx.x == 0 && again > 0) drain(again_bar, (again - 1) & 1);
     // rows of chunks behind the sequence's end
     if (first + live * kM < end) {
       __nv_bfloat16* o = p.o + b * p.os.b + h * p.os.h;
@@ -795,10 +796,9 @@ __global__ void __launch_bounds__(kGainThreads, 1)
         mma_commit(done + (j & 1));
         mma_commit(c_free + j % C::kDepthC);
       }
-      if (!ok) {
-        mma_commit(end_bar);
-        drain(end_bar, 0);
-      }
+      // what is in flight ends before its memory goes, even if the sums' warps have stopped waiting for it
+      mma_commit(end_bar);
+      drain(end_bar, 0);
     }
     __syncwarp();
   } else if (warp == kProducts + 1) {
@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(kGainThreads, 1)
           // b's place is free once its rows are split, c's once the products have ended (barriers of the places: those
           // of the chunks' parity could run two phases ahead of this warp)
           const int nb = j / C::kDepthB, nc = jc / C::kDepthC;
-          if (nb > 0 && !(ok = mbar_wait(b_free + j % C::kDepthB, (nb - 1) & 1, wctx))) break;
+          // (after a wait that ran out the rows' warps free it without having waited for what is on its way there)
+          if (nb > 0 && !(ok = mbar_wait(b_free + j % C::kDepthB, (nb - 1) & 1, wctx) && !*abort_flag)) break;
           mbar_arrive_expect_tx(b_full + j % C::kDepthB, kAtom);
           tma_load_4d(tile_b(j), &maps.b[run.kind], half * 64, t0, run.h, run.b, b_full + j % C::kDepthB);
           ++j;
@@ -826,10 +827,9 @@ __global__ void __launch_bounds__(kGainThreads, 1)
           ++jc;
         }
       }
-      if (!ok) {
-        for (int k = 0; k < C::kDepthB && k < j; ++k) drain(b_full + k, (j - 1 - k) / C::kDepthB & 1);
-        for (int k = 0; k < C::kDepthC && k < jc; ++k) drain(c_full + k, (jc - 1 - k) / C::kDepthC & 1);
-      }
+      // the last copies have landed, whoever still waits for them
+      for (int k = 0; k < C::kDepthB && k < j; ++k) drain(b_full + k, (j - 1 - k) / C::kDepthB & 1);
+      for (int k = 0; k < C::kDepthC && k < jc; ++k) drain(c_full + k, (jc - 1 - k) / C::kDepthC & 1);
     }
     __syncwarp();
   } else if (warp < kSplitWarps) {
