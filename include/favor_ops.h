@@ -249,14 +249,18 @@ size_t favor_bwd_qk_norm_rotary_workspace_bytes(int B, int Hq, int Hk, int L, in
  *  - dev_status: a bounded wait that ran out is reported there
  *    (FAVOR_ERR_TIMEOUT).
  * Infinities and NaN in a token of k or v reach its own and later rows of its
- * head, in a token of q its own row.  No output may overlap an input (but ST
- * may be S0).
+ * head, in a token of q its own row; on the tensor cores (bf16, below) rows and
+ * states behind it may be NaN where the formula has an infinity.  No output may
+ * overlap an input (but ST may be S0).
  * States and sums are fp32, and with fp32 tensors everything else is, too.
  * With bf16 tensors ST is formed from factors with all of
  * fp32's bits, while a term of o is rounded to bf16 once beside o's own rounding:
  * its weight where query and key are in one chunk of 128 tokens, its key where
  * they are not (tensors whose rows are no whole 16-byte pieces, or with a
- * stride of 0, and forward calls of L <= 16 are taken as fp32 ones).
+ * stride of 0, S0 or dST off 16 bytes and forward calls of L <= 16 are taken as fp32
+ * ones, on the CUDA cores: several times slower where sequences are long).  For
+ * outputs off by their own rounding alone the same values are passed as fp32
+ * tensors.
  * Supported: d <= 128, B H < 2^20, L <= 2^30.
  */
 favor_status favor_fwd_decay_attention(const void* q, const int64_t* q_strides, const void* k,

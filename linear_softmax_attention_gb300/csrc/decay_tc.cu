@@ -28,7 +28,7 @@
 // cycles a chunk, 1420 by the bytes), there are three launches, each CTA's first chunk
 // waits for everything, and CTAs do not come out even (256 on 304 places).  Measured (one GB300): 8
 // x 8 x 4096 x 64 54 us (gains 20, scan 5, pass 29; floor 20), 1 x 16 x 65536 x 128 350
-// us (161), backward of 2 x 8 x 12288 x 64 86 us (26) and of 8 x 8 x 4096 x 64 113 (35).
+// us (161), backward of 2 x 8 x 12288 x 64 87 us (26) and of 8 x 8 x 4096 x 64 113 (35).
 // The tensor pipe is 20 to 27 % busy, DRAM 37 to 49 %.  On the CUDA cores the same
 // shapes took 363 us (8 x 8 x 4096 x 64), 916 (1 x 16 x 16384 x 128; here 108) and,
 // of 64 tokens in each of 32 heads, 13.5 (here 8.7).

@@ -498,7 +498,13 @@ struct Plan {
 // fp32 37.8, 35.5, 34.3, 40.3 (2), bf16 22.0, 22.6, 25.3, 33.5 (1), 4 x 2048 x 32 of 96
 // fp32 36.7, 38.6, 35.5, 37.2 (1), 256 x 16 of 64 bf16 9.7, 6.9, 5.5, 5.0 (16: 4.6).
 // Backward: 75, 81, 97, 141 (1); 62, 61, 69, 95 (1); 40, 41, 55, 85 (1); 54, 58, 63, 74
-// (2); 13, 9.7, 8.2, 7.6 (8).
+// (2); 13, 9.7, 8.2, 7.6 (8).  The counts are those of pieces of 16 bytes; the other kernels
+// have fewer CTAs to an SM, and the rule serves them so: pieces of two elements, 2 x 4096 x
+// 16 heads of 90 bf16 forward 18.0, 18.7, 19.5, 25.4 us (1), backward 31.6, 32.1, 38.8, 50.6 (1),
+// 3 x 1111 x 10 of 90 fp32 9.1, 7.9, 7.4, 9.4 (2) and 18.3, 14.8, 18.2, 17.5 (2); rows of 512,
+// 8192 x 16 heads bf16 51.8, 56.8, 70, 102 (1) and 83, 105, 154, 250 (1); single elements, 2 x
+// 4096 x 16 heads of 33 fp32 15.6, 17.5, 17.0, 18.9 (2) and 27.7, 31.2, 37.3, 45.3 (2), bf16 17.1,
+// 18.3, 20.9, 25.1 (2) and 25.1, 28.4, 34.4, 44.8 (2): there it takes one CTA too many.
 void share_out(Plan* p, int64_t tokens, int heads, bool bf16, bool backward) {
   const int64_t sms = sm_count(), groups = (backward ? kThreads<true> : kThreads<false>) / p->lanes;
   const int64_t units = std::min((tokens + groups - 1) / groups, (backward ? 16 : 48) * sms);
